@@ -3,8 +3,9 @@
 A thin Python binding over the C ABI of ``libqlinear.so`` (declared in
 ``include/qlinear.h``): in-situ quantization of bf16 weights into Q8_0, Q4K
 or Q6K blocks (and Q5K, Q3K, Q2K, Q4_0, Q4_1, Q5_0, Q5_1), the fused
-dequantize-matmul that consumes them, the gated feed-forward projection and
-the quantized embedding lookup.  Every
+dequantize-matmul that consumes them, the gated feed-forward projection, the
+mixture-of-experts layer and its router, the quantized embedding lookup and
+the output head's log probabilities.  Every
 step of the computation runs in the library's HIP kernels; this module only
 checks tensors and passes pointers, sizes and the current HIP stream.
 PyTorch provides device memory and streams.
@@ -17,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -30,6 +32,8 @@ FMT = {"q8_0": 0, "q4k": 1, "q6k": 2, "q2k": 3, "q3k": 4, "q5k": 5, "q8k": 6,
 FMT_NAME = {v: k for k, v in FMT.items()}
 PATH = {"auto": 0, "gemv": 1, "mfma_bf16": 2, "mfma_i8": 3, "mfma_fp8": 4}
 ACT = {"silu": 0, "relu": 1, "sigmoid": 2}
+SCORE = {"softmax": 0, "sigmoid": 1}
+MAX_TOP_N = 64  # QLINEAR_MAX_TOP_N
 
 Q_OK, Q_EINVAL, Q_ESHAPE, Q_EALIGN, Q_ENOTSUP, Q_EHIP, Q_ESCRATCH = 0, -1, -2, -3, -4, -5, -6
 STATIC_SCRATCH_BYTES = 32 << 20  # QLINEAR_STATIC_SCRATCH_BYTES
@@ -48,6 +52,13 @@ SIGNATURES = {
     "q_embed": (_INT, [_INT, _P, _I64, _I64, _P, _I64, _P, _P]),
     "qmatmul_glu_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64]),
     "qmatmul_glu": (_INT, [_INT, _P, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _SZ, _P]),
+    "q_moe_route": (_INT, [_P, _I64, _I64, _INT, _INT, _P, _INT, ctypes.c_float, _P, _P, _P]),
+    "qmatmul_moe_workspace_bytes": (_SZ, [_INT, _INT, _I64, _I64, _INT, _I64, _I64]),
+    "qmatmul_moe": (_INT, [_INT, _P, _P, _INT, _P, _P, _P, _P, _P, _I64, _I64, _INT, _I64, _I64, _INT, _P, _SZ, _P]),
+    "q_logprobs_workspace_bytes": (_SZ, [_I64, _I64, _INT]),
+    "q_logprobs": (_INT, [_P, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "qmatmul_logprobs_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _INT]),
+    "qmatmul_logprobs": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "q_dequantize": (_INT, [_INT, _P, _I64, _I64, _P, _P]),
     "isq_resolve_level": (_INT, [_INT, _IP]),
     "isq_sensitive_fmt": (_INT, [_INT, _IP]),
@@ -116,6 +127,52 @@ def _dev(t: torch.Tensor, name: str, dtype=None):
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _shaped(t, name: str, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be of shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _out(t, name: str, shape, dtype, like: torch.Tensor) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    _shaped(t, name, shape)
+    return t
+
+
+def _blocks_fit(t: torch.Tensor, name: str, fmt: int, N: int, K: int):
+    """A block buffer at least as long as its [N][K] weight needs (a shape the
+    format does not take has no size here; the call reports it)."""
+    if t.numel() * t.element_size() < lib().q_blocks_bytes(fmt, N, K):
+        raise ValueError(f"{name} is too small for [{N}][{K}]")
+
+
+def _ws(t):
+    return (None, 0) if t is None else (_dev(t, "workspace"), t.numel() * t.element_size())
+
+
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *a):
+        return False
+
+
+_HERE_ALREADY = _Here()
+
+
+def _on(first: torch.Tensor, *more):
+    """The device of a call's tensors, which must be one; entered if it is not
+    the current one, so that the launch and its stream belong to it."""
+    d = first.device
+    for t in more:
+        if t is not None and t.device != d:
+            raise ValueError(f"tensors on different devices: {d} and {t.device}")
+    if d.type != "cuda" or d.index == torch.cuda.current_device():
+        return _HERE_ALREADY
+    return torch.cuda.device(d)
 
 
 # ----------------------------------------------------------------------------
@@ -269,6 +326,160 @@ def embed(fmt, blocks: torch.Tensor, N: int, K: int, ids: torch.Tensor,
     _check("q_embed", lib().q_embed(_fmt(fmt), _dev(blocks, "blocks", torch.uint8), N, K,
                                     _dev(ids, "ids", torch.int32), n, _dev(out, "out", torch.float32),
                                     _stream()))
+    return out
+
+
+def moe_route(logits: torch.Tensor, top_k: int, score="softmax", bias: torch.Tensor | None = None, renorm: bool = True,
+              scale: float = 1.0, ids: torch.Tensor | None = None, weights: torch.Tensor | None = None):
+    """A router's choice from its fp32 logits [T][E]: (ids int32 [T][top_k],
+    weights fp32 [T][top_k]).  ``score``: softmax | sigmoid; ``bias`` [E]
+    (sigmoid only) takes part in the choice; ``renorm``: weights divided by
+    their sum.  Logits of -inf are never chosen (id -1, weight 0)."""
+    if logits.dim() != 2:
+        raise ValueError("logits must be 2-D [T][E]")
+    T, E = logits.shape
+    _shaped(bias, "bias", (E,))
+    ids = _out(ids, "ids", (T, top_k), torch.int32, logits)
+    weights = _out(weights, "weights", (T, top_k), torch.float32, logits)
+    sc = SCORE[score] if isinstance(score, str) else int(score)
+    if T == 0:
+        return ids, weights
+    with _on(logits, bias, ids, weights):
+        _check("q_moe_route", lib().q_moe_route(_dev(logits, "logits", torch.float32), T, E, top_k, sc,
+                                                None if bias is None else _dev(bias, "bias", torch.float32),
+                                                int(bool(renorm)), scale, _dev(ids, "ids", torch.int32),
+                                                _dev(weights, "weights", torch.float32), _stream()))
+    return ids, weights
+
+
+def moe_workspace_bytes(fmt, fmt_down, T: int, E: int, top_k: int, F: int, K: int) -> int:
+    return int(lib().qmatmul_moe_workspace_bytes(_fmt(fmt), _fmt(fmt_down), T, E, top_k, F, K))
+
+
+def qmatmul_moe(fmt, gate_blocks: torch.Tensor, up_blocks: torch.Tensor, down_blocks: torch.Tensor, X: torch.Tensor,
+                ids: torch.Tensor, weights: torch.Tensor, E: int, F: int, act="silu", fmt_down=None,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Mixture-of-experts layer as fp32 [T][K]: sum over j of weights[t][j] *
+    Wd[e] . (act(Wg[e] . x) * (Wu[e] . x)), e = ids[t][j], for the blocks of the
+    experts' stacked [E*F][K] gate and up weights (``fmt``) and [E*K][F] down
+    weights (``fmt_down``, by default ``fmt``).  ids outside [0, E) add nothing."""
+    if X.dim() != 2 or ids.dim() != 2:
+        raise ValueError("X must be 2-D [T][K] and ids 2-D [T][top_k]")
+    T, K = X.shape
+    k = ids.shape[1]
+    if ids.shape[0] != T or weights.shape != ids.shape:
+        raise ValueError("ids and weights must be [T][top_k]")
+    f, fd = _fmt(fmt), _fmt(fmt if fmt_down is None else fmt_down)
+    _blocks_fit(gate_blocks, "gate_blocks", f, E * F, K)
+    _blocks_fit(up_blocks, "up_blocks", f, E * F, K)
+    _blocks_fit(down_blocks, "down_blocks", fd, E * K, F)
+    out = _out(out, "Y", (T, K), torch.float32, X)
+    a = ACT[act] if isinstance(act, str) else int(act)
+    if T == 0:
+        return out
+    L = lib()
+    if workspace is None:
+        need = L.qmatmul_moe_workspace_bytes(f, fd, T, E, k, F, K)
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
+    with _on(X, gate_blocks, up_blocks, down_blocks, ids, weights, out, workspace):
+        ws_ptr, ws_bytes = _ws(workspace)
+        _check("qmatmul_moe", L.qmatmul_moe(f, _dev(gate_blocks, "gate_blocks", torch.uint8),
+                                            _dev(up_blocks, "up_blocks", torch.uint8), fd,
+                                            _dev(down_blocks, "down_blocks", torch.uint8),
+                                            _dev(X, "X", torch.bfloat16), _dev(ids, "ids", torch.int32),
+                                            _dev(weights, "weights", torch.float32), _dev(out, "Y", torch.float32),
+                                            T, E, k, F, K, a, ws_ptr, ws_bytes, _stream()))
+    return out
+
+
+class LogProbs(NamedTuple):
+    """Results of ``logprobs``: logprob and rank [M] (None without targets),
+    entropy [M], top_ids and top_logprobs [M][top] (None for top = 0)."""
+    logprob: torch.Tensor | None
+    rank: torch.Tensor | None
+    entropy: torch.Tensor | None
+    top_ids: torch.Tensor | None
+    top_logprobs: torch.Tensor | None
+
+
+def _logprob_out(out, M, targets, top, like):
+    if targets is not None:
+        _shaped(targets, "targets", (M,))
+    if out is None:
+        f, i = dict(dtype=torch.float32, device=like.device), dict(dtype=torch.int32, device=like.device)
+        given = targets is not None
+        out = LogProbs(torch.empty(M, **f) if given else None, torch.empty(M, **i) if given else None,
+                       torch.empty(M, **f), torch.empty((M, top), **i) if top else None,
+                       torch.empty((M, top), **f) if top else None)
+    for t, name, shape in ((out.logprob, "logprob", (M,)), (out.rank, "rank", (M,)), (out.entropy, "entropy", (M,)),
+                           (out.top_ids, "top_ids", (M, top)), (out.top_logprobs, "top_logprobs", (M, top))):
+        _shaped(t, name, shape)
+    ptrs = [None if t is None else _dev(t, name, dt) for t, name, dt in
+            ((out.logprob, "logprob", torch.float32), (out.rank, "rank", torch.int32),
+             (out.entropy, "entropy", torch.float32), (out.top_ids, "top_ids", torch.int32),
+             (out.top_logprobs, "top_logprobs", torch.float32))]
+    return out, ptrs
+
+
+def logprobs_workspace_bytes(M: int, V: int, top: int = 0) -> int:
+    return int(lib().q_logprobs_workspace_bytes(M, V, top))
+
+
+def logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top: int = 0, out: LogProbs | None = None,
+             workspace: torch.Tensor | None = None) -> LogProbs:
+    """Log probability and rank of ``targets`` (int32 [M]; outside [0, V): not
+    scored, 0), entropy and the ``top`` most probable tokens of each row of
+    fp32 logits [M][V] (rows may be apart: any stride of at least V along M).
+    -inf masks a token.  ``out``: a LogProbs whose tensors are overwritten
+    (those that are None are not computed)."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be 2-D [M][V] with contiguous rows")
+    M, V = logits.shape
+    ld = logits.stride(0) if M > 1 else V
+    if logits.dtype != torch.float32 or not logits.is_cuda:
+        raise ValueError(f"logits must be a torch.float32 device tensor, got {logits.dtype}")
+    out, ptrs = _logprob_out(out, M, targets, top, logits)
+    if M == 0:
+        return out
+    L = lib()
+    if workspace is None:
+        need = L.q_logprobs_workspace_bytes(M, V, top)
+        workspace = torch.empty(need, dtype=torch.uint8, device=logits.device) if need else None
+    with _on(logits, targets, *out, workspace):
+        ws_ptr, ws_bytes = _ws(workspace)
+        _check("q_logprobs", L.q_logprobs(ctypes.c_void_p(logits.data_ptr()), M, V, ld,
+                                          None if targets is None else _dev(targets, "targets", torch.int32), top,
+                                          *ptrs, ws_ptr, ws_bytes, _stream()))
+    return out
+
+
+def head_workspace_bytes(fmt, M: int, N: int, K: int, top: int = 0) -> int:
+    return int(lib().qmatmul_logprobs_workspace_bytes(_fmt(fmt), M, N, K, top))
+
+
+def qmatmul_logprobs(fmt, blocks: torch.Tensor, X: torch.Tensor, N: int, targets: torch.Tensor | None = None,
+                     top: int = 0, out: LogProbs | None = None, workspace: torch.Tensor | None = None) -> LogProbs:
+    """``logprobs`` of the logits X . deq(W)^T of a quantized [N][K] output
+    head, for X bf16 [M][K], without holding the M x N logits (at most 2^26 of
+    them at a time, in the workspace)."""
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D [M][K]")
+    M, K = X.shape
+    f = _fmt(fmt)
+    _blocks_fit(blocks, "blocks", f, N, K)
+    out, ptrs = _logprob_out(out, M, targets, top, X)
+    if M == 0:
+        return out
+    L = lib()
+    if workspace is None:
+        need = L.qmatmul_logprobs_workspace_bytes(f, M, N, K, top)
+        workspace = torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
+    with _on(X, blocks, targets, *out, workspace):
+        ws_ptr, ws_bytes = _ws(workspace)
+        _check("qmatmul_logprobs", L.qmatmul_logprobs(f, _dev(blocks, "blocks", torch.uint8),
+                                                      _dev(X, "X", torch.bfloat16), M, N, K,
+                                                      None if targets is None else _dev(targets, "targets", torch.int32),
+                                                      top, *ptrs, ws_ptr, ws_bytes, _stream()))
     return out
 
 

@@ -3,6 +3,8 @@
 // argument error never launches anything.
 #include "../../include/qlinear.h"
 #include "gemv_fp8.h"
+#include "logprobs.h"
+#include "moe.h"
 #include "qlinear_internal.h"
 
 #include <stdint.h>
@@ -18,6 +20,7 @@ bool implemented(int fmt)
 }
 bool known(int fmt) { return fmt >= QFMT_Q8_0 && fmt <= QFMT_FP8; }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;
 
@@ -61,6 +64,58 @@ int matmul_args(int fmt, const void *blocks, const void *X, const float *Y, int6
         N * K > kMaxElems || M * K > kMaxElems || M * N > kMaxElems)
         return Q_ESHAPE;
     return Q_OK;
+}
+
+// shapes of a mixture-of-experts call: stacked [E*F][K] gate and up weights,
+// stacked [E*K][F] down weights
+int moe_shape(int fmt_gu, int fmt_d, int64_t T, int64_t E, int64_t k, int64_t F, int64_t K)
+{
+    if (!implemented(fmt_gu) || !implemented(fmt_d))
+        return Q_ENOTSUP;
+    if (T < 0 || T > QLINEAR_MAX_M || E < 1 || E > QLINEAR_MAX_EXPERTS || k < 1 || k > QLINEAR_MAX_TOP_K || F < 1 ||
+        F > QLINEAR_MAX_K || K < 1 || K > QLINEAR_MAX_K)
+        return Q_ESHAPE;
+    if (check_tensor(fmt_gu, E * F, K, QLINEAR_MAX_N) != Q_OK || check_tensor(fmt_d, E * K, F, QLINEAR_MAX_N) != Q_OK)
+        return Q_ESHAPE;
+    if (T * k * F > kMaxElems || T * k * K > kMaxElems)
+        return Q_ESHAPE;
+    return Q_OK;
+}
+
+// the parts of the log-probability calls that do not depend on the logits
+int logprob_args(const int32_t *targets, int top_n, const float *logprob, const int32_t *rank, const float *entropy,
+                 const int32_t *top_ids, const float *top_logprobs)
+{
+    if (top_n < 0 || top_n > QLINEAR_MAX_TOP_N)
+        return Q_ESHAPE;
+    if ((logprob || rank) && !targets)
+        return Q_EINVAL;
+    if (top_n > 0 && (!top_ids || !top_logprobs))
+        return Q_EINVAL;
+    if (!logprob && !rank && !entropy && top_n == 0)
+        return Q_EINVAL;  // nothing to compute
+    if (!aligned4(targets) || !aligned4(logprob) || !aligned4(rank) || !aligned4(entropy) || !aligned4(top_ids) ||
+        !aligned4(top_logprobs))
+        return Q_EALIGN;
+    return Q_OK;
+}
+
+// qmatmul_logprobs keeps at most 2^26 logits (256 MiB, the size of the last
+// cache) at a time, in whole tiles of the prefill kernel where more than one
+// tile of rows fits
+int64_t head_rows(int64_t M, int64_t N)
+{
+    int64_t rows = ((int64_t)1 << 26) / N;
+    rows = rows >= 256 ? rows / 256 * 256 : rows < 1 ? 1 : rows;
+    return rows < M ? rows : M;
+}
+size_t head_logits_bytes(int64_t rows, int64_t N) { return (size_t)ql::up16(4 * rows * N); }
+// partial results of the full chunks and of the last, shorter one
+int64_t head_parts_bytes(int64_t M, int64_t rows, int64_t N, int top_n)
+{
+    const int64_t a = ql::logprobs_workspace(rows, N, top_n), last = M % rows;
+    const int64_t b = last ? ql::logprobs_workspace(last, N, top_n) : 0;
+    return a > b ? a : b;
 }
 
 // the GEMV of a format: FP8 one- and two-token shapes on their own one-shot
@@ -296,6 +351,156 @@ int qmatmul_glu(int fmt, const void *gate_blocks, const void *up_blocks, const v
     return status_of(ql::launch_glu_apply(G, H_fp32, M * F, act, s));
 }
 
+int q_moe_route(const float *logits, int64_t T, int64_t E, int top_k, int score, const float *bias, int renorm,
+                float scale, int32_t *ids, float *weights, void *stream)
+{
+    if (!logits || !ids || !weights)
+        return Q_EINVAL;
+    if (score != QSCORE_SOFTMAX && score != QSCORE_SIGMOID)
+        return Q_EINVAL;
+    if (!aligned4(logits) || !aligned4(ids) || !aligned4(weights) || !aligned4(bias))
+        return Q_EALIGN;
+    if (T < 0 || T > QLINEAR_MAX_M || E < 1 || E > QLINEAR_MAX_EXPERTS || top_k < 1 || top_k > QLINEAR_MAX_TOP_K ||
+        top_k > E)
+        return Q_ESHAPE;
+    if (bias && score != QSCORE_SIGMOID)
+        return Q_ENOTSUP;
+    if (T == 0)
+        return Q_OK;
+    return status_of(ql::launch_moe_route(logits, (int)T, (int)E, top_k, score, bias, renorm, scale, ids, weights,
+                                          as_stream(stream)));
+}
+
+size_t qmatmul_moe_workspace_bytes(int fmt_gate_up, int fmt_down, int64_t T, int64_t E, int top_k, int64_t F, int64_t K)
+{
+    if (moe_shape(fmt_gate_up, fmt_down, T, E, top_k, F, K) != Q_OK || T == 0)
+        return 0;
+    return (size_t)ql::moe_workspace((int)T, (int)E, top_k, F, K);
+}
+
+int qmatmul_moe(int fmt_gate_up, const void *gate_blocks, const void *up_blocks, int fmt_down, const void *down_blocks,
+                const void *X_bf16, const int32_t *ids, const float *weights, float *Y_fp32, int64_t T, int64_t E,
+                int top_k, int64_t F, int64_t K, int act, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!known(fmt_gate_up) || !known(fmt_down))
+        return Q_EINVAL;
+    if (!implemented(fmt_gate_up) || !implemented(fmt_down))
+        return Q_ENOTSUP;
+    if (!gate_blocks || !up_blocks || !down_blocks || !X_bf16 || !ids || !weights || !Y_fp32)
+        return Q_EINVAL;
+    if (act < QACT_SILU || act > QACT_SIGMOID)
+        return Q_EINVAL;
+    if (!aligned16(gate_blocks) || !aligned16(up_blocks) || !aligned16(down_blocks) || !aligned16(X_bf16) ||
+        !aligned16(Y_fp32) || !aligned4(ids) || !aligned4(weights))
+        return Q_EALIGN;
+    const int st = moe_shape(fmt_gate_up, fmt_down, T, E, top_k, F, K);
+    if (st != Q_OK)
+        return st;
+    if (T == 0)
+        return Q_OK;
+    if (!workspace)
+        return Q_EINVAL;
+    if (!aligned16(workspace))
+        return Q_EALIGN;
+    if (workspace_bytes < qmatmul_moe_workspace_bytes(fmt_gate_up, fmt_down, T, E, top_k, F, K))
+        return Q_EINVAL;
+    ql::MoeArgs a;
+    a.fmt_gu = fmt_gate_up, a.fmt_d = fmt_down, a.act = act;
+    a.T = (int)T, a.E = (int)E, a.k = top_k, a.F = F, a.K = K;
+    a.gate = static_cast<const uint8_t *>(gate_blocks);
+    a.up = static_cast<const uint8_t *>(up_blocks);
+    a.down = static_cast<const uint8_t *>(down_blocks);
+    a.X = static_cast<const uint16_t *>(X_bf16);
+    a.ids = ids, a.weights = weights, a.Y = Y_fp32;
+    a.ws = static_cast<uint8_t *>(workspace);
+    return status_of(ql::launch_moe(a, as_stream(stream)));
+}
+
+size_t q_logprobs_workspace_bytes(int64_t M, int64_t V, int top_n)
+{
+    if (M < 1 || M > QLINEAR_MAX_M || V < 1 || V > QLINEAR_MAX_N || top_n < 0 || top_n > QLINEAR_MAX_TOP_N)
+        return 0;
+    return (size_t)ql::logprobs_workspace(M, V, top_n);
+}
+
+int q_logprobs(const float *logits, int64_t M, int64_t V, int64_t ld, const int32_t *targets, int top_n, float *logprob,
+               int32_t *rank, float *entropy, int32_t *top_ids, float *top_logprobs, void *workspace,
+               size_t workspace_bytes, void *stream)
+{
+    int st = logprob_args(targets, top_n, logprob, rank, entropy, top_ids, top_logprobs);
+    if (st != Q_OK)
+        return st;
+    if (!logits)
+        return Q_EINVAL;
+    if (!aligned4(logits))
+        return Q_EALIGN;
+    if (M < 0 || M > QLINEAR_MAX_M || V < 1 || V > QLINEAR_MAX_N || ld < V || ld > kMaxElems || M * ld > kMaxElems)
+        return Q_ESHAPE;
+    if (M == 0)
+        return Q_OK;
+    const size_t need = q_logprobs_workspace_bytes(M, V, top_n);
+    if (need) {
+        if (!workspace)
+            return Q_EINVAL;
+        if (!aligned16(workspace))
+            return Q_EALIGN;
+        if (workspace_bytes < need)
+            return Q_EINVAL;
+    }
+    ql::LogprobArgs a;
+    a.logits = logits, a.M = M, a.V = V, a.ld = ld, a.targets = targets, a.top = top_n;
+    a.logprob = logprob, a.rank = rank, a.entropy = entropy, a.top_ids = top_ids, a.top_logprobs = top_logprobs;
+    a.ws = static_cast<uint8_t *>(workspace);
+    return status_of(ql::launch_logprobs(a, as_stream(stream)));
+}
+
+size_t qmatmul_logprobs_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int top_n)
+{
+    if (!implemented(fmt) || M < 1 || M > QLINEAR_MAX_M || check_tensor(fmt, N, K, QLINEAR_MAX_N) != Q_OK ||
+        M * K > kMaxElems || top_n < 0 || top_n > QLINEAR_MAX_TOP_N)
+        return 0;
+    const int64_t rows = head_rows(M, N);
+    return head_logits_bytes(rows, N) + ql::up16(head_parts_bytes(M, rows, N, top_n));
+}
+
+int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M, int64_t N, int64_t K,
+                     const int32_t *targets, int top_n, float *logprob, int32_t *rank, float *entropy, int32_t *top_ids,
+                     float *top_logprobs, void *workspace, size_t workspace_bytes, void *stream)
+{
+    int st = logprob_args(targets, top_n, logprob, rank, entropy, top_ids, top_logprobs);
+    if (st != Q_OK)
+        return st;
+    if (M == 0)
+        return !known(fmt) ? Q_EINVAL : !implemented(fmt) ? Q_ENOTSUP : !blocks || !X_bf16 ? Q_EINVAL : Q_OK;
+    if (!workspace)
+        return Q_EINVAL;
+    st = matmul_args(fmt, blocks, X_bf16, static_cast<const float *>(workspace), M < 1 ? 1 : M, N, K);
+    if (st != Q_OK)
+        return st;
+    if (M < 1)
+        return Q_ESHAPE;
+    if (workspace_bytes < qmatmul_logprobs_workspace_bytes(fmt, M, N, K, top_n))
+        return Q_EINVAL;
+    const int64_t rows = head_rows(M, N);
+    const size_t logits_bytes = head_logits_bytes(rows, N);
+    float *logits = static_cast<float *>(workspace);
+    uint8_t *parts = static_cast<uint8_t *>(workspace) + logits_bytes;
+    const auto *X = static_cast<const uint16_t *>(X_bf16);
+    for (int64_t m = 0; m < M; m += rows) {
+        const int64_t n = M - m < rows ? M - m : rows;
+        st = qmatmul(fmt, blocks, X + m * K, logits, n, N, K, stream);
+        if (st != Q_OK)
+            return st;
+        st = q_logprobs(logits, n, N, N, targets ? targets + m : nullptr, top_n, logprob ? logprob + m : nullptr,
+                        rank ? rank + m : nullptr, entropy ? entropy + m : nullptr,
+                        top_n ? top_ids + m * top_n : nullptr, top_n ? top_logprobs + m * top_n : nullptr, parts,
+                        workspace_bytes - logits_bytes, stream);
+        if (st != Q_OK)
+            return st;
+    }
+    return Q_OK;
+}
+
 int q_dequantize(int fmt, const void *blocks, int64_t N, int64_t K, float *W_fp32, void *stream)
 {
     if (!known(fmt))
@@ -457,7 +662,7 @@ const char *q_strerror(int status)
     case Q_OK: return "ok";
     case Q_EINVAL: return "invalid argument (null pointer, unknown format or path, bad workspace)";
     case Q_ESHAPE: return "shape out of range (M, N, K limits; K a multiple of 256, or of 32 for Q8_0)";
-    case Q_EALIGN: return "pointer not 16-byte aligned";
+    case Q_EALIGN: return "pointer not aligned (16 bytes; 4 for ids, logits and per-row results)";
     case Q_ENOTSUP: return "format or path not implemented for these arguments";
     case Q_EHIP: return "HIP runtime error at launch";
     case Q_ESCRATCH: return "activation blocks larger than the library's fixed scratch buffer (QLINEAR_STATIC_SCRATCH_BYTES)";

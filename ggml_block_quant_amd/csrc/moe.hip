@@ -1,0 +1,837 @@
+// moe.hip -- the mixture-of-experts layer on block-quantized expert weights:
+//   Y[t] = sum_j w[t][j] * Wd[e] . (act(Wg[e] . x_t) * (Wu[e] . x_t)),  e = ids[t][j],
+// and the router's choice that produces ids and w.
+//
+// Two forms.
+//   Few tokens: two kernels.  moe_glu_kernel computes H[t][j] = act(g) * u, a
+//   workgroup per (token, choice) and group of rows; moe_down_kernel computes
+//   Y, a workgroup per token and group of output rows, whose lanes walk the
+//   chunks of all k chosen experts' rows at once, so the join over the
+//   choices is the reduction over the lanes and no partial result is stored.
+//   More tokens: the (token, choice) pairs are sorted by expert
+//   (moe_plan_kernel), two grouped matrix-core products run over tiles of one
+//   expert's pairs, and moe_join_kernel adds each token's k results in the
+//   order of its choices.
+//
+// Nothing is added atomically: a token's result does not depend on the order
+// in which workgroups run.
+#include "moe.h"
+#include "decode.h"
+
+#include <math.h>
+
+namespace ql {
+namespace {
+
+typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned u32x4_t __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ float bf16_lo(uint32_t p) { return __uint_as_float(p << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t p) { return __uint_as_float(p & 0xffff0000u); }
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+
+// Sums of V values over the 64 lanes (V a power of two <= 64): while more
+// than one is left a step keeps half of them, so V values cost about V + 4
+// additions.  Lanes 0 .. V-1 end with the total of value sum_index<V>(lane).
+template <int V>
+__device__ __forceinline__ float wave_sums(float (&v)[V], int lane)
+{
+    int left = V;
+#pragma unroll
+    for (int b = 0; b < 6; b++) {
+        auto partner = [&](float x) {
+            if (b == 0)
+                return dpp<0xB1>(x);  // lane ^ 1
+            if (b == 1)
+                return dpp<0x4E>(x);  // lane ^ 2
+            return __shfl_xor(x, 1 << b);
+        };
+        if (left > 1) {
+            left /= 2;
+            const bool up = (lane >> b) & 1;
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (i < left) {
+                    const float keep = up ? v[i + left] : v[i], send = up ? v[i] : v[i + left];
+                    v[i] = keep + partner(send);
+                }
+        } else {
+            v[0] += partner(v[0]);
+        }
+    }
+    return v[0];
+}
+template <int V>
+__device__ __forceinline__ int sum_index(int lane)
+{
+    int idx = 0, part = V;
+#pragma unroll
+    for (int b = 0; b < 6; b++)
+        if (part > 1) {
+            part >>= 1;
+            if ((lane >> b) & 1)
+                idx += part;
+        }
+    return idx;
+}
+
+// ---------------------------------------------------------------------------
+// Router: a wave per token.  Expert e sits in lane e % 64, register e / 64.
+// Choices are made one by one: the wave's largest key, the lowest index among
+// equal ones, which then leaves the race.
+// ---------------------------------------------------------------------------
+template <typename KT>
+__device__ __forceinline__ KT wave_max(KT v)
+{
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1) {
+        const KT o = __shfl_xor(v, s);
+        v = o > v ? o : v;
+    }
+    return v;
+}
+
+// BIAS: the key is sigmoid(x) + bias in 64 bits (where 32 would let the
+// rounding of e^-x decide between close experts); otherwise it is x itself,
+// in whose order both scores are.
+template <int VPT, bool BIAS>
+__global__ __launch_bounds__(256) void moe_route_kernel(const float *__restrict__ logits, int T, int E, int k, int score,
+                                                        const float *__restrict__ bias, int renorm, float scale,
+                                                        int32_t *__restrict__ ids, float *__restrict__ weights)
+{
+    using KT = std::conditional_t<BIAS, double, float>;
+    const int lane = threadIdx.x & 63;
+    const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= T)
+        return;
+    const float *row = logits + (int64_t)t * E;
+    KT key[VPT];
+    float x[VPT], m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < VPT; i++) {
+        const int e = lane + 64 * i;
+        float v = e < E ? row[e] : -INFINITY;
+        v = v == v ? fminf(v, 3.4028234663852886e38f) : -INFINITY;  // NaN: switched off
+        x[i] = v;
+        m = fmaxf(m, v);
+        if constexpr (BIAS)
+            key[i] = v > -INFINITY ? 1.0 / (1.0 + exp(-(double)v)) + (double)bias[e] : -(double)INFINITY;
+        else
+            key[i] = v;
+    }
+    m = wave_max(m);
+    int my_id = -1;
+    float my_x = 0.0f;
+    for (int j = 0; j < k; j++) {
+        KT best = key[0];
+        int at = 0;
+#pragma unroll
+        for (int i = 1; i < VPT; i++)
+            if (key[i] > best)
+                best = key[i], at = i;
+        const KT top = wave_max(best);
+        if (!(top > -(KT)INFINITY))
+            break;
+        // the lowest index with that key
+        int e = best == top ? lane + 64 * at : 0x7FFFFFFF;
+        const uint64_t who = __ballot(best == top);
+        if (__popcll(who) == 1)
+            e = __shfl(e, __ffsll((unsigned long long)who) - 1);
+        else
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1)
+                e = min(e, __shfl_xor(e, s));
+        float xe = 0.0f;
+#pragma unroll
+        for (int i = 0; i < VPT; i++)
+            if (e == lane + 64 * i) {
+                key[i] = -(KT)INFINITY;
+                xe = x[i];
+            }
+        xe = __shfl(xe, e & 63);
+        if (lane == j) {
+            my_id = e;
+            my_x = xe;
+        }
+    }
+    // the chosen experts' scores, one per lane
+    double p = 0.0;
+    if (score == 0) {
+        float z = 1.0f;
+        if (!renorm) {
+            z = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPT; i++)
+                z += x[i] > -INFINITY ? expf(x[i] - m) : 0.0f;
+#pragma unroll
+            for (int s = 1; s < 64; s <<= 1)
+                z += __shfl_xor(z, s);
+        }
+        p = my_id >= 0 ? (double)(expf(my_x - m) / z) : 0.0;
+    } else {
+        p = my_id >= 0 ? 1.0 / (1.0 + exp(-(double)my_x)) : 0.0;
+    }
+    if (renorm) {
+        double s = p;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1)
+            s += __shfl_xor(s, d);
+        p = s > 0.0 ? p / s : 0.0;
+    }
+    if (lane < k) {
+        ids[(int64_t)t * k + lane] = my_id;
+        weights[(int64_t)t * k + lane] = (float)(p * (double)scale);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Few tokens.  A row of K weights is cut into chunks of 32; a lane owns a
+// chunk of the row, keeps its 32 activations in registers (fp32: exact for
+// bf16 X, and H is never rounded to fewer bits) and walks down R rows, all of
+// whose loads are issued before the first is used.  Per row it forms
+// sum q * a of the codes and applies the block scales once, so only fp32
+// sums round; the lanes' sums are joined by wave_sums and, where a row takes
+// several waves, through LDS.
+// ---------------------------------------------------------------------------
+struct Mat {
+    const uint8_t *B;
+    Planes p;
+    int64_t K;  // row length
+};
+
+template <int FMT> struct Raw { int64_t task; };
+template <> struct Raw<FMT_Q4K> { uint4 c; uint32_t h; };
+template <> struct Raw<FMT_Q6K> { uint4 lo; uint2 hi; uint32_t sc2, d; };
+template <> struct Raw<FMT_Q8_0> { uint4 c0, c1; uint32_t d; };
+
+__device__ __forceinline__ uint4 stream16(const uint8_t *p)
+{
+    const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t *>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+}
+
+// chunk c of row n; the lanes of a quad hold chunks of one group of 256
+template <int FMT>
+__device__ __forceinline__ void load_raw(const Mat &w, int64_t n, int c, int lane, Raw<FMT> &r)
+{
+    if constexpr (FMT == FMT_Q4K) {
+        const int64_t sub = n * (w.K / 32) + c;
+        r.c = stream16(w.B + 16 * sub);
+        // one dword of the 16-byte group header per lane, shared in the quad
+        r.h = *reinterpret_cast<const uint32_t *>(w.B + w.p.scales + 16 * (sub >> 3) + 4 * (lane & 3));
+    } else if constexpr (FMT == FMT_Q6K) {
+        const int64_t g = n * (w.K / 256) + (c >> 3);
+        const int cc = c & 7;
+        r.lo = stream16(w.B + 192 * g + 16 * cc);
+        r.hi = *reinterpret_cast<const uint2 *>(w.B + 192 * g + 128 + 8 * cc);
+        r.sc2 = *reinterpret_cast<const uint16_t *>(w.B + w.p.scales + 16 * g + 2 * cc);
+        r.d = *reinterpret_cast<const uint16_t *>(w.B + w.p.d + 2 * g);
+    } else if constexpr (FMT == FMT_Q8_0) {
+        const int64_t b = n * (w.K / 32) + c;
+        r.c0 = stream16(w.B + 32 * b);
+        r.c1 = stream16(w.B + 32 * b + 16);
+        r.d = *reinterpret_cast<const uint16_t *>(w.B + w.p.scales + 2 * b);
+    } else {
+        r.task = 4 * (n * (w.K / 32) + c);
+    }
+}
+
+__device__ __forceinline__ float ub(uint32_t w, int b) { return (float)((w >> (8 * b)) & 0xffu); }
+__device__ __forceinline__ float sb(uint32_t w, int b) { return (float)(int8_t)(w >> (8 * b)); }
+
+// sum over the chunk of w * a; asum = sum of a over the chunk (Q4K's mins)
+template <int FMT>
+__device__ __forceinline__ float dot32(const Mat &w, const Raw<FMT> &r, int c, const float (&a)[32], float asum)
+{
+    if constexpr (FMT == FMT_Q4K) {
+        const int h = (int)r.h, j = c & 7;
+        const uint32_t h0 = __builtin_amdgcn_update_dpp(0, h, 0x00, 0xF, 0xF, false);
+        const uint32_t h1 = __builtin_amdgcn_update_dpp(0, h, 0x55, 0xF, 0xF, false);
+        const uint32_t h2 = __builtin_amdgcn_update_dpp(0, h, 0xAA, 0xF, 0xF, false);
+        const uint32_t h3 = __builtin_amdgcn_update_dpp(0, h, 0xFF, 0xF, 0xF, false);
+        const uint32_t sc = ((h1 >> (4 * j)) & 15u) | ((h3 >> (2 * j)) & 3u) << 4;
+        const uint32_t mq = ((h2 >> (4 * j)) & 15u) | ((h3 >> (16 + 2 * j)) & 3u) << 4;
+        const float S = f16_bits_to_f32(h0) * (float)sc, Mn = f16_bits_to_f32(h0 >> 16) * (float)mq;
+        const uint32_t cw[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+        float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            // bytes of the low nibbles: elements 0, 4, 1, 5; of the high ones: 2, 6, 3, 7
+            const uint32_t lo = cw[q] & 0x0F0F0F0Fu, hi = (cw[q] >> 4) & 0x0F0F0F0Fu;
+            const float *x = a + 8 * q;
+            d0 = fmaf(ub(lo, 0), x[0], d0);
+            d1 = fmaf(ub(lo, 1), x[4], d1);
+            d0 = fmaf(ub(lo, 2), x[1], d0);
+            d1 = fmaf(ub(lo, 3), x[5], d1);
+            d0 = fmaf(ub(hi, 0), x[2], d0);
+            d1 = fmaf(ub(hi, 1), x[6], d1);
+            d0 = fmaf(ub(hi, 2), x[3], d0);
+            d1 = fmaf(ub(hi, 3), x[7], d1);
+        }
+        return fmaf(S, d0 + d1, -Mn * asum);
+    } else if constexpr (FMT == FMT_Q6K) {
+        const float d = f16_bits_to_f32(r.d);
+        const uint32_t lw[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
+        const uint32_t hw[2] = {r.hi.x, r.hi.y};
+        float s[2] = {0.0f, 0.0f};  // the two sub-blocks of 16, in units of a quarter
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            // byte b of lo (hi): four times the signed code of elements
+            // 0, 4, 1, 5 (2, 6, 3, 7): the low nibble at bits 2-5, the two
+            // high bits above it, the top one flipped (u - 32 in two's complement)
+            const uint32_t H = hw[q >> 1] >> (8 * (q & 1)), H2 = H >> 2;
+            const uint32_t t0 = (H & 0x00030003u) | ((H & 0x00300030u) << 4);
+            const uint32_t t1 = (H2 & 0x00030003u) | ((H2 & 0x00300030u) << 4);
+            const uint32_t lo = (((lw[q] << 2) & 0x3C3C3C3Cu) | (t0 << 6)) ^ 0x80808080u;
+            const uint32_t hi = (((lw[q] >> 2) & 0x3C3C3C3Cu) | (t1 << 6)) ^ 0x80808080u;
+            const float *x = a + 8 * q;
+            float v = s[q >> 1];
+            v = fmaf(sb(lo, 0), x[0], v);
+            v = fmaf(sb(lo, 1), x[4], v);
+            v = fmaf(sb(lo, 2), x[1], v);
+            v = fmaf(sb(lo, 3), x[5], v);
+            v = fmaf(sb(hi, 0), x[2], v);
+            v = fmaf(sb(hi, 1), x[6], v);
+            v = fmaf(sb(hi, 2), x[3], v);
+            v = fmaf(sb(hi, 3), x[7], v);
+            s[q >> 1] = v;
+        }
+        const float Sa = d * (float)(int8_t)r.sc2, Sb = d * (float)(int8_t)(r.sc2 >> 8);
+        return 0.25f * fmaf(Sa, s[0], Sb * s[1]);
+    } else if constexpr (FMT == FMT_Q8_0) {
+        const uint32_t cw[8] = {r.c0.x, r.c0.y, r.c0.z, r.c0.w, r.c1.x, r.c1.y, r.c1.z, r.c1.w};
+        float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            d0 = fmaf(sb(cw[i], 0), a[4 * i], d0);
+            d1 = fmaf(sb(cw[i], 1), a[4 * i + 1], d1);
+            d0 = fmaf(sb(cw[i], 2), a[4 * i + 2], d0);
+            d1 = fmaf(sb(cw[i], 3), a[4 * i + 3], d1);
+        }
+        return f16_bits_to_f32(r.d) * (d0 + d1);
+    } else {
+        float d0 = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 4; t++) {
+            float v[8];
+            dequant8<FMT>(w.B, w.p, r.task + t, v);
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                d0 = fmaf(v[i], a[8 * t + i], d0);
+        }
+        return d0;
+    }
+}
+
+template <int FMT, int R>
+__global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint16_t *__restrict__ X,
+                                                      const int32_t *__restrict__ ids, float *__restrict__ H, int E, int k,
+                                                      int64_t F, int act)
+{
+    __shared__ float part[8][2 * R];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, KS = blockDim.x >> 6;
+    const int pair = blockIdx.y, t = pair / k;
+    const int e = ids[pair];
+    if (e < 0 || e >= E)
+        return;  // no expert: H of the pair is never read
+    const int64_t f0 = (int64_t)blockIdx.x * R, row0 = (int64_t)e * F;
+    const int C = (int)(wg.K / 32);
+    float v[2 * R];
+#pragma unroll
+    for (int i = 0; i < 2 * R; i++)
+        v[i] = 0.0f;
+    for (int c0 = wave * 64; c0 < C; c0 += KS * 64) {
+        const bool live = c0 + lane < C;
+        const int c = live ? c0 + lane : C - 1;  // lanes past the row: a zero activation
+        const uint4 *xp = reinterpret_cast<const uint4 *>(X + (int64_t)t * wg.K + 32 * (int64_t)c);
+        uint4 xq[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            xq[i] = xp[i];
+        Raw<FMT> g[R], u[R];
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            const int64_t n = row0 + (f0 + r < F ? f0 + r : F - 1);
+            load_raw<FMT>(wg, n, c, lane, g[r]);
+            load_raw<FMT>(wu, n, c, lane, u[r]);
+        }
+        float a[32], asum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const uint32_t w[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                a[8 * i + 2 * j] = live ? bf16_lo(w[j]) : 0.0f;
+                a[8 * i + 2 * j + 1] = live ? bf16_hi(w[j]) : 0.0f;
+            }
+        }
+        if (FMT == FMT_Q4K) {
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                asum += a[i];
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++) {
+            v[2 * r] += dot32<FMT>(wg, g[r], c, a, asum);
+            v[2 * r + 1] += dot32<FMT>(wu, u[r], c, a, asum);
+        }
+    }
+    const float tot = wave_sums<2 * R>(v, lane);
+    if (lane < 2 * R)
+        part[wave][sum_index<2 * R>(lane)] = tot;
+    __syncthreads();
+    if (threadIdx.x < R && f0 + threadIdx.x < F) {
+        float gs = 0.0f, us = 0.0f;
+        for (int w = 0; w < KS; w++) {
+            gs += part[w][2 * threadIdx.x];
+            us += part[w][2 * threadIdx.x + 1];
+        }
+        H[(int64_t)pair * F + f0 + threadIdx.x] = act_f32(act, gs) * us;
+    }
+}
+
+template <int FMT, int R>
+__global__ __launch_bounds__(1024) void moe_down_kernel(Mat wd, const float *__restrict__ H,
+                                                        const int32_t *__restrict__ ids, const float *__restrict__ weights,
+                                                        float *__restrict__ Y, int E, int k, int64_t K)
+{
+    __shared__ float part[16][R];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, KS = blockDim.x >> 6;
+    const int t = blockIdx.y;
+    const int64_t n0 = (int64_t)blockIdx.x * R;
+    const int CF = (int)(wd.K / 32), items = k * CF;
+    float v[R];
+#pragma unroll
+    for (int i = 0; i < R; i++)
+        v[i] = 0.0f;
+    for (int i0 = wave * 64; i0 < items; i0 += KS * 64) {
+        const int it = min(i0 + lane, items - 1);
+        const int slot = it / CF, c = it - slot * CF;
+        int e = ids[t * k + slot];
+        const bool live = i0 + lane < items && e >= 0 && e < E;
+        const float wt = live ? weights[t * k + slot] : 0.0f;
+        e = live ? e : 0;
+        Raw<FMT> w[R];
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            load_raw<FMT>(wd, (int64_t)e * K + (n0 + r < K ? n0 + r : K - 1), c, lane, w[r]);
+        // H of a choice without an expert was never written
+        const float4 *hp = reinterpret_cast<const float4 *>(H + ((int64_t)t * k + slot) * wd.K + 32 * (int64_t)c);
+        float a[32], asum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            const float4 q = live ? hp[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            a[4 * i] = q.x, a[4 * i + 1] = q.y, a[4 * i + 2] = q.z, a[4 * i + 3] = q.w;
+        }
+        if (FMT == FMT_Q4K) {
+#pragma unroll
+            for (int i = 0; i < 32; i++)
+                asum += a[i];
+        }
+#pragma unroll
+        for (int r = 0; r < R; r++)
+            v[r] = fmaf(wt, dot32<FMT>(wd, w[r], c, a, asum), v[r]);
+    }
+    const float tot = wave_sums<R>(v, lane);
+    if (lane < R)
+        part[wave][sum_index<R>(lane)] = tot;
+    __syncthreads();
+    if (threadIdx.x < R && n0 + threadIdx.x < K) {
+        float s = 0.0f;
+        for (int w = 0; w < KS; w++)
+            s += part[w][threadIdx.x];
+        Y[(int64_t)t * K + n0 + threadIdx.x] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// More tokens: sort the pairs by expert.  One workgroup; counts and cursors
+// in LDS.  The order of an expert's pairs varies from run to run, but a
+// pair's results do not depend on its place.
+// ---------------------------------------------------------------------------
+struct Plan {
+    int32_t *tiles;   // [4]: number of tiles; then {expert, first, count, 0} per tile
+    int32_t *pair;    // sorted place -> pair
+    int32_t *place;   // pair -> sorted place, -1 without an expert
+};
+constexpr int MAXE = 1024;
+
+__global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *__restrict__ ids, int P, int E, int BM, Plan pl)
+{
+    __shared__ int cnt[MAXE], off[MAXE], til[MAXE], scan[2][1024];
+    const int tid = threadIdx.x;
+    cnt[tid] = 0;
+    __syncthreads();
+    for (int p = tid; p < P; p += 1024) {
+        const int e = ids[p];
+        if (e >= 0 && e < E)
+            atomicAdd(&cnt[e], 1);
+    }
+    __syncthreads();
+    // inclusive scans of the counts and of the tile counts
+    const int c = cnt[tid], nt = (c + BM - 1) / BM;
+    scan[0][tid] = c;
+    scan[1][tid] = nt;
+    __syncthreads();
+    for (int s = 1; s < 1024; s <<= 1) {
+        const int a = tid >= s ? scan[0][tid - s] : 0, b = tid >= s ? scan[1][tid - s] : 0;
+        __syncthreads();
+        scan[0][tid] += a;
+        scan[1][tid] += b;
+        __syncthreads();
+    }
+    off[tid] = scan[0][tid] - c;
+    til[tid] = scan[1][tid] - nt;
+    if (tid == 1023)
+        pl.tiles[0] = scan[1][tid];
+    cnt[tid] = 0;
+    int4 *tl = reinterpret_cast<int4 *>(pl.tiles + 4);
+    for (int i = 0; i < nt; i++)
+        tl[til[tid] + i] = make_int4(tid, off[tid] + i * BM, min(BM, c - i * BM), 0);
+    __syncthreads();
+    for (int p = tid; p < P; p += 1024) {
+        const int e = ids[p];
+        int at = -1;
+        if (e >= 0 && e < E) {
+            at = off[e] + atomicAdd(&cnt[e], 1);
+            pl.pair[at] = p;
+        }
+        pl.place[p] = at;
+    }
+}
+
+// Y[t] = sum_j w[t][j] * P[place of (t, j)], in the order of j
+__global__ __launch_bounds__(256) void moe_join_kernel(const float *__restrict__ Pd, const int32_t *__restrict__ place,
+                                                       const float *__restrict__ weights, float *__restrict__ Y, int k,
+                                                       int64_t K)
+{
+    const int t = blockIdx.x;
+    const int64_t n = ((int64_t)blockIdx.y * 256 + threadIdx.x) * 4;
+    if (n >= K)
+        return;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < k; j++) {
+        const int at = place[(int64_t)t * k + j];
+        if (at < 0)
+            continue;
+        const float w = weights[(int64_t)t * k + j];
+        const float4 v = *reinterpret_cast<const float4 *>(Pd + (int64_t)at * K + n);
+        s.x = fmaf(w, v.x, s.x);
+        s.y = fmaf(w, v.y, s.y);
+        s.z = fmaf(w, v.z, s.z);
+        s.w = fmaf(w, v.w, s.w);
+    }
+    *reinterpret_cast<float4 *>(Y + (int64_t)t * K + n) = s;
+}
+
+// ---------------------------------------------------------------------------
+// Grouped matrix-core products.  A workgroup of four waves takes one tile of
+// up to 16 TM pairs of an expert and 64 NT rows of its weights; the pairs'
+// activations are staged in LDS in slabs of 128 (double buffered) and shared
+// by the waves.  Lane (g, r) decodes block 4 s + g of its rows in slab s
+// (dequant8, exact in fp32) and feeds four v_mfma_f32_16x16x32_bf16 steps
+// whose k order inside the slab is the same on both operands.  Each fp32
+// value enters as a bf16 pair hi + lo (16 bits of it): weights as hi and lo,
+// X is bf16 already, H as hi and lo, dropping lo * lo; error at most about
+// 2^-16 of sum |w||x|.
+// ---------------------------------------------------------------------------
+constexpr int SLAB = 128, PITCH = 2 * SLAB + 16;
+
+__device__ __forceinline__ void split_bf16(float a, float b, uint32_t &hi, uint32_t &lo)
+{
+    typedef __bf16 b2 __attribute__((ext_vector_type(2)));
+    const b2 h = {(__bf16)a, (__bf16)b};
+    hi = __builtin_bit_cast(uint32_t, h);
+    const b2 l = {(__bf16)(a - (float)h.x), (__bf16)(b - (float)h.y)};
+    lo = __builtin_bit_cast(uint32_t, l);
+}
+
+// GLU: X rows are gathered by pair, rows i < NT / 2 of a wave's row tiles are
+// gate rows and the others the same rows of up; writes H hi / lo.  Otherwise:
+// A = H by sorted place, writes Pd.
+template <int FMT, int TM, int NT, bool GLU>
+__global__ __launch_bounds__(256) void moe_gemm_kernel(Mat w0, Mat w1, const uint16_t *__restrict__ A,
+                                                       const uint16_t *__restrict__ Alo, Plan pl, int k, int64_t N, int act,
+                                                       uint16_t *__restrict__ Hhi, uint16_t *__restrict__ Hlo,
+                                                       float *__restrict__ Pd)
+{
+    constexpr int BM = 16 * TM, PL = GLU ? 1 : 2;  // planes of A
+    constexpr int NF = GLU ? NT / 2 : NT;          // row tiles of outputs per wave
+    static_assert(!GLU || NT % 2 == 0, "gate and up tiles");
+    __shared__ __attribute__((aligned(16))) uint8_t sX[2][PL][BM * PITCH];
+    if ((int)blockIdx.x >= pl.tiles[0])
+        return;
+    const int4 tile = reinterpret_cast<const int4 *>(pl.tiles + 4)[blockIdx.x];
+    const int expert = tile.x, first = tile.y, count = tile.z;
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int g = lane >> 4, r16 = lane & 15;
+    const int64_t K = w0.K, n_wave = (int64_t)blockIdx.y * (64 * NF) + wave * 16 * NF;
+    const int nslab = (int)((K + SLAB - 1) / SLAB);
+    const int blocks = (int)(K / 32);
+    int64_t wpiece[NT];
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+        wpiece[i] = ((int64_t)expert * N + min(n_wave + 16 * (i % NF) + r16, N - 1)) * (K / 8);
+    // rows of A this thread stages: 16 pieces of 8 per row and slab
+    int64_t arow[TM];
+    bool alive[TM];
+#pragma unroll
+    for (int t = 0; t < TM; t++) {
+        const int row = (tid + 256 * t) / 16;
+        alive[t] = row < count;
+        const int at = first + (alive[t] ? row : 0);
+        arow[t] = GLU ? (int64_t)(pl.pair[at] / k) : at;
+    }
+    const int q8 = 8 * (tid & 15);
+    uint4 xr[PL][TM];
+    auto load_x = [&](int s) {
+#pragma unroll
+        for (int t = 0; t < TM; t++) {
+            const bool in = alive[t] && s * SLAB + q8 < K;
+#pragma unroll
+            for (int p = 0; p < PL; p++)
+                xr[p][t] = in ? *reinterpret_cast<const uint4 *>((p ? Alo : A) + arow[t] * K + s * SLAB + q8)
+                              : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto store_x = [&](int buf) {
+#pragma unroll
+        for (int t = 0; t < TM; t++)
+#pragma unroll
+            for (int p = 0; p < PL; p++)
+                *reinterpret_cast<uint4 *>(&sX[buf][p][((tid + 256 * t) / 16) * PITCH + 2 * q8]) = xr[p][t];
+    };
+    f32x4_t acc[NT][TM];
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+            acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    load_x(0);
+    store_x(0);
+    if (nslab > 1)
+        load_x(1);
+    lds_barrier();
+    for (int s = 0; s < nslab; s++) {
+        const int buf = s & 1;
+        const int blk = min(4 * s + g, blocks - 1);  // past the row: the A operand is zero
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            const Mat &w = GLU && i >= NF ? w1 : w0;
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                float v[8];
+                dequant8<FMT>(w.B, w.p, wpiece[i] + 4 * blk + t, v);
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    split_bf16(v[2 * e], v[2 * e + 1], h[e], l[e]);
+                const bf16x8_t bh = __builtin_bit_cast(bf16x8_t, make_uint4(h[0], h[1], h[2], h[3]));
+                const bf16x8_t bl = __builtin_bit_cast(bf16x8_t, make_uint4(l[0], l[1], l[2], l[3]));
+#pragma unroll
+                for (int j = 0; j < TM; j++) {
+                    const int at = (16 * j + r16) * PITCH + 64 * g + 16 * t;
+                    const bf16x8_t xh = *reinterpret_cast<const bf16x8_t *>(&sX[buf][0][at]);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bh, xh, acc[i][j], 0, 0, 0);
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bl, xh, acc[i][j], 0, 0, 0);
+                    if constexpr (!GLU) {
+                        const bf16x8_t xl = *reinterpret_cast<const bf16x8_t *>(&sX[buf][PL - 1][at]);
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bh, xl, acc[i][j], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        if (s + 1 < nslab) {
+            store_x(buf ^ 1);
+            if (s + 2 < nslab)
+                load_x(s + 2);
+        }
+        lds_barrier();
+    }
+    // lane holds D[row 4 g + i][pair r16] of each 16 x 16 tile: four
+    // consecutive outputs of one pair (N is a multiple of 32, so all or none exist)
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+        const int m = 16 * j + r16;
+        if (m >= count)
+            continue;
+        const int64_t at = (int64_t)(first + m) * N;
+#pragma unroll
+        for (int i = 0; i < NF; i++) {
+            const int64_t n = n_wave + 16 * i + 4 * g;
+            if (n >= N)
+                continue;
+            if constexpr (GLU) {
+                float h[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    h[e] = act_f32(act, acc[i][j][e]) * acc[i + NF][j][e];
+                uint2 hi, lo;
+                split_bf16(h[0], h[1], hi.x, lo.x);
+                split_bf16(h[2], h[3], hi.y, lo.y);
+                *reinterpret_cast<uint2 *>(Hhi + at + n) = hi;
+                *reinterpret_cast<uint2 *>(Hlo + at + n) = lo;
+            } else {
+                *reinterpret_cast<float4 *>(Pd + at + n) = make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+// Few tokens: up to four, where the chosen experts hardly repeat.
+bool few(int T) { return T <= 4; }
+
+// Workspace, few tokens: H fp32 [T k][F].  Otherwise, P = T k pairs:
+// H hi, H lo bf16 [P][F], Pd fp32 [P][K], the plan.
+struct Layout {
+    int64_t hlo, pd, tiles, pair, place, total;
+};
+Layout layout_of(int T, int E, int k, int64_t F, int64_t K)
+{
+    const int64_t P = (int64_t)T * k;
+    Layout l{};
+    if (few(T)) {
+        l.total = up16(4 * P * F);
+        return l;
+    }
+    const int64_t most = P / 16 + (P < E ? P : E) + 1;
+    l.hlo = up16(2 * P * F);
+    l.pd = l.hlo + up16(2 * P * F);
+    l.tiles = l.pd + 4 * P * K;
+    l.pair = l.tiles + 16 * (1 + most);
+    l.place = l.pair + up16(4 * P);
+    l.total = l.place + up16(4 * P);
+    return l;
+}
+
+template <int FMT>
+hipError_t glu_few(const MoeArgs &a, float *H, hipStream_t s)
+{
+    const Mat wg{a.gate, planes_of(FMT, a.E * a.F, a.K), a.K}, wu{a.up, wg.p, a.K};
+    const int C = (int)(a.K / 32), KS = C > 7 * 64 ? 8 : (C + 63) / 64;
+    constexpr int R = 4;
+    moe_glu_kernel<FMT, R><<<dim3((unsigned)((a.F + R - 1) / R), a.T * a.k), 64 * KS, 0, s>>>(wg, wu, a.X, a.ids, H, a.E,
+                                                                                             a.k, a.F, a.act);
+    return hipGetLastError();
+}
+
+template <int FMT>
+hipError_t down_few(const MoeArgs &a, const float *H, hipStream_t s)
+{
+    const Mat wd{a.down, planes_of(FMT, a.E * a.K, a.F), a.F};
+    const int64_t items = a.k * (a.F / 32);
+    const int KS = items > 15 * 64 ? 16 : (int)((items + 63) / 64);
+    constexpr int R = 4;
+    moe_down_kernel<FMT, R><<<dim3((unsigned)((a.K + R - 1) / R), a.T), 64 * KS, 0, s>>>(wd, H, a.ids, a.weights, a.Y, a.E,
+                                                                                        a.k, a.K);
+    return hipGetLastError();
+}
+
+template <int FMT, int TM, int NT, bool GLU>
+hipError_t gemm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, hipStream_t s)
+{
+    uint16_t *hhi = reinterpret_cast<uint16_t *>(a.ws), *hlo = reinterpret_cast<uint16_t *>(a.ws + l.hlo);
+    float *pd = reinterpret_cast<float *>(a.ws + l.pd);
+    const int64_t N = GLU ? a.F : a.K, K = GLU ? a.K : a.F, per = 64 * (GLU ? NT / 2 : NT);
+    const Planes p = planes_of(FMT, a.E * N, K);
+    const Mat w0{GLU ? a.gate : a.down, p, K}, w1{GLU ? a.up : a.down, p, K};
+    moe_gemm_kernel<FMT, TM, NT, GLU><<<dim3(max_tiles, (unsigned)((N + per - 1) / per)), 256, 0, s>>>(
+        w0, w1, GLU ? a.X : hhi, hlo, pl, a.k, N, a.act, hhi, hlo, pd);
+    return hipGetLastError();
+}
+
+template <int FMT, bool GLU>
+hipError_t gemm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, int max_tiles, hipStream_t s)
+{
+    if (tm == 1)
+        return gemm<FMT, 1, 2, GLU>(a, l, pl, max_tiles, s);
+    if (tm == 2)
+        return gemm<FMT, 2, 2, GLU>(a, l, pl, max_tiles, s);
+    return gemm<FMT, 4, 2, GLU>(a, l, pl, max_tiles, s);
+}
+
+#define QL_EACH_FMT(X)                                                                                               \
+    X(FMT_Q8_0) X(FMT_Q4K) X(FMT_Q6K) X(FMT_Q2K) X(FMT_Q3K) X(FMT_Q5K) X(FMT_Q4_0) X(FMT_Q4_1) X(FMT_Q5_0) X(FMT_Q5_1) \
+        X(FMT_FP8)
+
+}  // namespace
+
+int64_t moe_workspace(int T, int E, int k, int64_t F, int64_t K) { return layout_of(T, E, k, F, K).total; }
+
+hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
+{
+    const Layout l = layout_of(a.T, a.E, a.k, a.F, a.K);
+    hipError_t e = hipErrorNotSupported;
+    if (few(a.T)) {
+        float *H = reinterpret_cast<float *>(a.ws);
+        switch (a.fmt_gu) {
+#define X(f) case f: e = glu_few<f>(a, H, s); break;
+            QL_EACH_FMT(X)
+#undef X
+        }
+        if (e != hipSuccess)
+            return e;
+        switch (a.fmt_d) {
+#define X(f) case f: return down_few<f>(a, H, s);
+            QL_EACH_FMT(X)
+#undef X
+        }
+        return hipErrorNotSupported;
+    }
+    const int P = a.T * a.k;
+    // tokens per tile: the expected number of an expert's pairs
+    const int per = P / a.E, tm = per <= 16 ? 1 : per <= 32 ? 2 : 4, BM = 16 * tm;
+    const int max_tiles = P / BM + (P < a.E ? P : a.E);
+    const Plan pl{reinterpret_cast<int32_t *>(a.ws + l.tiles), reinterpret_cast<int32_t *>(a.ws + l.pair),
+                  reinterpret_cast<int32_t *>(a.ws + l.place)};
+    moe_plan_kernel<<<1, 1024, 0, s>>>(a.ids, P, a.E, BM, pl);
+    if ((e = hipGetLastError()) != hipSuccess)
+        return e;
+    e = hipErrorNotSupported;
+    switch (a.fmt_gu) {
+#define X(f) case f: e = gemm_tm<f, true>(a, l, pl, tm, max_tiles, s); break;
+        QL_EACH_FMT(X)
+#undef X
+    }
+    if (e != hipSuccess)
+        return e;
+    e = hipErrorNotSupported;
+    switch (a.fmt_d) {
+#define X(f) case f: e = gemm_tm<f, false>(a, l, pl, tm, max_tiles, s); break;
+        QL_EACH_FMT(X)
+#undef X
+    }
+    if (e != hipSuccess)
+        return e;
+    moe_join_kernel<<<dim3(a.T, (unsigned)((a.K + 1023) / 1024)), 256, 0, s>>>(
+        reinterpret_cast<const float *>(a.ws + l.pd), pl.place, a.weights, a.Y, a.k, a.K);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_route(const float *logits, int T, int E, int k, int score, const float *bias, int renorm,
+                            float scale, int32_t *ids, float *weights, hipStream_t s)
+{
+    const unsigned grid = (unsigned)((T + 3) / 4);
+#define ROUTE(V)                                                                                                     \
+    if (E <= 64 * V) {                                                                                               \
+        if (bias)                                                                                                    \
+            moe_route_kernel<V, true><<<grid, 256, 0, s>>>(logits, T, E, k, score, bias, renorm, scale, ids, weights);  \
+        else                                                                                                         \
+            moe_route_kernel<V, false><<<grid, 256, 0, s>>>(logits, T, E, k, score, bias, renorm, scale, ids, weights); \
+        return hipGetLastError();                                                                                    \
+    }
+    ROUTE(1) ROUTE(2) ROUTE(4) ROUTE(8) ROUTE(16)
+#undef ROUTE
+    return hipErrorNotSupported;
+}
+
+}  // namespace ql

@@ -239,6 +239,89 @@ int qmatmul_glu(int fmt, const void *gate_blocks, const void *up_blocks, const v
                 int64_t M, int64_t F, int64_t K, int act, void *workspace, size_t workspace_bytes,
                 void *stream);
 
+/* Router of a mixture-of-experts layer: each token's experts and their
+ * weights from the router's logits.
+ * logits: device fp32 [T][E] (for instance qmatmul of a quantized router).
+ * Scores p: QSCORE_SOFTMAX over the row's experts, or QSCORE_SIGMOID of each.
+ * The top_k experts of a token are those of the largest logits or, with
+ * `bias` (device fp32 [E] or NULL; QSCORE_SIGMOID only), of the largest
+ * p + bias, formed in fp64 (in fp32 the rounding of the sigmoid would choose
+ * between close experts); ties go to the lower expert.  The bias takes part
+ * in the choice only.  ids: device int32 [T][top_k], in the order of choice.
+ * weights: device fp32 [T][top_k], p of the chosen, divided by their sum when
+ * renorm != 0, times `scale`.
+ * A logit of -inf (or NaN) switches an expert off for that token: it is
+ * never chosen and adds nothing to the softmax.  Where fewer than top_k are
+ * left the last ids are -1 with weight 0.  +inf counts as the largest finite
+ * value.  All pointers 4-byte aligned.  T == 0 launches nothing. */
+enum { QSCORE_SOFTMAX = 0, QSCORE_SIGMOID = 1 };
+#define QLINEAR_MAX_EXPERTS 1024
+#define QLINEAR_MAX_TOP_K 32
+int q_moe_route(const float *logits, int64_t T, int64_t E, int top_k, int score, const float *bias, int renorm,
+                float scale, int32_t *ids, float *weights, void *stream);
+
+/* Mixture-of-experts layer on block-quantized expert weights (gated
+ * projections as in qmatmul_glu, chosen per token):
+ *   Y[t] = sum_j weights[t][j] * Wd[e] . (act(Wg[e] . x_t) * (Wu[e] . x_t)),
+ *   e = ids[t][j], j = 0 .. top_k - 1.
+ * gate_blocks / up_blocks: device, isq_quantize(fmt_gate_up, W, E*F, K) of
+ * the experts' [F][K] weights stacked along the rows (expert e: rows e*F ..
+ * e*F + F - 1); down_blocks: isq_quantize(fmt_down, W, E*K, F) of the stacked
+ * [K][F] weights.  K and F are row lengths and follow their format's rule (a
+ * multiple of 256; Q8_0: of 32).  X_bf16: device [T][K].  ids: device int32
+ * [T][top_k]; an id outside [0, E) stands for no expert and adds nothing (a
+ * token without any gives a row of zeros), the same expert twice counts
+ * twice.  weights: device fp32 [T][top_k].  Y_fp32: device [T][K],
+ * overwritten.  act as in qmatmul_glu.  ids and weights 4-byte aligned.
+ * The products between the two weights stay in fp32 for up to four tokens;
+ * for more they enter the second product as a pair of bf16 values (16
+ * significant bits).  Accuracy: within 1e-3 of the magnitudes summed, as
+ * qmatmul.  Results do not depend on the order in which workgroups run.
+ * workspace: device, qmatmul_moe_workspace_bytes() bytes, 16-byte aligned,
+ * overwritten (nothing in it needs to start at zero); calls that can overlap
+ * in time need one each.  T == 0 launches nothing; 0 <= T <= QLINEAR_MAX_M. */
+size_t qmatmul_moe_workspace_bytes(int fmt_gate_up, int fmt_down, int64_t T, int64_t E, int top_k, int64_t F, int64_t K);
+int qmatmul_moe(int fmt_gate_up, const void *gate_blocks, const void *up_blocks, int fmt_down, const void *down_blocks,
+                const void *X_bf16, const int32_t *ids, const float *weights, float *Y_fp32, int64_t T, int64_t E,
+                int top_k, int64_t F, int64_t K, int act, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Log probabilities of given tokens from an output head's logits, with each
+ * row's entropy and top alternatives, in one pass over the logits.
+ * logits: device fp32, M rows of V, ld >= V elements apart, 4-byte aligned.
+ * For a row x, lse = ln sum e^x:
+ *   logprob[m] = x[targets[m]] - lse (0 for a target outside [0, V): a row
+ *     whose token is not scored);
+ *   rank[m] = 1 + the number of logits above x[targets[m]] (0 likewise);
+ *   entropy[m] = -sum p ln p (natural logarithm);
+ *   top_ids[m][i], top_logprobs[m][i], i < top_n: the largest logits in
+ *     falling order, ties to the lower index, and their x - lse.
+ * Any of logprob, rank, entropy may be NULL (not wanted), and targets may be
+ * NULL where logprob and rank are; top_ids and top_logprobs are read only for
+ * top_n > 0.  A logit of -inf is a masked token: probability 0, log
+ * probability -inf, never an alternative; where fewer than top_n tokens are
+ * left the last ids are -1 with -inf.  A row with none left has entropy 0.
+ * NaN and +inf break the precondition: the row's values are unspecified, its
+ * top_ids stay within [-1, V).  workspace: device,
+ * q_logprobs_workspace_bytes() bytes (0: may be NULL), 16-byte aligned,
+ * overwritten; calls that can overlap in time need one each.  0 <= M <=
+ * QLINEAR_MAX_M, 1 <= V <= QLINEAR_MAX_N, 0 <= top_n <= QLINEAR_MAX_TOP_N;
+ * M == 0 launches nothing. */
+#define QLINEAR_MAX_TOP_N 64
+size_t q_logprobs_workspace_bytes(int64_t M, int64_t V, int top_n);
+int q_logprobs(const float *logits, int64_t M, int64_t V, int64_t ld, const int32_t *targets, int top_n, float *logprob,
+               int32_t *rank, float *entropy, int32_t *top_ids, float *top_logprobs, void *workspace,
+               size_t workspace_bytes, void *stream);
+
+/* The same for the logits X . deq(W)^T of a quantized output head, without
+ * holding them: rows go through qmatmul (AUTO path) and q_logprobs in chunks
+ * whose logits (at most 2^26, or one row) stay in the workspace.  blocks,
+ * X_bf16, N, K as in qmatmul (the [N][K] head), the rest as in q_logprobs
+ * with V = N.  The workspace is always needed for M > 0. */
+size_t qmatmul_logprobs_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int top_n);
+int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M, int64_t N, int64_t K,
+                     const int32_t *targets, int top_n, float *logprob, int32_t *rank, float *entropy, int32_t *top_ids,
+                     float *top_logprobs, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Quantized embedding lookup (page "Quantization types", section
  * "Sensitive tensor precision": token embeddings are stored quantized, and
  * a tied output head reuses the embedding instead of a second copy -- the
