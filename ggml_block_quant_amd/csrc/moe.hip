@@ -39,32 +39,37 @@ __device__ __forceinline__ float dpp(float v)
 // Sums of V values over the 64 lanes (V a power of two <= 64): while more
 // than one is left a step keeps half of them, so V values cost about V + 4
 // additions.  Lanes 0 .. V-1 end with the total of value sum_index<V>(lane).
+// Step B pairs lanes that differ in bit B.
+template <int B>
+__device__ __forceinline__ float partner(float x)
+{
+    if constexpr (B == 0)
+        return dpp<0xB1>(x);
+    else if constexpr (B == 1)
+        return dpp<0x4E>(x);
+    else
+        return __shfl_xor(x, 1 << B);
+}
+template <int LEFT, int B, int V>
+__device__ __forceinline__ void sum_step(float (&v)[V], int lane)
+{
+    if constexpr (LEFT > 1) {
+        const bool up = (lane >> B) & 1;
+#pragma unroll
+        for (int i = 0; i < LEFT / 2; i++) {
+            const float keep = up ? v[i + LEFT / 2] : v[i], send = up ? v[i] : v[i + LEFT / 2];
+            v[i] = keep + partner<B>(send);
+        }
+    } else {
+        v[0] += partner<B>(v[0]);
+    }
+    if constexpr (B < 5)
+        sum_step<(LEFT > 1 ? LEFT / 2 : 1), B + 1>(v, lane);
+}
 template <int V>
 __device__ __forceinline__ float wave_sums(float (&v)[V], int lane)
 {
-    int left = V;
-#pragma unroll
-    for (int b = 0; b < 6; b++) {
-        auto partner = [&](float x) {
-            if (b == 0)
-                return dpp<0xB1>(x);  // lane ^ 1
-            if (b == 1)
-                return dpp<0x4E>(x);  // lane ^ 2
-            return __shfl_xor(x, 1 << b);
-        };
-        if (left > 1) {
-            left /= 2;
-            const bool up = (lane >> b) & 1;
-#pragma unroll
-            for (int i = 0; i < V; i++)
-                if (i < left) {
-                    const float keep = up ? v[i + left] : v[i], send = up ? v[i] : v[i + left];
-                    v[i] = keep + partner(send);
-                }
-        } else {
-            v[0] += partner(v[0]);
-        }
-    }
+    sum_step<V, 0>(v, lane);
     return v[0];
 }
 template <int V>
@@ -192,12 +197,16 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const float *__restrict_
 
 // ---------------------------------------------------------------------------
 // Few tokens.  A row of K weights is cut into chunks of 32; a lane owns a
-// chunk of the row, keeps its 32 activations in registers (fp32: exact for
-// bf16 X, and H is never rounded to fewer bits) and walks down R rows, all of
-// whose loads are issued before the first is used.  Per row it forms
-// sum q * a of the codes and applies the block scales once, so only fp32
-// sums round; the lanes' sums are joined by wave_sums and, where a row takes
-// several waves, through LDS.
+// chunk of the row, keeps its 32 activations in registers and walks down the
+// workgroup's rows, R at a time: the loads of the next R rows are issued
+// before the current ones are used, so a wave always has R to 2 R rows of
+// loads in flight and the activations are read once for all of them.  Per row
+// a lane forms sum q * a of its chunk and applies the block scales once, so
+// only fp32 sums round; the lanes' sums are joined by wave_sums and, where a
+// row takes several waves, through LDS.
+// Activations: bf16 X of Q4K weights stays in bf16 pairs for v_dot2_f32_bf16
+// (the 4-bit codes are exact in bf16); otherwise they are fp32, which holds
+// bf16 X exactly and does not round H.
 // ---------------------------------------------------------------------------
 struct Mat {
     const uint8_t *B;
@@ -216,34 +225,73 @@ __device__ __forceinline__ uint4 stream16(const uint8_t *p)
     return make_uint4(v.x, v.y, v.z, v.w);
 }
 
-// chunk c of row n; the lanes of a quad hold chunks of one group of 256
+// Where a lane's chunk c of row n lies; row n + i is i row strides on.  The
+// lanes of a quad hold chunks of one group of 256.
+template <int FMT> struct At {
+    const uint8_t *codes, *aux, *scales, *d;  // aux: Q6K's high bits
+    int64_t task;                             // the other formats
+};
+
 template <int FMT>
-__device__ __forceinline__ void load_raw(const Mat &w, int64_t n, int c, int lane, Raw<FMT> &r)
+__device__ __forceinline__ At<FMT> at_row(const Mat &w, int64_t n, int c, int lane)
 {
+    At<FMT> p{};
+    const int64_t sub = n * (w.K / 32) + c, g = sub >> 3;
     if constexpr (FMT == FMT_Q4K) {
-        const int64_t sub = n * (w.K / 32) + c;
-        r.c = stream16(w.B + 16 * sub);
+        p.codes = w.B + 16 * sub;
         // one dword of the 16-byte group header per lane, shared in the quad
-        r.h = *reinterpret_cast<const uint32_t *>(w.B + w.p.scales + 16 * (sub >> 3) + 4 * (lane & 3));
+        p.scales = w.B + w.p.scales + 16 * g + 4 * (lane & 3);
     } else if constexpr (FMT == FMT_Q6K) {
-        const int64_t g = n * (w.K / 256) + (c >> 3);
-        const int cc = c & 7;
-        r.lo = stream16(w.B + 192 * g + 16 * cc);
-        r.hi = *reinterpret_cast<const uint2 *>(w.B + 192 * g + 128 + 8 * cc);
-        r.sc2 = *reinterpret_cast<const uint16_t *>(w.B + w.p.scales + 16 * g + 2 * cc);
-        r.d = *reinterpret_cast<const uint16_t *>(w.B + w.p.d + 2 * g);
+        p.codes = w.B + 192 * g + 16 * (c & 7);
+        p.aux = w.B + 192 * g + 128 + 8 * (c & 7);
+        p.scales = w.B + w.p.scales + 16 * g + 2 * (c & 7);
+        p.d = w.B + w.p.d + 2 * g;
     } else if constexpr (FMT == FMT_Q8_0) {
-        const int64_t b = n * (w.K / 32) + c;
-        r.c0 = stream16(w.B + 32 * b);
-        r.c1 = stream16(w.B + 32 * b + 16);
-        r.d = *reinterpret_cast<const uint16_t *>(w.B + w.p.scales + 2 * b);
+        p.codes = w.B + 32 * sub;
+        p.d = w.B + w.p.scales + 2 * sub;
     } else {
-        r.task = 4 * (n * (w.K / 32) + c);
+        p.task = 4 * sub;
+    }
+    return p;
+}
+
+// the chunk `row` rows on
+template <int FMT>
+__device__ __forceinline__ void load_raw(const Mat &w, const At<FMT> &p, int64_t row, Raw<FMT> &r)
+{
+    const int64_t gs = row * (w.K / 256);  // groups (Q8_0 rows may end in a part of one)
+    if constexpr (FMT == FMT_Q4K) {
+        r.c = stream16(p.codes + 128 * gs);
+        r.h = *reinterpret_cast<const uint32_t *>(p.scales + 16 * gs);
+    } else if constexpr (FMT == FMT_Q6K) {
+        r.lo = stream16(p.codes + 192 * gs);
+        r.hi = *reinterpret_cast<const uint2 *>(p.aux + 192 * gs);
+        r.sc2 = *reinterpret_cast<const uint16_t *>(p.scales + 16 * gs);
+        r.d = *reinterpret_cast<const uint16_t *>(p.d + 2 * gs);
+    } else if constexpr (FMT == FMT_Q8_0) {
+        r.c0 = stream16(p.codes + row * w.K);
+        r.c1 = stream16(p.codes + row * w.K + 16);
+        r.d = *reinterpret_cast<const uint16_t *>(p.d + row * (w.K / 16));
+    } else {
+        r.task = p.task + row * (w.K / 8);
     }
 }
 
 __device__ __forceinline__ float ub(uint32_t w, int b) { return (float)((w >> (8 * b)) & 0xffu); }
 __device__ __forceinline__ float sb(uint32_t w, int b) { return (float)(int8_t)(w >> (8 * b)); }
+
+// Q6K: byte b of lo (hi): four times the signed code of elements 0, 4, 1, 5
+// (2, 6, 3, 7) of an octet: the low nibble at bits 2-5, the two high bits
+// above it, the top one flipped (u - 32 in two's complement).  H: the octet's
+// high bits at bits 0-7 (even elements) and 16-23 (odd ones).
+__device__ __forceinline__ void q6k_bytes(uint32_t lw, uint32_t H, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t H2 = H >> 2;
+    const uint32_t t0 = (H & 0x00030003u) | ((H & 0x00300030u) << 4);
+    const uint32_t t1 = (H2 & 0x00030003u) | ((H2 & 0x00300030u) << 4);
+    lo = (((lw << 2) & 0x3C3C3C3Cu) | (t0 << 6)) ^ 0x80808080u;
+    hi = (((lw >> 2) & 0x3C3C3C3Cu) | (t1 << 6)) ^ 0x80808080u;
+}
 
 // sum over the chunk of w * a; asum = sum of a over the chunk (Q4K's mins)
 template <int FMT>
@@ -282,14 +330,8 @@ __device__ __forceinline__ float dot32(const Mat &w, const Raw<FMT> &r, int c, c
         float s[2] = {0.0f, 0.0f};  // the two sub-blocks of 16, in units of a quarter
 #pragma unroll
         for (int q = 0; q < 4; q++) {
-            // byte b of lo (hi): four times the signed code of elements
-            // 0, 4, 1, 5 (2, 6, 3, 7): the low nibble at bits 2-5, the two
-            // high bits above it, the top one flipped (u - 32 in two's complement)
-            const uint32_t H = hw[q >> 1] >> (8 * (q & 1)), H2 = H >> 2;
-            const uint32_t t0 = (H & 0x00030003u) | ((H & 0x00300030u) << 4);
-            const uint32_t t1 = (H2 & 0x00030003u) | ((H2 & 0x00300030u) << 4);
-            const uint32_t lo = (((lw[q] << 2) & 0x3C3C3C3Cu) | (t0 << 6)) ^ 0x80808080u;
-            const uint32_t hi = (((lw[q] >> 2) & 0x3C3C3C3Cu) | (t1 << 6)) ^ 0x80808080u;
+            uint32_t lo, hi;
+            q6k_bytes(lw[q], hw[q >> 1] >> (8 * (q & 1)), lo, hi);
             const float *x = a + 8 * q;
             float v = s[q >> 1];
             v = fmaf(sb(lo, 0), x[0], v);
@@ -329,24 +371,213 @@ __device__ __forceinline__ float dot32(const Mat &w, const Raw<FMT> &r, int c, c
     }
 }
 
-template <int FMT, int R>
-__global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint16_t *__restrict__ X,
-                                                      const int32_t *__restrict__ ids, float *__restrict__ H, int E, int k,
-                                                      int64_t F, int act)
+// The activations of a chunk as the products take them.
+template <bool PAIRS> struct Acts;
+template <> struct Acts<true> {
+    uint32_t p[16];  // bf16 pairs (0,4), (1,5), (2,6), (3,7) of each octet
+    float sum;
+};
+template <> struct Acts<false> {
+    float a[32];
+    float sum;  // Q4K only
+};
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16v2_t;
+
+__device__ __forceinline__ float dot2(uint32_t a, uint32_t b, float c)
 {
-    __shared__ float part[8][2 * R];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, KS = blockDim.x >> 6;
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16v2_t, a), __builtin_bit_cast(bf16v2_t, b), c, false);
+}
+
+// bytes 2H, 2H + 1 of w, each 0 .. 15, as the bf16 pair of those numbers: as
+// an E4M3 byte u is u * 2^-9
+template <bool H>
+__device__ __forceinline__ uint32_t nib_pair(uint32_t w)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 512.0f, H));
+}
+
+// Q4K's scale and minimum of sub-block j from the quad's header dwords
+__device__ __forceinline__ void q4k_scales(uint32_t hd, int j, float &S, float &Mn)
+{
+    const int h = (int)hd;
+    const uint32_t h0 = __builtin_amdgcn_update_dpp(0, h, 0x00, 0xF, 0xF, false);
+    const uint32_t h1 = __builtin_amdgcn_update_dpp(0, h, 0x55, 0xF, 0xF, false);
+    const uint32_t h2 = __builtin_amdgcn_update_dpp(0, h, 0xAA, 0xF, 0xF, false);
+    const uint32_t h3 = __builtin_amdgcn_update_dpp(0, h, 0xFF, 0xF, 0xF, false);
+    const uint32_t sc = __builtin_amdgcn_ubfe(h1, 4 * j, 4) | (__builtin_amdgcn_ubfe(h3, 2 * j, 2) << 4);
+    const uint32_t mq = __builtin_amdgcn_ubfe(h2, 4 * j, 4) | (__builtin_amdgcn_ubfe(h3, 16 + 2 * j, 2) << 4);
+    S = f16_bits_to_f32(h0) * (float)sc;
+    Mn = f16_bits_to_f32(h0 >> 16) * (float)mq;
+}
+
+template <int FMT, bool PAIRS>
+__device__ __forceinline__ float dot(const Mat &w, const Raw<FMT> &r, int c, const Acts<PAIRS> &x)
+{
+    if constexpr (PAIRS) {
+        float S, Mn;
+        q4k_scales(r.h, c & 7, S, Mn);
+        const uint32_t cw[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+        float d0 = 0.0f, d1 = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint32_t lo = cw[q] & 0x0F0F0F0Fu, hi = (cw[q] >> 4) & 0x0F0F0F0Fu;
+            d0 = dot2(nib_pair<false>(lo), x.p[4 * q], d0);
+            d1 = dot2(nib_pair<true>(lo), x.p[4 * q + 1], d1);
+            d0 = dot2(nib_pair<false>(hi), x.p[4 * q + 2], d0);
+            d1 = dot2(nib_pair<true>(hi), x.p[4 * q + 3], d1);
+        }
+        return fmaf(S, d0 + d1, -Mn * x.sum);
+    } else {
+        return dot32<FMT>(w, r, c, x.a, x.sum);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// H between the two kernels.  For the tuned formats a chunk of 32 is stored
+// as whole numbers v = h * 2^e of 23 bits, e chosen per chunk, split into
+// three signed base-256 digits (v = 65536 d2 + 256 d1 + d0), because codes
+// are small whole numbers too: v_dot4_i32_i8 then takes four products an
+// instruction, exactly (24 instructions a chunk instead of 32 conversions
+// and 32 fused multiply-adds; Q4K 122 -> 65 VALU instructions a chunk in
+// all).  A value is held to 2^-23 of the largest of its chunk.  H8 is 7
+// 16-byte words a chunk: digits d0 (2), d1 (2), d2 (2), then {2^-e, sum of h}.
+// The bytes stand in the order in which the format's codes come out of their
+// dwords: Q8_0 as they are; Q4K and Q6K per octet 0, 4, 1, 5 (low nibbles),
+// 2, 6, 3, 7 (high nibbles).  The other formats take H in fp32.
+// ---------------------------------------------------------------------------
+__host__ __device__ constexpr bool digits_fmt(int fmt) { return fmt == FMT_Q4K || fmt == FMT_Q6K || fmt == FMT_Q8_0; }
+constexpr int HW = 7;  // 16-byte words per chunk
+
+// place of element i in the eo order of a chunk, in bytes
+__device__ __forceinline__ int eo_place(int i)
+{
+    const int o = i & 7;  // 0 4 1 5 2 6 3 7
+    return (i & 24) | ((o & 2) << 1) | ((o & 1) << 1) | (o >> 2);
+}
+
+// One value per lane, 32 lanes (one half of a wave) a chunk: writes the chunk
+// `out` (HW words).  All 32 lanes of the half take part.
+__device__ __forceinline__ void write_digits(float h, uint4 *__restrict__ out, bool eo)
+{
+    const int i = threadIdx.x & 31;
+    float m = fabsf(h), sum = h;
+#pragma unroll
+    for (int s = 1; s < 32; s <<= 1) {
+        m = fmaxf(m, __shfl_xor(m, s));
+        sum += __shfl_xor(sum, s);
+    }
+    int e = m > 0.0f ? 23 - __builtin_amdgcn_frexp_expf(m) : 0;  // m 2^e in [2^22, 2^23)
+    if (__builtin_amdgcn_ldexpf(m, e) > 8355711.0f)              // 127 (65536 + 256 + 1): the largest v
+        e--;
+    e = min(e, 126);  // keeps 2^-e normal (such a chunk is below 2^-103)
+    const int v = (int)rintf(__builtin_amdgcn_ldexpf(h, e));
+    const int d0 = (int8_t)v, v1 = (v - d0) >> 8, d1 = (int8_t)v1, d2 = (v1 - d1) >> 8;
+    int8_t *b = reinterpret_cast<int8_t *>(out) + (eo ? eo_place(i) : i);
+    b[0] = (int8_t)d0;
+    b[32] = (int8_t)d1;
+    b[64] = (int8_t)d2;
+    if (i == 0)
+        *reinterpret_cast<float2 *>(out + 6) = make_float2(__builtin_amdgcn_ldexpf(1.0f, -e), sum);
+}
+
+struct Digits {
+    uint32_t d[3][8];
+    float unit, sum;  // 2^-e and sum of h, both times the choice's weight
+};
+
+__device__ __forceinline__ int dot4(uint32_t a, uint32_t b, int c) { return __builtin_amdgcn_sdot4((int)a, (int)b, c, false); }
+
+// 65536 s2 + 256 s1 + s0: the first two exact (below 2^24), one rounding
+__device__ __forceinline__ float digit_sum(int s2, int s1, int s0) { return fmaf((float)((s2 << 8) + s1), 256.0f, (float)s0); }
+
+template <int FMT>
+__device__ __forceinline__ float dot(const Raw<FMT> &r, int c, const Digits &x)
+{
+    int s0 = 0, s1 = 0, s2 = 0;
+    if constexpr (FMT == FMT_Q4K) {
+        float S, Mn;
+        q4k_scales(r.h, c & 7, S, Mn);
+        const uint32_t cw[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            const uint32_t lo = cw[q] & 0x0F0F0F0Fu, hi = (cw[q] >> 4) & 0x0F0F0F0Fu;
+            s0 = dot4(lo, x.d[0][2 * q], s0), s0 = dot4(hi, x.d[0][2 * q + 1], s0);
+            s1 = dot4(lo, x.d[1][2 * q], s1), s1 = dot4(hi, x.d[1][2 * q + 1], s1);
+            s2 = dot4(lo, x.d[2][2 * q], s2), s2 = dot4(hi, x.d[2][2 * q + 1], s2);
+        }
+        return fmaf(S * x.unit, digit_sum(s2, s1, s0), -Mn * x.sum);
+    } else if constexpr (FMT == FMT_Q6K) {
+        const uint32_t lw[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
+        const uint32_t hw[2] = {r.hi.x, r.hi.y};
+        float t[2];
+#pragma unroll
+        for (int q = 0; q < 4; q++) {
+            uint32_t lo, hi;
+            q6k_bytes(lw[q], hw[q >> 1] >> (8 * (q & 1)), lo, hi);
+            if (q == 2)
+                t[0] = digit_sum(s2, s1, s0), s0 = s1 = s2 = 0;
+            s0 = dot4(lo, x.d[0][2 * q], s0), s0 = dot4(hi, x.d[0][2 * q + 1], s0);
+            s1 = dot4(lo, x.d[1][2 * q], s1), s1 = dot4(hi, x.d[1][2 * q + 1], s1);
+            s2 = dot4(lo, x.d[2][2 * q], s2), s2 = dot4(hi, x.d[2][2 * q + 1], s2);
+        }
+        t[1] = digit_sum(s2, s1, s0);
+        const float Sa = (float)(int8_t)r.sc2, Sb = (float)(int8_t)(r.sc2 >> 8);
+        return 0.25f * f16_bits_to_f32(r.d) * x.unit * fmaf(Sa, t[0], Sb * t[1]);
+    } else {
+        const uint32_t cw[8] = {r.c0.x, r.c0.y, r.c0.z, r.c0.w, r.c1.x, r.c1.y, r.c1.z, r.c1.w};
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            s0 = dot4(cw[i], x.d[0][i], s0);
+            s1 = dot4(cw[i], x.d[1][i], s1);
+            s2 = dot4(cw[i], x.d[2][i], s2);
+        }
+        return f16_bits_to_f32(r.d) * x.unit * digit_sum(s2, s1, s0);
+    }
+}
+
+constexpr int MAXG = 16;  // groups of R rows per workgroup
+
+// Groups 0 .. groups - 1 of R rows: `load(g, rows)` issues a group's loads,
+// `ready()` runs once they are out (the activations' set-up), `use(g, rows)`
+// consumes them while the next group's are in flight.
+template <typename RowsT, typename L, typename P, typename U>
+__device__ __forceinline__ void walk(int groups, L load, P ready, U use)
+{
+    RowsT a;
+    load(0, a);
+    ready();
+    for (int g = 0; g + 1 < groups; g++) {
+        RowsT b;
+        load(g + 1, b);
+        use(g, a);
+        a = b;
+    }
+    use(groups - 1, a);
+}
+
+// A workgroup computes the 32 values of one chunk of H: KS waves along a row
+// (each a chunk of the row per lane and pass) times RW waves of 32 / RW rows.
+// HMODE: 0 fp32, 1 digits in natural order, 2 digits in eo order.
+template <int FMT, int R, int HMODE>
+__global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint16_t *__restrict__ X,
+                                                       const int32_t *__restrict__ ids, void *__restrict__ H, int E, int k,
+                                                       int64_t F, int act, int KS)
+{
+    constexpr bool PAIRS = FMT == FMT_Q4K;
+    __shared__ float part[8][2 * 32];  // [wave along the row][row, gate and up], 32 rows
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int waves = blockDim.x >> 6, RW = waves / KS;
+    const int kw = wave % KS, rw = wave / KS, rows = 32 / RW, groups = rows / R;
     const int pair = blockIdx.y, t = pair / k;
     const int e = ids[pair];
     if (e < 0 || e >= E)
         return;  // no expert: H of the pair is never read
-    const int64_t f0 = (int64_t)blockIdx.x * R, row0 = (int64_t)e * F;
+    const int64_t f0 = (int64_t)blockIdx.x * 32;  // F is a multiple of 32
+    const int64_t row0 = (int64_t)e * F + f0 + rw * rows;
     const int C = (int)(wg.K / 32);
-    float v[2 * R];
-#pragma unroll
-    for (int i = 0; i < 2 * R; i++)
-        v[i] = 0.0f;
-    for (int c0 = wave * 64; c0 < C; c0 += KS * 64) {
+    for (int c0 = kw * 64; c0 < C; c0 += KS * 64) {
         const bool live = c0 + lane < C;
         const int c = live ? c0 + lane : C - 1;  // lanes past the row: a zero activation
         const uint4 *xp = reinterpret_cast<const uint4 *>(X + (int64_t)t * wg.K + 32 * (int64_t)c);
@@ -354,99 +585,161 @@ __global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint
 #pragma unroll
         for (int i = 0; i < 4; i++)
             xq[i] = xp[i];
-        Raw<FMT> g[R], u[R];
+        Acts<PAIRS> x;
+        struct Rows {
+            Raw<FMT> g[R], u[R];
+        };
+        const At<FMT> pg = at_row<FMT>(wg, row0, c, lane), pu = at_row<FMT>(wu, row0, c, lane);
+        auto load = [&](int g, Rows &w) {
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            const int64_t n = row0 + (f0 + r < F ? f0 + r : F - 1);
-            load_raw<FMT>(wg, n, c, lane, g[r]);
-            load_raw<FMT>(wu, n, c, lane, u[r]);
-        }
-        float a[32], asum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const uint32_t w[4] = {xq[i].x, xq[i].y, xq[i].z, xq[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                a[8 * i + 2 * j] = live ? bf16_lo(w[j]) : 0.0f;
-                a[8 * i + 2 * j + 1] = live ? bf16_hi(w[j]) : 0.0f;
+            for (int r = 0; r < R; r++) {
+                load_raw<FMT>(wg, pg, g * R + r, w.g[r]);
+                load_raw<FMT>(wu, pu, g * R + r, w.u[r]);
             }
-        }
-        if (FMT == FMT_Q4K) {
+        };
+        auto ready = [&] {
+            {  // after the first loads are out
+                float sum = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-                asum += a[i];
-        }
+                for (int i = 0; i < 4; i++) {
+                    const uint32_t keep = live ? ~0u : 0u;
+                    const uint32_t v[4] = {xq[i].x & keep, xq[i].y & keep, xq[i].z & keep, xq[i].w & keep};
+                    if constexpr (PAIRS) {
+                        x.p[4 * i] = __builtin_amdgcn_perm(v[2], v[0], 0x05040100u);
+                        x.p[4 * i + 1] = __builtin_amdgcn_perm(v[2], v[0], 0x07060302u);
+                        x.p[4 * i + 2] = __builtin_amdgcn_perm(v[3], v[1], 0x05040100u);
+                        x.p[4 * i + 3] = __builtin_amdgcn_perm(v[3], v[1], 0x07060302u);
 #pragma unroll
-        for (int r = 0; r < R; r++) {
-            v[2 * r] += dot32<FMT>(wg, g[r], c, a, asum);
-            v[2 * r + 1] += dot32<FMT>(wu, u[r], c, a, asum);
-        }
+                        for (int j = 0; j < 4; j++)
+                            sum = dot2(v[j], 0x3F803F80u, sum);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            x.a[8 * i + 2 * j] = bf16_lo(v[j]);
+                            x.a[8 * i + 2 * j + 1] = bf16_hi(v[j]);
+                        }
+                    }
+                }
+                x.sum = sum;
+            }
+        };
+        auto use = [&](int g, const Rows &w) {
+            float v[2 * R];
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                v[r] = dot<FMT, PAIRS>(wg, w.g[r], c, x);
+                v[R + r] = dot<FMT, PAIRS>(wu, w.u[r], c, x);
+            }
+            const float tot = wave_sums<2 * R>(v, lane);
+            if (lane < 2 * R) {
+                const int i = sum_index<2 * R>(lane);  // gate rows, then up rows
+                float &p = part[kw][(i >= R ? 32 : 0) + rw * rows + g * R + i % R];
+                p = c0 == kw * 64 ? tot : p + tot;
+            }
+        };
+        walk<Rows>(groups, load, ready, use);
     }
-    const float tot = wave_sums<2 * R>(v, lane);
-    if (lane < 2 * R)
-        part[wave][sum_index<2 * R>(lane)] = tot;
     __syncthreads();
-    if (threadIdx.x < R && f0 + threadIdx.x < F) {
+    if (threadIdx.x < 32) {
         float gs = 0.0f, us = 0.0f;
         for (int w = 0; w < KS; w++) {
-            gs += part[w][2 * threadIdx.x];
-            us += part[w][2 * threadIdx.x + 1];
+            gs += part[w][threadIdx.x];
+            us += part[w][32 + threadIdx.x];
         }
-        H[(int64_t)pair * F + f0 + threadIdx.x] = act_f32(act, gs) * us;
+        const float h = act_f32(act, gs) * us;
+        if constexpr (HMODE == 0)
+            static_cast<float *>(H)[(int64_t)pair * F + f0 + threadIdx.x] = h;
+        else
+            write_digits(h, static_cast<uint4 *>(H) + HW * (pair * (F / 32) + blockIdx.x), HMODE == 2);
     }
 }
 
+// Rows n0 .. of Y for token blockIdx.y: lane l of a wave holds chunks l, l +
+// 64 KS, .. of the k choices' rows laid end to end.
 template <int FMT, int R>
-__global__ __launch_bounds__(1024) void moe_down_kernel(Mat wd, const float *__restrict__ H,
+__global__ __launch_bounds__(512) void moe_down_kernel(Mat wd, const void *__restrict__ H,
                                                         const int32_t *__restrict__ ids, const float *__restrict__ weights,
-                                                        float *__restrict__ Y, int E, int k, int64_t K)
+                                                        float *__restrict__ Y, int E, int k, int64_t K, int groups)
 {
-    __shared__ float part[16][R];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, KS = blockDim.x >> 6;
+    constexpr bool DIG = digits_fmt(FMT);
+    __shared__ float part[MAXG][8][R];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), KS = blockDim.x >> 6;
     const int t = blockIdx.y;
-    const int64_t n0 = (int64_t)blockIdx.x * R;
+    const int64_t n0 = (int64_t)blockIdx.x * (groups * R);
+    const int left = (int)(K - n0 < groups * R ? K - n0 : groups * R);  // rows there are
     const int CF = (int)(wd.K / 32), items = k * CF;
-    float v[R];
-#pragma unroll
-    for (int i = 0; i < R; i++)
-        v[i] = 0.0f;
     for (int i0 = wave * 64; i0 < items; i0 += KS * 64) {
         const int it = min(i0 + lane, items - 1);
-        const int slot = it / CF, c = it - slot * CF;
+        const int slot = (int)((unsigned)it / (unsigned)CF), c = it - slot * CF;
         int e = ids[t * k + slot];
         const bool live = i0 + lane < items && e >= 0 && e < E;
+        // (H of a choice without an expert was never written: whatever is there
+        // is replaced by zero)
         const float wt = live ? weights[t * k + slot] : 0.0f;
         e = live ? e : 0;
-        Raw<FMT> w[R];
+        const int64_t chunk = ((int64_t)t * k + slot) * CF + c;
+        const uint4 *hp = static_cast<const uint4 *>(H) + (DIG ? HW : 8) * chunk;
+        uint4 hq[DIG ? HW : 8];
 #pragma unroll
-        for (int r = 0; r < R; r++)
-            load_raw<FMT>(wd, (int64_t)e * K + (n0 + r < K ? n0 + r : K - 1), c, lane, w[r]);
-        // H of a choice without an expert was never written
-        const float4 *hp = reinterpret_cast<const float4 *>(H + ((int64_t)t * k + slot) * wd.K + 32 * (int64_t)c);
-        float a[32], asum = 0.0f;
+        for (int i = 0; i < (DIG ? HW : 8); i++)
+            hq[i] = hp[i];
+        std::conditional_t<DIG, Digits, Acts<false>> x;
+        struct Rows {
+            Raw<FMT> w[R];
+        };
+        const At<FMT> pd = at_row<FMT>(wd, (int64_t)e * K + n0, c, lane);
+        auto load = [&](int g, Rows &w) {
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            const float4 q = live ? hp[i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            a[4 * i] = q.x, a[4 * i + 1] = q.y, a[4 * i + 2] = q.z, a[4 * i + 3] = q.w;
-        }
-        if (FMT == FMT_Q4K) {
+            for (int r = 0; r < R; r++)
+                load_raw<FMT>(wd, pd, g * R + r < left ? g * R + r : left - 1, w.w[r]);
+        };
+        auto ready = [&] {
+            {
+                if constexpr (DIG) {
 #pragma unroll
-            for (int i = 0; i < 32; i++)
-                asum += a[i];
-        }
+                    for (int j = 0; j < 3; j++) {
+                        x.d[j][0] = hq[2 * j].x, x.d[j][1] = hq[2 * j].y, x.d[j][2] = hq[2 * j].z, x.d[j][3] = hq[2 * j].w;
+                        x.d[j][4] = hq[2 * j + 1].x, x.d[j][5] = hq[2 * j + 1].y, x.d[j][6] = hq[2 * j + 1].z,
+                        x.d[j][7] = hq[2 * j + 1].w;
+                    }
+                    x.unit = live ? __uint_as_float(hq[6].x) * wt : 0.0f;
+                    x.sum = live ? __uint_as_float(hq[6].y) * wt : 0.0f;
+                } else {
+                    x.sum = 0.0f;
 #pragma unroll
-        for (int r = 0; r < R; r++)
-            v[r] = fmaf(wt, dot32<FMT>(wd, w[r], c, a, asum), v[r]);
+                    for (int i = 0; i < 8; i++) {
+                        x.a[4 * i] = live ? __uint_as_float(hq[i].x) * wt : 0.0f;
+                        x.a[4 * i + 1] = live ? __uint_as_float(hq[i].y) * wt : 0.0f;
+                        x.a[4 * i + 2] = live ? __uint_as_float(hq[i].z) * wt : 0.0f;
+                        x.a[4 * i + 3] = live ? __uint_as_float(hq[i].w) * wt : 0.0f;
+                    }
+                }
+            }
+        };
+        auto use = [&](int g, const Rows &w) {
+            float v[R];
+#pragma unroll
+            for (int r = 0; r < R; r++) {
+                if constexpr (DIG)
+                    v[r] = dot<FMT>(w.w[r], c, x);
+                else
+                    v[r] = dot<FMT, false>(wd, w.w[r], c, x);
+            }
+            const float tot = wave_sums<R>(v, lane);
+            if (lane < R) {
+                float &p = part[g][wave][sum_index<R>(lane)];
+                p = i0 == wave * 64 ? tot : p + tot;
+            }
+        };
+        walk<Rows>(groups, load, ready, use);
     }
-    const float tot = wave_sums<R>(v, lane);
-    if (lane < R)
-        part[wave][sum_index<R>(lane)] = tot;
     __syncthreads();
-    if (threadIdx.x < R && n0 + threadIdx.x < K) {
+    for (int i = threadIdx.x; i < groups * R; i += blockDim.x) {
         float s = 0.0f;
         for (int w = 0; w < KS; w++)
-            s += part[w][threadIdx.x];
-        Y[(int64_t)t * K + n0 + threadIdx.x] = s;
+            s += part[i / R][w][i % R];
+        if (n0 + i < K)
+            Y[(int64_t)t * K + n0 + i] = s;
     }
 }
 
@@ -690,7 +983,8 @@ __global__ __launch_bounds__(256) void moe_gemm_kernel(Mat w0, Mat w1, const uin
 // Few tokens: up to four, where the chosen experts hardly repeat.
 bool few(int T) { return T <= 4; }
 
-// Workspace, few tokens: H fp32 [T k][F].  Otherwise, P = T k pairs:
+// Workspace, few tokens: H [T k][F] in 4 bytes a value (fp32; the digits take
+// 3.5).  Otherwise, P = T k pairs:
 // H hi, H lo bf16 [P][F], Pd fp32 [P][K], the plan.
 struct Layout {
     int64_t hlo, pd, tiles, pair, place, total;
@@ -713,26 +1007,50 @@ Layout layout_of(int T, int E, int k, int64_t F, int64_t K)
     return l;
 }
 
-template <int FMT>
-hipError_t glu_few(const MoeArgs &a, float *H, hipStream_t s)
+// Groups of R rows per workgroup: one while the launch has up to `want` waves,
+// then as many as keep it near that, so that the activations are read once for
+// more rows and the next rows' loads overlap the current ones' products.
+int groups_for(int64_t rows, int R, int64_t waves_per_group, int64_t want)
+{
+    const int64_t g = ((rows + R - 1) / R * waves_per_group + want - 1) / want;
+    return (int)(g < 1 ? 1 : g > MAXG ? MAXG : g);
+}
+
+template <int FMT, int R, int HMODE>
+hipError_t glu_few(const MoeArgs &a, hipStream_t s)
 {
     const Mat wg{a.gate, planes_of(FMT, a.E * a.F, a.K), a.K}, wu{a.up, wg.p, a.K};
     const int C = (int)(a.K / 32), KS = C > 7 * 64 ? 8 : (C + 63) / 64;
-    constexpr int R = 4;
-    moe_glu_kernel<FMT, R><<<dim3((unsigned)((a.F + R - 1) / R), a.T * a.k), 64 * KS, 0, s>>>(wg, wu, a.X, a.ids, H, a.E,
-                                                                                             a.k, a.F, a.act);
+    int RW = 1;
+    while (RW < 32 / R && 2 * RW * KS <= 8 && RW * KS * (a.F / 32) * a.T * a.k < 4096)
+        RW *= 2;
+    const dim3 grid((unsigned)(a.F / 32), a.T * a.k);
+    moe_glu_kernel<FMT, R, HMODE><<<grid, 64 * KS * RW, 0, s>>>(wg, wu, a.X, a.ids, a.ws, a.E, a.k, a.F, a.act, KS);
     return hipGetLastError();
 }
 
 template <int FMT>
-hipError_t down_few(const MoeArgs &a, const float *H, hipStream_t s)
+hipError_t glu_few(const MoeArgs &a, hipStream_t s)
+{
+    constexpr int R = 2;
+    if (!digits_fmt(a.fmt_d))
+        return glu_few<FMT, R, 0>(a, s);
+    if (a.fmt_d == FMT_Q8_0)
+        return glu_few<FMT, R, 1>(a, s);
+    return glu_few<FMT, R, 2>(a, s);
+}
+
+template <int FMT>
+hipError_t down_few(const MoeArgs &a, hipStream_t s)
 {
     const Mat wd{a.down, planes_of(FMT, a.E * a.K, a.F), a.F};
     const int64_t items = a.k * (a.F / 32);
-    const int KS = items > 15 * 64 ? 16 : (int)((items + 63) / 64);
-    constexpr int R = 4;
-    moe_down_kernel<FMT, R><<<dim3((unsigned)((a.K + R - 1) / R), a.T), 64 * KS, 0, s>>>(wd, H, a.ids, a.weights, a.Y, a.E,
-                                                                                        a.k, a.K);
+    const int KS = items > 7 * 64 ? 8 : (int)((items + 63) / 64);
+    constexpr int R = 2;
+    const int gr = groups_for(a.K, R, (int64_t)KS * a.T, 2048);
+    const int64_t per = gr * R;
+    const dim3 grid((unsigned)((a.K + per - 1) / per), a.T);
+    moe_down_kernel<FMT, R><<<grid, 64 * KS, 0, s>>>(wd, a.ws, a.ids, a.weights, a.Y, a.E, a.k, a.K, gr);
     return hipGetLastError();
 }
 
@@ -772,16 +1090,15 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
     const Layout l = layout_of(a.T, a.E, a.k, a.F, a.K);
     hipError_t e = hipErrorNotSupported;
     if (few(a.T)) {
-        float *H = reinterpret_cast<float *>(a.ws);
         switch (a.fmt_gu) {
-#define X(f) case f: e = glu_few<f>(a, H, s); break;
+#define X(f) case f: e = glu_few<f>(a, s); break;
             QL_EACH_FMT(X)
 #undef X
         }
         if (e != hipSuccess)
             return e;
         switch (a.fmt_d) {
-#define X(f) case f: return down_few<f>(a, H, s);
+#define X(f) case f: return down_few<f>(a, s);
             QL_EACH_FMT(X)
 #undef X
         }
