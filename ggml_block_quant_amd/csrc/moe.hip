@@ -749,13 +749,13 @@ __global__ __launch_bounds__(512) void moe_down_kernel(Mat wd, const void *__res
 // pair's results do not depend on its place.
 // ---------------------------------------------------------------------------
 struct Plan {
-    int32_t *tiles;   // [4]: number of tiles; then {expert, first, count, 0} per tile
+    int32_t *tiles;   // [4]: numbers of tiles and of pairs with an expert; then {expert, first, count, 0} per tile
     int32_t *pair;    // sorted place -> pair
     int32_t *place;   // pair -> sorted place, -1 without an expert
 };
 constexpr int MAXE = 1024;
 
-__global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *__restrict__ ids, int P, int E, int BM, Plan pl)
+__device__ void plan_block(const int32_t *__restrict__ ids, int P, int E, int BM, const Plan &pl)
 {
     __shared__ int cnt[MAXE], off[MAXE], til[MAXE], scan[2][1024];
     const int tid = threadIdx.x;
@@ -781,8 +781,10 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *__restric
     }
     off[tid] = scan[0][tid] - c;
     til[tid] = scan[1][tid] - nt;
-    if (tid == 1023)
+    if (tid == 1023) {
         pl.tiles[0] = scan[1][tid];
+        pl.tiles[1] = scan[0][tid];
+    }
     cnt[tid] = 0;
     int4 *tl = reinterpret_cast<int4 *>(pl.tiles + 4);
     for (int i = 0; i < nt; i++)
@@ -797,6 +799,11 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *__restric
         }
         pl.place[p] = at;
     }
+}
+
+__global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *__restrict__ ids, int P, int E, int BM, Plan pl)
+{
+    plan_block(ids, P, E, BM, pl);
 }
 
 // Y[t] = sum_j w[t][j] * P[place of (t, j)], in the order of j
@@ -978,16 +985,672 @@ __global__ __launch_bounds__(256) void moe_gemm_kernel(Mat w0, Mat w1, const uin
 }
 
 // ---------------------------------------------------------------------------
+// Grouped products of the tuned formats (Q4K, Q6K, Q8_0) on
+// v_mfma_f32_16x16x32_f16.  Weights enter as whole numbers, which fp16 holds
+// exactly, and their scales multiply fp32 sums of products:
+//   Q4K   sc * u <= 63 * 15 as one operand, scale d per 256; the minimums as
+//         one more product per slab of 128 (bf16): m times the sums of the
+//         activations over the blocks of 32;
+//   Q6K   sc * q has 13 bits, so sc = 16 sh + sl and two operands, 16 sh q and
+//         sl q; scale d per 256;
+//   Q8_0  q as one operand, scale d per 32.
+// So X costs one product per weight (Q6K two) where a bf16 pair per weight
+// costs two, and only sums round.
+// Activations are fp16 times a power of two per row (row maximum in [2^14,
+// 2^15)): every bf16 value of X down to 2^-32 of its token's largest is exact;
+// H is a pair of fp16, 22 significant bits.
+//
+// k order: for Q4K and Q6K lane (g, r) holds block 4 s + g of row r in slab s
+// (one 16-byte load of codes) and step t multiplies octet t of the four
+// blocks; for Q8_0, whose scale is per block, step t is block 4 s + t.
+//
+// D[m = 4 g + i][n = r]: tokens are the A operand, so that a lane's results
+// belong to the row whose scales it holds.
+//
+// Two kernels.  moe_thin_kernel, up to 32 pairs an expert (TM <= 2 tiles of 16):
+// the waves read X from the caches straight into operands, there is no barrier
+// in the loop, and the weights stream; in the down product the eight waves of
+// a workgroup split the row and add their sums through LDS.  moe_wide_kernel,
+// more pairs: tiles of 64 pairs whose slabs are staged in LDS, double
+// buffered, and shared by four waves of 64 rows each, so that a weight is
+// decoded once per 64 pairs.
+// ---------------------------------------------------------------------------
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pk(float a, float b) { return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b}); }
+__device__ __forceinline__ f16x2_t h2(uint32_t v) { return __builtin_bit_cast(f16x2_t, v); }
+__device__ __forceinline__ uint32_t u2(f16x2_t v) { return __builtin_bit_cast(uint32_t, v); }
+__device__ __forceinline__ f16x8_t h8(uint4 v) { return __builtin_bit_cast(f16x8_t, v); }
+__device__ __forceinline__ uint32_t pkb(float a, float b) { return __builtin_bit_cast(uint32_t, bf16x2_t{(__bf16)a, (__bf16)b}); }
+
+// v = h + m + l, three bf16 (24 significant bits)
+__device__ __forceinline__ void split3(float v, float &h, float &m, float &l)
+{
+    h = (float)(__bf16)v;
+    m = (float)(__bf16)(v - h);
+    l = v - h - m;
+}
+// A block's sum of activations and its minimum's factor as the eight k of one
+// MFMA step: h h m m h l 0 0 against H M H M L H 0 0, the products of three
+// bf16 parts each down to 2^-24 of the whole.
+__device__ __forceinline__ uint4 sum_entry(float v)
+{
+    float h, m, l;
+    split3(v, h, m, l);
+    return make_uint4(pkb(h, h), pkb(m, m), pkb(h, l), 0u);
+}
+__device__ __forceinline__ bf16x8_t min_entry(float v)
+{
+    float h, m, l;
+    split3(v, h, m, l);
+    return __builtin_bit_cast(bf16x8_t, make_uint4(pkb(h, m), pkb(h, m), pkb(l, h), 0u));
+}
+
+struct Acts16 {          // activations of a product
+    const uint16_t *hi;  // [rows][pitch] fp16
+    const uint16_t *lo;  // H only
+    const uint4 *sums;   // [rows][pitch / 32]: sum_entry of the blocks
+    const float *unit;   // [rows]: 2^-e
+    int64_t pitch;       // a multiple of 128, zeros past the row's end
+};
+
+// What a lane loads of one row tile and slab, and its operands.
+template <int FMT> struct Tile16;
+template <> struct Tile16<FMT_Q4K> { uint4 c, h; };
+template <> struct Tile16<FMT_Q6K> { uint4 c; uint2 hi; uint32_t sc, d; };
+template <> struct Tile16<FMT_Q8_0> { uint2 c[4]; uint32_t d[2]; };
+
+template <int FMT>
+__device__ __forceinline__ void load_tile(const Mat &w, int64_t n, int s, int g, Tile16<FMT> &t)
+{
+    if constexpr (FMT == FMT_Q4K) {
+        const int64_t sub = n * (w.K / 32) + 4 * s + g;
+        t.c = stream16(w.B + 16 * sub);
+        t.h = *reinterpret_cast<const uint4 *>(w.B + w.p.scales + 16 * (sub >> 3));
+    } else if constexpr (FMT == FMT_Q6K) {
+        const int64_t G = n * (w.K / 256) + (s >> 1);
+        const int c = 4 * (s & 1) + g;
+        t.c = stream16(w.B + 192 * G + 16 * c);
+        t.hi = *reinterpret_cast<const uint2 *>(w.B + 192 * G + 128 + 8 * c);
+        t.sc = *reinterpret_cast<const uint16_t *>(w.B + w.p.scales + 16 * G + 2 * c);
+        t.d = *reinterpret_cast<const uint16_t *>(w.B + w.p.d + 2 * G);
+    } else {
+        const int blocks = (int)(w.K / 32);
+        const int64_t b0 = n * blocks;
+        const uint8_t *dp = w.B + w.p.scales + 2 * b0;
+        if (4 * s + 4 <= blocks) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                t.c[i] = *reinterpret_cast<const uint2 *>(w.B + 32 * (b0 + 4 * s + i) + 8 * g);
+            if (blocks % 4 == 0) {  // eight aligned bytes
+                const uint2 d = *reinterpret_cast<const uint2 *>(dp + 8 * s);
+                t.d[0] = d.x, t.d[1] = d.y;
+                return;
+            }
+        } else {  // the row ends inside the slab: its last block again (X is zero there)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                t.c[i] = *reinterpret_cast<const uint2 *>(w.B + 32 * (b0 + min(4 * s + i, blocks - 1)) + 8 * g);
+        }
+        uint32_t d[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            d[i] = *reinterpret_cast<const uint16_t *>(dp + 2 * min(4 * s + i, blocks - 1));
+        t.d[0] = d[0] | d[1] << 16, t.d[1] = d[2] | d[3] << 16;
+    }
+}
+
+// the fp16 operands of steps 2 h, 2 h + 1 of a slab (h = 0, 1)
+template <int FMT> constexpr int PER = FMT == FMT_Q6K ? 2 : 1;  // operands per step
+template <int FMT>
+__device__ __forceinline__ void decode_half(const Tile16<FMT> &t, int s, int g, int h, f16x8_t (&o)[2][PER<FMT>])
+{
+    if constexpr (FMT == FMT_Q4K) {
+        const int j = 4 * (s & 1) + g;
+        const uint32_t sc = __builtin_amdgcn_ubfe(t.h.y, 4 * j, 4) | (__builtin_amdgcn_ubfe(t.h.w, 2 * j, 2) << 4);
+        const _Float16 sh = (_Float16)(float)sc;
+        const f16x2_t S = {sh, sh}, S16 = S * (_Float16)0.0625f, N = S * (_Float16)-1024.0f, N16 = S * (_Float16)-64.0f;
+        const uint32_t cw[2] = {h ? t.c.z : t.c.x, h ? t.c.w : t.c.y};
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            // 1024 + u in the low nibbles' pairs, 1024 + 16 u in the next ones';
+            // the fused multiply-adds leave sc u exactly
+            const uint32_t a = cw[q], b = cw[q] >> 8;
+            const f16x2_t p0 = __builtin_elementwise_fma(h2((a & 0x000F000Fu) | 0x64006400u), S, N);
+            const f16x2_t p1 = __builtin_elementwise_fma(h2((a & 0x00F000F0u) | 0x64006400u), S16, N16);
+            const f16x2_t p2 = __builtin_elementwise_fma(h2((b & 0x000F000Fu) | 0x64006400u), S, N);
+            const f16x2_t p3 = __builtin_elementwise_fma(h2((b & 0x00F000F0u) | 0x64006400u), S16, N16);
+            o[q][0] = h8(make_uint4(u2(p0), u2(p1), u2(p2), u2(p3)));
+        }
+    } else if constexpr (FMT == FMT_Q6K) {
+        // one sub-scale per half: sc = 16 sh + sl; pairs 0, 2 hold q, pairs 1, 3 hold 16 q
+        const int sc = (int)(int8_t)(h ? t.sc >> 8 : t.sc);
+        const _Float16 hi16 = (_Float16)(float)(sc & ~15), lo16 = (_Float16)(float)(sc & 15);
+        const f16x2_t Hs = {hi16, hi16}, Ls = {lo16, lo16}, Hs16 = Hs * (_Float16)0.0625f, Ls16 = Ls * (_Float16)0.0625f;
+        const f16x2_t off1 = {(_Float16)-1056.0f, (_Float16)-1056.0f}, off16 = {(_Float16)-1536.0f, (_Float16)-1536.0f};
+        const uint32_t cw[2] = {h ? t.c.z : t.c.x, h ? t.c.w : t.c.y}, hw = h ? t.hi.y : t.hi.x;
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            const uint32_t a = cw[q], b = cw[q] >> 8, H = hw >> (8 * q);
+            const f16x2_t q0 = h2((a & 0x000F000Fu) | ((H << 4) & 0x00300030u) | 0x64006400u) + off1;
+            const f16x2_t q1 = h2((a & 0x00F000F0u) | ((H << 6) & 0x03000300u) | 0x64006400u) + off16;
+            const f16x2_t q2 = h2((b & 0x000F000Fu) | (H & 0x00300030u) | 0x64006400u) + off1;
+            const f16x2_t q3 = h2((b & 0x00F000F0u) | ((H << 2) & 0x03000300u) | 0x64006400u) + off16;
+            o[q][0] = h8(make_uint4(u2(q0 * Hs), u2(q1 * Hs16), u2(q2 * Hs), u2(q3 * Hs16)));
+            o[q][1] = h8(make_uint4(u2(q0 * Ls), u2(q1 * Ls16), u2(q2 * Ls), u2(q3 * Ls16)));
+        }
+    } else {
+        const f16x2_t off = {(_Float16)-1152.0f, (_Float16)-1152.0f};  // 1024 + 128 + q -> q
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            const uint32_t x = t.c[2 * h + q].x ^ 0x80808080u, y = t.c[2 * h + q].y ^ 0x80808080u;
+            o[q][0] = h8(make_uint4(u2(h2(__builtin_amdgcn_perm(0x64646464u, x, 0x04010400u)) + off),
+                                    u2(h2(__builtin_amdgcn_perm(0x64646464u, x, 0x04030402u)) + off),
+                                    u2(h2(__builtin_amdgcn_perm(0x64646464u, y, 0x04010400u)) + off),
+                                    u2(h2(__builtin_amdgcn_perm(0x64646464u, y, 0x04030402u)) + off)));
+        }
+    }
+}
+
+// scale of the slab's 256 (Q4K, Q6K) or of its block i (Q8_0)
+template <int FMT>
+__device__ __forceinline__ float scale_of(const Tile16<FMT> &t, int i)
+{
+    if constexpr (FMT == FMT_Q4K)
+        return f16_bits_to_f32(t.h.x);
+    else if constexpr (FMT == FMT_Q6K)
+        return f16_bits_to_f32(t.d);
+    else
+        return f16_bits_to_f32(t.d[i >> 1] >> (16 * (i & 1)));
+}
+// Q4K: the 6-bit minimum of the lane's block
+__device__ __forceinline__ float min_code(const Tile16<FMT_Q4K> &t, int s, int g)
+{
+    const int j = 4 * (s & 1) + g;
+    return (float)(__builtin_amdgcn_ubfe(t.h.z, 4 * j, 4) | (__builtin_amdgcn_ubfe(t.h.w, 16 + 2 * j, 2) << 4));
+}
+
+// byte offset in a 256-byte slab of a row of activations: step t, lane group g
+template <int FMT>
+__device__ __forceinline__ int slab_at(int t, int g)
+{
+    return FMT == FMT_Q8_0 ? 64 * t + 16 * g : 64 * g + 16 * t;
+}
+
+__device__ __forceinline__ f32x4_t mfma16(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+
+// Work order: the tiles of one expert share its weights and the blocks of one
+// tile its activations, so workgroups that run together take 8 tiles x 8
+// blocks, and each XCD (workgroup id modulo 8) takes a contiguous part.
+__device__ __forceinline__ bool place_of_block(int ntiles, int nblk, int &tile, int &blk)
+{
+    const int64_t total = (int64_t)ntiles * nblk, per = (total + 7) / 8;
+    const int64_t bid = blockIdx.x, at = (bid & 7) * per + (bid >> 3);
+    if ((bid >> 3) >= per || at >= total)
+        return false;
+    const int band = (int)(at / ((int64_t)nblk * 8));         // 8 tiles
+    const int tiles = min(8, ntiles - 8 * band);
+    const int in = (int)(at - (int64_t)band * nblk * 8);
+    blk = in / tiles;
+    tile = 8 * band + in % tiles;
+    return true;
+}
+
+
+// What the two kernels share: the tile, the rows, the results.
+// GLU: row tiles i < NT / 2 are gate rows, the others the same rows of up;
+// H[place][column] = act(gate) * up in fp32 (columns past the row: 0).
+template <bool GLU, int NT, int TM>
+__device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], const Acts16 &x, const Plan &pl, int k, int first,
+                                              int count, int64_t n_wave, int64_t N, int64_t pitch, int act,
+                                              float *__restrict__ out)
+{
+    constexpr int NF = GLU ? NT / 2 : NT;
+    const int lane = threadIdx.x & 63, g = lane >> 4, r16 = lane & 15;
+#pragma unroll
+    for (int j = 0; j < TM; j++)
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const int m = 16 * j + 4 * g + e;
+            if (m >= count)
+                continue;
+            const int at = first + m;
+            const float u = x.unit[GLU ? pl.pair[at] / k : at];
+#pragma unroll
+            for (int i = 0; i < NF; i++) {
+                const int64_t n = n_wave + 16 * i + r16;
+                if constexpr (GLU) {
+                    if (n < pitch)
+                        out[at * pitch + n] = n < N ? act_f32(act, acc[i][j][e] * u) * (acc[i + NF][j][e] * u) : 0.0f;
+                } else {
+                    if (n < N)
+                        out[at * pitch + n] = acc[i][j][e] * u;
+                }
+            }
+        }
+}
+
+template <int FMT, int TM, int NT, bool GLU>
+__global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
+                                                                  int nblk, int act, float *__restrict__ out,
+                                                                  int64_t out_pitch)
+{
+    constexpr int WAVES = GLU ? 4 : 8, NF = GLU ? NT / 2 : NT;
+    __shared__ f32x4_t red[GLU ? 1 : WAVES * NT * TM * 64];
+    int ti, blk;
+    if (!place_of_block(pl.tiles[0], nblk, ti, blk))
+        return;
+    const int4 tile = reinterpret_cast<const int4 *>(pl.tiles + 4)[ti];
+    const int expert = tile.x, first = tile.y, count = tile.z;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r16 = lane & 15;
+    const int64_t K = w0.K, n_wave = (int64_t)blk * (GLU ? 64 * NF : 16 * NF) + (GLU ? wave * 16 * NF : 0);
+    const int slabs = (int)((K + 127) / 128);
+    const int s0 = GLU ? 0 : slabs * wave / WAVES, s1 = GLU ? slabs : slabs * (wave + 1) / WAVES;
+    int64_t wrow[NF];
+#pragma unroll
+    for (int i = 0; i < NF; i++)
+        wrow[i] = (int64_t)expert * N + min(n_wave + 16 * i + r16, N - 1);
+    f32x4_t acc[NT][TM];
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+            acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    Tile16<FMT> raw[NT];
+    auto load_w = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            load_tile<FMT>(GLU && i >= NF ? w1 : w0, wrow[i % NF], s, g, raw[i]);
+    };
+    // the lane's token of each tile (past the end: the last one)
+    int64_t arow[TM];
+#pragma unroll
+    for (int j = 0; j < TM; j++) {
+        const int at = first + min(16 * j + r16, count - 1);
+        arow[j] = GLU ? pl.pair[at] / k : at;
+    }
+    if (s0 < s1)
+        load_w(s0);
+    for (int s = s0; s < s1; s++) {
+        f16x8_t xh[TM][4], xl[TM][4];
+        bf16x8_t xs[TM];
+#pragma unroll
+        for (int j = 0; j < TM; j++) {
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                const int64_t at = arow[j] * x.pitch + 128 * (int64_t)s + slab_at<FMT>(t, g) / 2;
+                xh[j][t] = *reinterpret_cast<const f16x8_t *>(x.hi + at);
+                if constexpr (!GLU)
+                    xl[j][t] = *reinterpret_cast<const f16x8_t *>(x.lo + at);
+            }
+            if constexpr (FMT == FMT_Q4K)
+                xs[j] = __builtin_bit_cast(bf16x8_t, x.sums[arow[j] * (x.pitch / 32) + 4 * s + g]);
+        }
+        Tile16<FMT> cur[NT];
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            cur[i] = raw[i];
+        load_w(min(s + 1, s1 - 1));
+        const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NT; i++) {
+            f32x4_t p[TM];
+#pragma unroll
+            for (int j = 0; j < TM; j++)
+                p[j] = zero;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                f16x8_t o[2][PER<FMT>];
+                decode_half<FMT>(cur[i], s, g, h, o);
+#pragma unroll
+                for (int j = 0; j < TM; j++)
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+#pragma unroll
+                        for (int c = 0; c < PER<FMT>; c++) {
+                            p[j] = mfma16(xh[j][2 * h + q], o[q][c], p[j]);
+                            if constexpr (!GLU)
+                                p[j] = mfma16(xl[j][2 * h + q], o[q][c], p[j]);
+                        }
+                        if constexpr (FMT == FMT_Q8_0) {
+                            const float d = scale_of<FMT>(cur[i], 2 * h + q);
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                acc[i][j][e] = fmaf(d, p[j][e], acc[i][j][e]);
+                            p[j] = zero;
+                        }
+                    }
+            }
+            if constexpr (FMT != FMT_Q8_0) {
+                const float d = scale_of<FMT>(cur[i], 0);
+#pragma unroll
+                for (int j = 0; j < TM; j++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        acc[i][j][e] = fmaf(d, p[j][e], acc[i][j][e]);
+            }
+            if constexpr (FMT == FMT_Q4K) {
+                const float dm = f16_bits_to_f32(cur[i].h.x >> 16);
+                const bf16x8_t mo = min_entry(min_code(cur[i], s, g));  // the code is exact in one part
+#pragma unroll
+                for (int j = 0; j < TM; j++) {
+                    const f32x4_t q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[j], mo, zero, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        acc[i][j][e] = fmaf(-dm, q[e], acc[i][j][e]);
+                }
+            }
+        }
+    }
+    if constexpr (!GLU) {  // the waves' sums, in order: wave w takes every WAVES-th tile of the result
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int j = 0; j < TM; j++)
+                red[((wave * NT + i) * TM + j) * 64 + lane] = acc[i][j];
+        __syncthreads();
+        static_assert(NT * TM <= WAVES, "a tile per wave");
+        if (wave >= NT * TM)
+            return;
+        f32x4_t v[1][1] = {{red[wave * 64 + lane]}};
+#pragma unroll
+        for (int w = 1; w < WAVES; w++)
+            v[0][0] += red[(w * NT * TM + wave) * 64 + lane];
+        const int i = wave / TM, j = wave % TM;
+        store_results<false, 1, 1>(v, x, pl, k, first + 16 * j, count - 16 * j, n_wave + 16 * i, N, out_pitch, act, out);
+    } else {
+        store_results<GLU, NT, TM>(acc, x, pl, k, first, count, n_wave, N, out_pitch, act, out);
+    }
+}
+
+// Four waves of 16 NT rows over a tile of 16 TM pairs.  The accumulators hold
+// the sum in units of the current scale D of each row (Q4K, Q6K): at a new
+// group of 256 they are multiplied by D_old / D_new (a group of scale 0 keeps
+// D), which needs no second set of accumulators; Q4K's minimums enter as
+// -(dmin / D) m.  Q8_0 adds each block's products times its scale.
+template <int FMT, int TM, int NT, bool GLU>
+__global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, int nblk,
+                                                          int act, float *__restrict__ out, int64_t out_pitch)
+{
+    constexpr int BM = 16 * TM, PL = GLU ? 1 : 2, NF = GLU ? NT / 2 : NT;
+    constexpr bool SUMS = FMT == FMT_Q4K, RUN = FMT != FMT_Q8_0;
+    constexpr int PX = 256 + 16, PS = 64 + 16;  // bytes of a row's slab, and of its sums
+    constexpr int BUF = BM * (PL * PX + (SUMS ? PS : 0));
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
+    int ti, blk;
+    if (!place_of_block(pl.tiles[0], nblk, ti, blk))
+        return;
+    const int4 tile = reinterpret_cast<const int4 *>(pl.tiles + 4)[ti];
+    const int expert = tile.x, first = tile.y, count = tile.z;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, r16 = lane & 15;
+    const int64_t K = w0.K, n_wave = (int64_t)blk * (64 * NF) + wave * 16 * NF;
+    const int slabs = (int)((K + 127) / 128);
+    int64_t wrow[NF];
+#pragma unroll
+    for (int i = 0; i < NF; i++)
+        wrow[i] = (int64_t)expert * N + min(n_wave + 16 * i + r16, N - 1);
+    f32x4_t acc[NT][TM];
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+#pragma unroll
+        for (int j = 0; j < TM; j++)
+            acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    float D[NT];
+#pragma unroll
+    for (int i = 0; i < NT; i++)
+        D[i] = 1.0f;
+    Tile16<FMT> raw[NT];
+    auto load_w = [&](int s) {
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            load_tile<FMT>(GLU && i >= NF ? w1 : w0, wrow[i % NF], s, g, raw[i]);
+    };
+    // rows this thread stages: 16 pieces of 16 bytes per row and slab; the
+    // sums of row tid / 4, block tid % 4
+    auto row_of = [&](int m) -> int64_t {
+        const int at = first + min(m, count - 1);
+        return GLU ? pl.pair[at] / k : at;
+    };
+    uint32_t srow[TM];
+#pragma unroll
+    for (int t = 0; t < TM; t++)
+        srow[t] = (uint32_t)row_of((tid + 256 * t) / 16);
+    static_assert(!SUMS || 4 * BM <= 256, "one sum per thread");
+    const int64_t sumrow = SUMS ? row_of(min(tid / 4, BM - 1)) * (x.pitch / 32) + (tid & 3) : 0;
+    uint4 xr[PL][TM], xsum;
+    auto load_x = [&](int s) {
+#pragma unroll
+        for (int t = 0; t < TM; t++)
+#pragma unroll
+            for (int p = 0; p < PL; p++)
+                xr[p][t] = *reinterpret_cast<const uint4 *>((p ? x.lo : x.hi) + srow[t] * x.pitch + 128 * s + 8 * (tid & 15));
+        if constexpr (SUMS)
+            xsum = x.sums[sumrow + 4 * s];
+    };
+    auto store_x = [&](int buf) {
+        uint8_t *b = smem + buf * BUF;
+#pragma unroll
+        for (int t = 0; t < TM; t++)
+#pragma unroll
+            for (int p = 0; p < PL; p++)
+                *reinterpret_cast<uint4 *>(b + p * BM * PX + ((tid + 256 * t) / 16) * PX + 16 * (tid & 15)) = xr[p][t];
+        if constexpr (SUMS)
+            if (4 * BM == 256 || tid < 4 * BM)
+                *reinterpret_cast<uint4 *>(b + PL * BM * PX + (tid / 4) * PS + 16 * (tid & 3)) = xsum;
+    };
+    load_x(0);
+    load_w(0);
+    store_x(0);
+    load_x(min(1, slabs - 1));
+    lds_barrier();
+    for (int s = 0; s < slabs; s++) {
+        const uint8_t *sx = smem + (s & 1) * BUF;
+        Tile16<FMT> cur[NT];
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            cur[i] = raw[i];
+        load_w(min(s + 1, slabs - 1));
+        if constexpr (RUN) {
+            if ((s & 1) == 0) {
+#pragma unroll
+                for (int i = 0; i < NT; i++) {
+                    const float d = scale_of<FMT>(cur[i], 0), dn = d != 0.0f ? d : D[i];
+                    // D / dn to half a step: quotient and one correction
+                    const float rc = __builtin_amdgcn_rcpf(dn), q0 = D[i] * rc, rho = fmaf(fmaf(-dn, q0, D[i]), rc, q0);
+                    D[i] = dn;
+#pragma unroll
+                    for (int j = 0; j < TM; j++)
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            acc[i][j][e] *= rho;
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            f16x8_t o[NT][2][PER<FMT>];
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+                decode_half<FMT>(cur[i], s, g, h, o[i]);
+#pragma unroll
+            for (int j = 0; j < TM; j++) {
+#pragma unroll
+                for (int q = 0; q < 2; q++) {
+                    const uint8_t *p = sx + (16 * j + r16) * PX + slab_at<FMT>(2 * h + q, g);
+                    const f16x8_t xh = *reinterpret_cast<const f16x8_t *>(p);
+                    f16x8_t xl;
+                    if constexpr (!GLU)
+                        xl = *reinterpret_cast<const f16x8_t *>(p + BM * PX);
+                    if constexpr (RUN) {
+#pragma unroll
+                        for (int c = 0; c < PER<FMT>; c++)
+#pragma unroll
+                            for (int i = 0; i < NT; i++)
+                                acc[i][j] = mfma16(xh, o[i][q][c], acc[i][j]);
+                        if constexpr (!GLU) {
+#pragma unroll
+                            for (int c = 0; c < PER<FMT>; c++)
+#pragma unroll
+                                for (int i = 0; i < NT; i++)
+                                    acc[i][j] = mfma16(xl, o[i][q][c], acc[i][j]);
+                        }
+                    } else {
+                        f32x4_t v[NT];
+#pragma unroll
+                        for (int i = 0; i < NT; i++)
+                            v[i] = mfma16(xh, o[i][q][0], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                        if constexpr (!GLU) {
+#pragma unroll
+                            for (int i = 0; i < NT; i++)
+                                v[i] = mfma16(xl, o[i][q][0], v[i]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < NT; i++) {
+                            const float d = scale_of<FMT>(cur[i], 2 * h + q);
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                acc[i][j][e] = fmaf(d, v[i][e], acc[i][j][e]);
+                        }
+                    }
+                }
+            }
+        }
+        if constexpr (SUMS) {
+            bf16x8_t mo[NT];
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+                mo[i] = min_entry(-f16_bits_to_f32(cur[i].h.x >> 16) * min_code(cur[i], s, g) * __builtin_amdgcn_rcpf(D[i]));
+#pragma unroll
+            for (int j = 0; j < TM; j++) {
+                const bf16x8_t xs = *reinterpret_cast<const bf16x8_t *>(sx + PL * BM * PX + (16 * j + r16) * PS + 16 * g);
+#pragma unroll
+                for (int i = 0; i < NT; i++)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs, mo[i], acc[i][j], 0, 0, 0);
+            }
+        }
+        store_x((s + 1) & 1);
+        load_x(min(s + 2, slabs - 1));
+        lds_barrier();
+    }
+    if constexpr (RUN) {
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+#pragma unroll
+            for (int j = 0; j < TM; j++)
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    acc[i][j][e] *= D[i];
+    }
+    store_results<GLU, NT, TM>(acc, x, pl, k, first, count, n_wave, N, out_pitch, act, out);
+}
+
+// A row of `n` values as fp16 times 2^e (and, for fp32 rows, the rest of each
+// value as a second fp16), its block sums, zeros up to `pitch`.  One workgroup.
+template <bool F32>
+__device__ void row_to_f16(const void *__restrict__ src, int n, int64_t pitch, uint16_t *__restrict__ hi,
+                           uint16_t *__restrict__ lo, uint4 *__restrict__ sums, float *__restrict__ unit)
+{
+    __shared__ float wm[16];
+    const int tid = threadIdx.x, n8 = n / 8, p8 = (int)(pitch / 8);
+    auto read = [&](int i, float (&v)[8]) {
+        if constexpr (F32) {
+            const float4 a = static_cast<const float4 *>(src)[2 * i], b = static_cast<const float4 *>(src)[2 * i + 1];
+            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+        } else {
+            const uint4 a = static_cast<const uint4 *>(src)[i];
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                v[2 * j] = bf16_lo(w[j]), v[2 * j + 1] = bf16_hi(w[j]);
+        }
+    };
+    float m = 0.0f;
+    for (int i = tid; i < n8; i += blockDim.x) {
+        float v[8];
+        read(i, v);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            m = fmaxf(m, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int s = 1; s < 64; s <<= 1)
+        m = fmaxf(m, __shfl_xor(m, s));
+    if ((tid & 63) == 0)
+        wm[tid >> 6] = m;
+    __syncthreads();
+    for (int w = 0; w < (int)blockDim.x / 64; w++)
+        m = fmaxf(m, wm[w]);
+    int ex = m > 0.0f ? 15 - __builtin_amdgcn_frexp_expf(m) : 0;  // m 2^ex in [2^14, 2^15)
+    ex = min(ex, 126);
+    if (tid == 0)
+        *unit = __builtin_amdgcn_ldexpf(1.0f, -ex);
+    for (int i = tid; i < p8; i += blockDim.x) {
+        float v[8], s = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[j] = 0.0f;
+        if (i < n8)
+            read(i, v);
+        uint32_t h[4], l[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float a = __builtin_amdgcn_ldexpf(v[2 * j], ex), b = __builtin_amdgcn_ldexpf(v[2 * j + 1], ex);
+            const f16x2_t q = {(_Float16)a, (_Float16)b};
+            h[j] = u2(q);
+            if constexpr (F32)
+                l[j] = pk(a - (float)q.x, b - (float)q.y);
+            s += a + b;
+        }
+        *reinterpret_cast<uint4 *>(hi + 8 * (int64_t)i) = make_uint4(h[0], h[1], h[2], h[3]);
+        if constexpr (F32)
+            *reinterpret_cast<uint4 *>(lo + 8 * (int64_t)i) = make_uint4(l[0], l[1], l[2], l[3]);
+        s += dpp<0xB1>(s);  // four threads a block of 32 (p8 is a multiple of 16: all four are here)
+        s += dpp<0x4E>(s);
+        if ((i & 3) == 0)
+            sums[i >> 2] = sum_entry(s);
+    }
+}
+
+// Block T sorts the pairs; block t < T prepares X[t].
+__global__ __launch_bounds__(1024) void moe_prep_kernel(const int32_t *__restrict__ ids, int P, int E, int BM, Plan pl,
+                                                        const uint16_t *__restrict__ X, int T, int64_t K,
+                                                        uint16_t *__restrict__ xh, uint4 *__restrict__ sums,
+                                                        float *__restrict__ unit, int64_t pitch)
+{
+    const int64_t t = blockIdx.x;
+    if (t == T)
+        plan_block(ids, P, E, BM, pl);
+    else
+        row_to_f16<false>(X + t * K, (int)K, pitch, xh + t * pitch, nullptr, sums + t * (pitch / 32), unit + t);
+}
+
+// H of the sorted pairs for the down product
+__global__ __launch_bounds__(512) void moe_h_kernel(const float *__restrict__ H, Plan pl, uint16_t *__restrict__ hi,
+                                                    uint16_t *__restrict__ lo, uint4 *__restrict__ sums,
+                                                    float *__restrict__ unit, int64_t pitch)
+{
+    const int64_t at = blockIdx.x;
+    if (at < pl.tiles[1])
+        row_to_f16<true>(H + at * pitch, (int)pitch, pitch, hi + at * pitch, lo + at * pitch, sums + at * (pitch / 32), unit + at);
+}
+
+// ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
 // Few tokens: up to four, where the chosen experts hardly repeat.
 bool few(int T) { return T <= 4; }
 
 // Workspace, few tokens: H [T k][F] in 4 bytes a value (fp32; the digits take
-// 3.5).  Otherwise, P = T k pairs:
-// H hi, H lo bf16 [P][F], Pd fp32 [P][K], the plan.
+// 3.5).  Otherwise, P = T k pairs: the plan, Pd fp32 [P][K], and H: two planes
+// [P][F], and for the tuned formats F padded to 128, its sums and units, its
+// fp32 form, and X in fp16 with its sums and units.  One layout for every
+// format and tile size.
 struct Layout {
-    int64_t hlo, pd, tiles, pair, place, total;
+    int64_t hlo, hsum, hunit, h32, xh, xsum, xunit, pd, tiles, pair, place, total;
+    int64_t fp, kp;
 };
 Layout layout_of(int T, int E, int k, int64_t F, int64_t K)
 {
@@ -998,9 +1661,18 @@ Layout layout_of(int T, int E, int k, int64_t F, int64_t K)
         return l;
     }
     const int64_t most = P / 16 + (P < E ? P : E) + 1;
-    l.hlo = up16(2 * P * F);
-    l.pd = l.hlo + up16(2 * P * F);
-    l.tiles = l.pd + 4 * P * K;
+    l.fp = (F + 127) / 128 * 128;
+    l.kp = (K + 127) / 128 * 128;
+    l.hlo = 2 * P * l.fp;
+    l.hsum = l.hlo + 2 * P * l.fp;
+    l.hunit = l.hsum + P * l.fp / 2;
+    l.h32 = l.hunit + up16(4 * P);
+    l.xh = l.h32 + 4 * P * l.fp;
+    l.xsum = l.xh + 2 * T * l.kp;
+    l.xunit = l.xsum + T * l.kp / 2;
+    // Pd takes the place of H's fp32 form where that is large enough
+    l.pd = K <= l.fp ? l.h32 : l.xunit + up16(4 * T);
+    l.tiles = K <= l.fp ? l.xunit + up16(4 * T) : l.pd + 4 * P * K;
     l.pair = l.tiles + 16 * (1 + most);
     l.place = l.pair + up16(4 * P);
     l.total = l.place + up16(4 * P);
@@ -1077,6 +1749,53 @@ hipError_t gemm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, in
     return gemm<FMT, 4, 2, GLU>(a, l, pl, max_tiles, s);
 }
 
+template <int FMT, int TM, bool GLU>
+hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, hipStream_t s)
+{
+    constexpr int NT = 4;
+    constexpr bool THIN = TM <= 2;
+    const int64_t N = GLU ? a.F : a.K, K = GLU ? a.K : a.F, per = GLU ? 32 * NT : THIN ? 16 * NT : 64 * NT;
+    const Planes p = planes_of(FMT, a.E * N, K);
+    const Mat w0{GLU ? a.gate : a.down, p, K}, w1{GLU ? a.up : a.down, p, K};
+    const auto u16 = [&](int64_t at) { return reinterpret_cast<const uint16_t *>(a.ws + at); };
+    const auto u4 = [&](int64_t at) { return reinterpret_cast<const uint4 *>(a.ws + at); };
+    const auto f32 = [&](int64_t at) { return reinterpret_cast<float *>(a.ws + at); };
+    const Acts16 x = GLU ? Acts16{u16(l.xh), nullptr, u4(l.xsum), f32(l.xunit), l.kp}
+                         : Acts16{u16(0), u16(l.hlo), u4(l.hsum), f32(l.hunit), l.fp};
+    const int64_t nblk = (N + per - 1) / per, grid = (nblk * max_tiles + 7) / 8 * 8;
+    if (grid >= (int64_t(1) << 31))
+        return hipErrorNotSupported;
+    float *out = f32(GLU ? l.h32 : l.pd);
+    const int64_t pitch = GLU ? l.fp : a.K;
+    if constexpr (THIN)
+        moe_thin_kernel<FMT, TM, NT, GLU><<<dim3((unsigned)grid), GLU ? 256 : 512, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk,
+                                                                                         a.act, out, pitch);
+    else
+        moe_wide_kernel<FMT, TM, NT, GLU><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk, a.act, out,
+                                                                              pitch);
+    return hipGetLastError();
+}
+
+template <int FMT, bool GLU>
+hipError_t mm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, int max_tiles, hipStream_t s)
+{
+    if (tm == 1)
+        return mm<FMT, 1, GLU>(a, l, pl, max_tiles, s);
+    if (tm == 2)
+        return mm<FMT, 2, GLU>(a, l, pl, max_tiles, s);
+    return mm<FMT, 4, GLU>(a, l, pl, max_tiles, s);
+}
+
+template <bool GLU>
+hipError_t mm_fmt(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, int max_tiles, hipStream_t s)
+{
+    switch (GLU ? a.fmt_gu : a.fmt_d) {
+    case FMT_Q4K: return mm_tm<FMT_Q4K, GLU>(a, l, pl, tm, max_tiles, s);
+    case FMT_Q6K: return mm_tm<FMT_Q6K, GLU>(a, l, pl, tm, max_tiles, s);
+    default: return mm_tm<FMT_Q8_0, GLU>(a, l, pl, tm, max_tiles, s);
+    }
+}
+
 #define QL_EACH_FMT(X)                                                                                               \
     X(FMT_Q8_0) X(FMT_Q4K) X(FMT_Q6K) X(FMT_Q2K) X(FMT_Q3K) X(FMT_Q5K) X(FMT_Q4_0) X(FMT_Q4_1) X(FMT_Q5_0) X(FMT_Q5_1) \
         X(FMT_FP8)
@@ -1110,25 +1829,38 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
     const int max_tiles = P / BM + (P < a.E ? P : a.E);
     const Plan pl{reinterpret_cast<int32_t *>(a.ws + l.tiles), reinterpret_cast<int32_t *>(a.ws + l.pair),
                   reinterpret_cast<int32_t *>(a.ws + l.place)};
-    moe_plan_kernel<<<1, 1024, 0, s>>>(a.ids, P, a.E, BM, pl);
-    if ((e = hipGetLastError()) != hipSuccess)
-        return e;
-    e = hipErrorNotSupported;
-    switch (a.fmt_gu) {
+    if (digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d)) {
+        moe_prep_kernel<<<a.T + 1, 1024, 0, s>>>(
+            a.ids, P, a.E, BM, pl, a.X, a.T, a.K, reinterpret_cast<uint16_t *>(a.ws + l.xh),
+            reinterpret_cast<uint4 *>(a.ws + l.xsum), reinterpret_cast<float *>(a.ws + l.xunit), l.kp);
+        if ((e = hipGetLastError()) != hipSuccess || (e = mm_fmt<true>(a, l, pl, tm, max_tiles, s)) != hipSuccess)
+            return e;
+        moe_h_kernel<<<P, 512, 0, s>>>(reinterpret_cast<const float *>(a.ws + l.h32), pl, reinterpret_cast<uint16_t *>(a.ws),
+                                       reinterpret_cast<uint16_t *>(a.ws + l.hlo), reinterpret_cast<uint4 *>(a.ws + l.hsum),
+                                       reinterpret_cast<float *>(a.ws + l.hunit), l.fp);
+        if ((e = hipGetLastError()) != hipSuccess || (e = mm_fmt<false>(a, l, pl, tm, max_tiles, s)) != hipSuccess)
+            return e;
+    } else {
+        moe_plan_kernel<<<1, 1024, 0, s>>>(a.ids, P, a.E, BM, pl);
+        if ((e = hipGetLastError()) != hipSuccess)
+            return e;
+        e = hipErrorNotSupported;
+        switch (a.fmt_gu) {
 #define X(f) case f: e = gemm_tm<f, true>(a, l, pl, tm, max_tiles, s); break;
-        QL_EACH_FMT(X)
+            QL_EACH_FMT(X)
 #undef X
-    }
-    if (e != hipSuccess)
-        return e;
-    e = hipErrorNotSupported;
-    switch (a.fmt_d) {
+        }
+        if (e != hipSuccess)
+            return e;
+        e = hipErrorNotSupported;
+        switch (a.fmt_d) {
 #define X(f) case f: e = gemm_tm<f, false>(a, l, pl, tm, max_tiles, s); break;
-        QL_EACH_FMT(X)
+            QL_EACH_FMT(X)
 #undef X
+        }
+        if (e != hipSuccess)
+            return e;
     }
-    if (e != hipSuccess)
-        return e;
     moe_join_kernel<<<dim3(a.T, (unsigned)((a.K + 1023) / 1024)), 256, 0, s>>>(
         reinterpret_cast<const float *>(a.ws + l.pd), pl.place, a.weights, a.Y, a.k, a.K);
     return hipGetLastError();
