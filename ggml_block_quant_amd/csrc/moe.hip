@@ -1061,50 +1061,106 @@ template <> struct Tile16<FMT_Q4K> { uint4 c, h; };
 template <> struct Tile16<FMT_Q6K> { uint4 c; uint2 hi; uint32_t sc, d; };
 template <> struct Tile16<FMT_Q8_0> { uint2 c[4]; uint32_t d[2]; };
 
+// One expert's matrix: the planes at its first row (the same for the whole
+// wave) and 32-bit byte offsets of a lane's row in them, so that a slab's
+// addresses are scalar additions.  launch_moe keeps an expert's planes below
+// 2^31 bytes here.
+struct Planes16 {
+    const uint8_t *codes, *sc, *d;
+    int K;
+};
 template <int FMT>
-__device__ __forceinline__ void load_tile(const Mat &w, int64_t n, int s, int g, Tile16<FMT> &t)
+__device__ __forceinline__ Planes16 expert_planes(const Mat &w, int64_t row)
+{
+    Planes16 p;
+    p.K = (int)w.K;
+    if constexpr (FMT == FMT_Q4K) {
+        p.codes = w.B + row * (w.K / 2);
+        p.sc = w.B + w.p.scales + row * (w.K / 16);
+        p.d = nullptr;
+    } else if constexpr (FMT == FMT_Q6K) {
+        p.codes = w.B + row * (w.K / 256 * 192);
+        p.sc = w.B + w.p.scales + row * (w.K / 16);
+        p.d = w.B + w.p.d + row * (w.K / 128);
+    } else {
+        p.codes = w.B + row * w.K;
+        p.sc = nullptr;
+        p.d = w.B + w.p.scales + row * (w.K / 16);
+    }
+    return p;
+}
+struct Row16 {
+    uint32_t codes, sc, d;
+};
+template <int FMT>
+__device__ __forceinline__ Row16 row_offsets(int K, int row, int g)
+{
+    const uint32_t r = (uint32_t)row, k = (uint32_t)K;
+    if constexpr (FMT == FMT_Q4K)
+        return Row16{r * (k / 2) + 16u * g, r * (k / 16), 0u};
+    else if constexpr (FMT == FMT_Q6K)
+        return Row16{r * (k / 256 * 192), r * (k / 16) + 2u * g, r * (k / 128)};
+    else
+        return Row16{r * k + 8u * g, 0u, r * (k / 16)};
+}
+
+// TAIL: Q8_0 rows that end inside a slab (their last block again past it; X is
+// zero there)
+template <int FMT, bool TAIL>
+__device__ __forceinline__ void load_tile(const Planes16 &w, const Row16 &r, int s, int g, Tile16<FMT> &t)
 {
     if constexpr (FMT == FMT_Q4K) {
-        const int64_t sub = n * (w.K / 32) + 4 * s + g;
-        t.c = stream16(w.B + 16 * sub);
-        t.h = *reinterpret_cast<const uint4 *>(w.B + w.p.scales + 16 * (sub >> 3));
+        t.c = stream16(w.codes + 64 * s + r.codes);
+        t.h = *reinterpret_cast<const uint4 *>(w.sc + 16 * (s >> 1) + r.sc);
     } else if constexpr (FMT == FMT_Q6K) {
-        const int64_t G = n * (w.K / 256) + (s >> 1);
-        const int c = 4 * (s & 1) + g;
-        t.c = stream16(w.B + 192 * G + 16 * c);
-        t.hi = *reinterpret_cast<const uint2 *>(w.B + 192 * G + 128 + 8 * c);
-        t.sc = *reinterpret_cast<const uint16_t *>(w.B + w.p.scales + 16 * G + 2 * c);
-        t.d = *reinterpret_cast<const uint16_t *>(w.B + w.p.d + 2 * G);
-    } else {
-        const int blocks = (int)(w.K / 32);
-        const int64_t b0 = n * blocks;
-        const uint8_t *dp = w.B + w.p.scales + 2 * b0;
-        if (4 * s + 4 <= blocks) {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                t.c[i] = *reinterpret_cast<const uint2 *>(w.B + 32 * (b0 + 4 * s + i) + 8 * g);
-            if (blocks % 4 == 0) {  // eight aligned bytes
-                const uint2 d = *reinterpret_cast<const uint2 *>(dp + 8 * s);
-                t.d[0] = d.x, t.d[1] = d.y;
-                return;
-            }
-        } else {  // the row ends inside the slab: its last block again (X is zero there)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                t.c[i] = *reinterpret_cast<const uint2 *>(w.B + 32 * (b0 + min(4 * s + i, blocks - 1)) + 8 * g);
-        }
-        uint32_t d[4];
+        const uint8_t *c = w.codes + 192 * (s >> 1) + 64 * (s & 1), *h = w.codes + 192 * (s >> 1) + 128 + 32 * (s & 1);
+        t.c = stream16(c + (r.codes + 16u * g));
+        t.hi = *reinterpret_cast<const uint2 *>(h + (r.codes + 8u * g));
+        t.sc = *reinterpret_cast<const uint16_t *>(w.sc + 16 * (s >> 1) + 8 * (s & 1) + r.sc);
+        t.d = *reinterpret_cast<const uint16_t *>(w.d + 2 * (s >> 1) + r.d);
+    } else if constexpr (!TAIL) {
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            d[i] = *reinterpret_cast<const uint16_t *>(dp + 2 * min(4 * s + i, blocks - 1));
+            t.c[i] = *reinterpret_cast<const uint2 *>(w.codes + 128 * s + 32 * i + r.codes);
+        const uint2 d = *reinterpret_cast<const uint2 *>(w.d + 8 * s + r.d);
+        t.d[0] = d.x, t.d[1] = d.y;
+    } else {
+        uint32_t d[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int b = min(4 * s + i, w.K / 32 - 1);
+            t.c[i] = *reinterpret_cast<const uint2 *>(w.codes + 32 * b + r.codes);
+            d[i] = *reinterpret_cast<const uint16_t *>(w.d + 2 * b + r.d);
+        }
         t.d[0] = d[0] | d[1] << 16, t.d[1] = d[2] | d[3] << 16;
     }
+}
+
+// (a & mask) | 0x64006400 in one instruction: the mask in a register, the
+// constant in a scalar one (the compiler would use an and and an or with
+// literals)
+struct Nibbles {
+    uint32_t low, next;  // 0x000F000F, 0x00F000F0
+};
+__device__ __forceinline__ Nibbles make_nibbles()
+{
+    Nibbles n;
+    asm volatile("v_mov_b32 %0, 0x000f000f" : "=v"(n.low));
+    asm volatile("v_mov_b32 %0, 0x00f000f0" : "=v"(n.next));
+    return n;
+}
+__device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c)
+{
+    uint32_t r;
+    asm("v_and_or_b32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(mask), "s"(c));
+    return r;
 }
 
 // the fp16 operands of steps 2 h, 2 h + 1 of a slab (h = 0, 1)
 template <int FMT> constexpr int PER = FMT == FMT_Q6K ? 2 : 1;  // operands per step
 template <int FMT>
-__device__ __forceinline__ void decode_half(const Tile16<FMT> &t, int s, int g, int h, f16x8_t (&o)[2][PER<FMT>])
+__device__ __forceinline__ void decode_half(const Nibbles &nb, const Tile16<FMT> &t, int s, int g, int h,
+                                            f16x8_t (&o)[2][PER<FMT>])
 {
     if constexpr (FMT == FMT_Q4K) {
         const int j = 4 * (s & 1) + g;
@@ -1117,10 +1173,10 @@ __device__ __forceinline__ void decode_half(const Tile16<FMT> &t, int s, int g, 
             // 1024 + u in the low nibbles' pairs, 1024 + 16 u in the next ones';
             // the fused multiply-adds leave sc u exactly
             const uint32_t a = cw[q], b = cw[q] >> 8;
-            const f16x2_t p0 = __builtin_elementwise_fma(h2((a & 0x000F000Fu) | 0x64006400u), S, N);
-            const f16x2_t p1 = __builtin_elementwise_fma(h2((a & 0x00F000F0u) | 0x64006400u), S16, N16);
-            const f16x2_t p2 = __builtin_elementwise_fma(h2((b & 0x000F000Fu) | 0x64006400u), S, N);
-            const f16x2_t p3 = __builtin_elementwise_fma(h2((b & 0x00F000F0u) | 0x64006400u), S16, N16);
+            const f16x2_t p0 = __builtin_elementwise_fma(h2(and_or(a, nb.low, 0x64006400u)), S, N);
+            const f16x2_t p1 = __builtin_elementwise_fma(h2(and_or(a, nb.next, 0x64006400u)), S16, N16);
+            const f16x2_t p2 = __builtin_elementwise_fma(h2(and_or(b, nb.low, 0x64006400u)), S, N);
+            const f16x2_t p3 = __builtin_elementwise_fma(h2(and_or(b, nb.next, 0x64006400u)), S16, N16);
             o[q][0] = h8(make_uint4(u2(p0), u2(p1), u2(p2), u2(p3)));
         }
     } else if constexpr (FMT == FMT_Q6K) {
@@ -1164,6 +1220,12 @@ __device__ __forceinline__ float scale_of(const Tile16<FMT> &t, int i)
     else
         return f16_bits_to_f32(t.d[i >> 1] >> (16 * (i & 1)));
 }
+// min_entry of a number that one bf16 holds
+__device__ __forceinline__ bf16x8_t min_entry1(float v)
+{
+    const uint32_t h = __float_as_uint(v) >> 16;
+    return __builtin_bit_cast(bf16x8_t, make_uint4(h, h, h << 16, 0u));
+}
 // Q4K: the 6-bit minimum of the lane's block
 __device__ __forceinline__ float min_code(const Tile16<FMT_Q4K> &t, int s, int g)
 {
@@ -1176,6 +1238,29 @@ template <int FMT>
 __device__ __forceinline__ int slab_at(int t, int g)
 {
     return FMT == FMT_Q8_0 ? 64 * t + 16 * g : 64 * g + 16 * t;
+}
+
+// Direct global -> LDS loads: lane i's 16 bytes at base + off_i land at LDS
+// address lds + 16 i (base and lds the same for the whole wave).  They write
+// no register; every read of what they bring comes after an explicit wait for
+// vmcnt 0 and a barrier.
+typedef __attribute__((address_space(3))) void *lds_ptr_t;
+__device__ __forceinline__ uint32_t lds_addr(const uint8_t *p) { return (uint32_t)(uintptr_t)(lds_ptr_t)p; }
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is a reserved name on a clobber list
+__device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(off), "s"(base), "s"(lds)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+// every load of this wave is in, then the workgroup's
+__device__ __forceinline__ void loads_barrier()
+{
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_barrier();
+    __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
 
 __device__ __forceinline__ f32x4_t mfma16(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
@@ -1231,7 +1316,7 @@ __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], cons
         }
 }
 
-template <int FMT, int TM, int NT, bool GLU>
+template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
                                                                   int nblk, int act, float *__restrict__ out,
                                                                   int64_t out_pitch)
@@ -1248,51 +1333,77 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
     const int64_t K = w0.K, n_wave = (int64_t)blk * (GLU ? 64 * NF : 16 * NF) + (GLU ? wave * 16 * NF : 0);
     const int slabs = (int)((K + 127) / 128);
     const int s0 = GLU ? 0 : slabs * wave / WAVES, s1 = GLU ? slabs : slabs * (wave + 1) / WAVES;
-    int64_t wrow[NF];
+    const Planes16 e0 = expert_planes<FMT>(w0, expert * N), e1 = expert_planes<FMT>(w1, expert * N);
+    Row16 wrow[NF];
 #pragma unroll
     for (int i = 0; i < NF; i++)
-        wrow[i] = (int64_t)expert * N + min(n_wave + 16 * i + r16, N - 1);
+        wrow[i] = row_offsets<FMT>((int)K, (int)min(n_wave + 16 * i + r16, N - 1), g);
     f32x4_t acc[NT][TM];
 #pragma unroll
     for (int i = 0; i < NT; i++)
 #pragma unroll
         for (int j = 0; j < TM; j++)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
+    const Nibbles nb = make_nibbles();
     Tile16<FMT> raw[NT];
     auto load_w = [&](int s) {
 #pragma unroll
         for (int i = 0; i < NT; i++)
-            load_tile<FMT>(GLU && i >= NF ? w1 : w0, wrow[i % NF], s, g, raw[i]);
+            load_tile<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s, g, raw[i]);
     };
     // the lane's token of each tile (past the end: the last one)
-    int64_t arow[TM];
+    const uint16_t *ahi[TM], *alo[TM];
+    const uint4 *asum[TM];
 #pragma unroll
     for (int j = 0; j < TM; j++) {
         const int at = first + min(16 * j + r16, count - 1);
-        arow[j] = GLU ? pl.pair[at] / k : at;
+        const int64_t row = GLU ? pl.pair[at] / k : at;
+        ahi[j] = x.hi + row * x.pitch + slab_at<FMT>(0, g) / 2;
+        alo[j] = x.lo + row * x.pitch + slab_at<FMT>(0, g) / 2;
+        asum[j] = x.sums + row * (x.pitch / 32) + g;
     }
-    if (s0 < s1)
-        load_w(s0);
-    for (int s = s0; s < s1; s++) {
-        f16x8_t xh[TM][4], xl[TM][4];
-        bf16x8_t xs[TM];
+    f16x8_t nh[TM][4], nl[TM][4];
+    bf16x8_t ns[TM];
+    auto load_x = [&](int s) {
 #pragma unroll
         for (int j = 0; j < TM; j++) {
 #pragma unroll
             for (int t = 0; t < 4; t++) {
-                const int64_t at = arow[j] * x.pitch + 128 * (int64_t)s + slab_at<FMT>(t, g) / 2;
-                xh[j][t] = *reinterpret_cast<const f16x8_t *>(x.hi + at);
+                const int at = 128 * s + (slab_at<FMT>(t, 0) - slab_at<FMT>(0, 0)) / 2;
+                nh[j][t] = *reinterpret_cast<const f16x8_t *>(ahi[j] + at);
                 if constexpr (!GLU)
-                    xl[j][t] = *reinterpret_cast<const f16x8_t *>(x.lo + at);
+                    nl[j][t] = *reinterpret_cast<const f16x8_t *>(alo[j] + at);
             }
             if constexpr (FMT == FMT_Q4K)
-                xs[j] = __builtin_bit_cast(bf16x8_t, x.sums[arow[j] * (x.pitch / 32) + 4 * s + g]);
+                ns[j] = *reinterpret_cast<const bf16x8_t *>(asum[j] + 4 * s);
         }
+    };
+    if (s0 < s1) {
+        load_w(s0);
+        load_x(s0);
+    }
+    for (int s = s0; s < s1; s++) {
+        f16x8_t xh[TM][4], xl[TM][4];
+        bf16x8_t xs[TM];
         Tile16<FMT> cur[NT];
 #pragma unroll
         for (int i = 0; i < NT; i++)
             cur[i] = raw[i];
+#pragma unroll
+        for (int j = 0; j < TM; j++) {
+#pragma unroll
+            for (int t = 0; t < 4; t++) {
+                xh[j][t] = nh[j][t];
+                if constexpr (!GLU)
+                    xl[j][t] = nl[j][t];
+            }
+            if constexpr (FMT == FMT_Q4K)
+                xs[j] = ns[j];
+        }
+        // the next slab's loads go out before this one's products
         load_w(min(s + 1, s1 - 1));
+        load_x(min(s + 1, s1 - 1));
+        __builtin_amdgcn_sched_barrier(0);
         const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < NT; i++) {
@@ -1303,7 +1414,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 f16x8_t o[2][PER<FMT>];
-                decode_half<FMT>(cur[i], s, g, h, o);
+                decode_half<FMT>(nb, cur[i], s, g, h, o);
 #pragma unroll
                 for (int j = 0; j < TM; j++)
 #pragma unroll
@@ -1333,7 +1444,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
             }
             if constexpr (FMT == FMT_Q4K) {
                 const float dm = f16_bits_to_f32(cur[i].h.x >> 16);
-                const bf16x8_t mo = min_entry(min_code(cur[i], s, g));  // the code is exact in one part
+                const bf16x8_t mo = min_entry1(min_code(cur[i], s, g));
 #pragma unroll
                 for (int j = 0; j < TM; j++) {
                     const f32x4_t q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[j], mo, zero, 0, 0, 0);
@@ -1370,14 +1481,18 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 // group of 256 they are multiplied by D_old / D_new (a group of scale 0 keeps
 // D), which needs no second set of accumulators; Q4K's minimums enter as
 // -(dmin / D) m.  Q8_0 adds each block's products times its scale.
-template <int FMT, int TM, int NT, bool GLU>
+template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, int nblk,
                                                           int act, float *__restrict__ out, int64_t out_pitch)
 {
     constexpr int BM = 16 * TM, PL = GLU ? 1 : 2, NF = GLU ? NT / 2 : NT;
     constexpr bool SUMS = FMT == FMT_Q4K, RUN = FMT != FMT_Q8_0;
-    constexpr int PX = 256 + 16, PS = 64 + 16;  // bytes of a row's slab, and of its sums
-    constexpr int BUF = BM * (PL * PX + (SUMS ? PS : 0));
+    // A buffer: per plane BM rows of 256 bytes, 16-byte piece c of row m at
+    // place c ^ (m & 15), then the sums, BM rows of 64 bytes, piece c at c ^
+    // ((m >> 2) & 3): the 16 rows that a read touches together lie in
+    // different banks, and rows need no padding, which direct loads to LDS
+    // could not write.
+    constexpr int PLANE = BM * 256, BUF = PL * PLANE + (SUMS ? BM * 64 : 0);
     __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
     int ti, blk;
     if (!place_of_block(pl.tiles[0], nblk, ti, blk))
@@ -1388,10 +1503,11 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
     const int g = lane >> 4, r16 = lane & 15;
     const int64_t K = w0.K, n_wave = (int64_t)blk * (64 * NF) + wave * 16 * NF;
     const int slabs = (int)((K + 127) / 128);
-    int64_t wrow[NF];
+    const Planes16 e0 = expert_planes<FMT>(w0, expert * N), e1 = expert_planes<FMT>(w1, expert * N);
+    Row16 wrow[NF];
 #pragma unroll
     for (int i = 0; i < NF; i++)
-        wrow[i] = (int64_t)expert * N + min(n_wave + 16 * i + r16, N - 1);
+        wrow[i] = row_offsets<FMT>((int)K, (int)min(n_wave + 16 * i + r16, N - 1), g);
     f32x4_t acc[NT][TM];
 #pragma unroll
     for (int i = 0; i < NT; i++)
@@ -1402,57 +1518,56 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
 #pragma unroll
     for (int i = 0; i < NT; i++)
         D[i] = 1.0f;
+    const Nibbles nb = make_nibbles();
     Tile16<FMT> raw[NT];
     auto load_w = [&](int s) {
 #pragma unroll
         for (int i = 0; i < NT; i++)
-            load_tile<FMT>(GLU && i >= NF ? w1 : w0, wrow[i % NF], s, g, raw[i]);
+            load_tile<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s, g, raw[i]);
     };
-    // rows this thread stages: 16 pieces of 16 bytes per row and slab; the
-    // sums of row tid / 4, block tid % 4
-    auto row_of = [&](int m) -> int64_t {
-        const int at = first + min(m, count - 1);
-        return GLU ? pl.pair[at] / k : at;
+    // Wave w stages rows 16 w TM / 4 .., four rows of 256 bytes a load, and
+    // the sums of as many rows, 16 rows a load.
+    const uint16_t *xb0 = GLU ? x.hi : x.hi + (int64_t)first * x.pitch, *xb1 = GLU ? nullptr : x.lo + (int64_t)first * x.pitch;
+    const uint4 *xbs = GLU ? x.sums : x.sums + (int64_t)first * (x.pitch / 32);
+    auto row_of = [&](int m) -> uint32_t {  // GLU: the token; otherwise the place in the tile
+        const int in = min(m, count - 1);
+        return (uint32_t)(GLU ? pl.pair[first + in] / k : in);
     };
-    uint32_t srow[TM];
+    uint32_t xo[TM], so = 0;
 #pragma unroll
-    for (int t = 0; t < TM; t++)
-        srow[t] = (uint32_t)row_of((tid + 256 * t) / 16);
-    static_assert(!SUMS || 4 * BM <= 256, "one sum per thread");
-    const int64_t sumrow = SUMS ? row_of(min(tid / 4, BM - 1)) * (x.pitch / 32) + (tid & 3) : 0;
-    uint4 xr[PL][TM], xsum;
-    auto load_x = [&](int s) {
+    for (int t = 0; t < TM; t++) {
+        const int m = 4 * (TM * wave + t) + (lane >> 4);
+        xo[t] = row_of(m) * (uint32_t)(2 * x.pitch) + 16u * ((lane & 15) ^ (m & 15));
+    }
+    if constexpr (SUMS) {
+        const int m = 4 * TM * wave + (lane >> 2);
+        so = row_of(m) * (uint32_t)(x.pitch / 2) + 16u * ((lane & 3) ^ ((m >> 2) & 3));
+    }
+    static_assert(!SUMS || TM == 4, "a wave stages the sums of 16 rows");
+    auto load_x = [&](int s, int buf) {
+        const uint32_t at = lds_addr(smem + buf * BUF) + 1024 * TM * wave;
 #pragma unroll
-        for (int t = 0; t < TM; t++)
-#pragma unroll
-            for (int p = 0; p < PL; p++)
-                xr[p][t] = *reinterpret_cast<const uint4 *>((p ? x.lo : x.hi) + srow[t] * x.pitch + 128 * s + 8 * (tid & 15));
+        for (int t = 0; t < TM; t++) {
+            dma16(xb0 + 128 * s, xo[t], at + 1024 * t);
+            if constexpr (!GLU)
+                dma16(xb1 + 128 * s, xo[t], at + PLANE + 1024 * t);
+        }
         if constexpr (SUMS)
-            xsum = x.sums[sumrow + 4 * s];
+            dma16(xbs + 4 * s, so, lds_addr(smem + buf * BUF + PL * PLANE) + 1024 * wave);
     };
-    auto store_x = [&](int buf) {
-        uint8_t *b = smem + buf * BUF;
-#pragma unroll
-        for (int t = 0; t < TM; t++)
-#pragma unroll
-            for (int p = 0; p < PL; p++)
-                *reinterpret_cast<uint4 *>(b + p * BM * PX + ((tid + 256 * t) / 16) * PX + 16 * (tid & 15)) = xr[p][t];
-        if constexpr (SUMS)
-            if (4 * BM == 256 || tid < 4 * BM)
-                *reinterpret_cast<uint4 *>(b + PL * BM * PX + (tid / 4) * PS + 16 * (tid & 3)) = xsum;
-    };
-    load_x(0);
+    load_x(0, 0);
     load_w(0);
-    store_x(0);
-    load_x(min(1, slabs - 1));
-    lds_barrier();
+    loads_barrier();
     for (int s = 0; s < slabs; s++) {
         const uint8_t *sx = smem + (s & 1) * BUF;
         Tile16<FMT> cur[NT];
 #pragma unroll
         for (int i = 0; i < NT; i++)
             cur[i] = raw[i];
+        if (s + 1 < slabs)
+            load_x(s + 1, (s + 1) & 1);
         load_w(min(s + 1, slabs - 1));
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (RUN) {
             if ((s & 1) == 0) {
 #pragma unroll
@@ -1474,16 +1589,16 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
             f16x8_t o[NT][2][PER<FMT>];
 #pragma unroll
             for (int i = 0; i < NT; i++)
-                decode_half<FMT>(cur[i], s, g, h, o[i]);
+                decode_half<FMT>(nb, cur[i], s, g, h, o[i]);
 #pragma unroll
             for (int j = 0; j < TM; j++) {
 #pragma unroll
                 for (int q = 0; q < 2; q++) {
-                    const uint8_t *p = sx + (16 * j + r16) * PX + slab_at<FMT>(2 * h + q, g);
+                    const uint8_t *p = sx + 256 * (16 * j + r16) + (slab_at<FMT>(2 * h + q, g) ^ (16 * r16));
                     const f16x8_t xh = *reinterpret_cast<const f16x8_t *>(p);
                     f16x8_t xl;
                     if constexpr (!GLU)
-                        xl = *reinterpret_cast<const f16x8_t *>(p + BM * PX);
+                        xl = *reinterpret_cast<const f16x8_t *>(p + PLANE);
                     if constexpr (RUN) {
 #pragma unroll
                         for (int c = 0; c < PER<FMT>; c++)
@@ -1525,15 +1640,13 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
                 mo[i] = min_entry(-f16_bits_to_f32(cur[i].h.x >> 16) * min_code(cur[i], s, g) * __builtin_amdgcn_rcpf(D[i]));
 #pragma unroll
             for (int j = 0; j < TM; j++) {
-                const bf16x8_t xs = *reinterpret_cast<const bf16x8_t *>(sx + PL * BM * PX + (16 * j + r16) * PS + 16 * g);
+                const bf16x8_t xs = *reinterpret_cast<const bf16x8_t *>(sx + PL * PLANE + 64 * (16 * j + r16) + 16 * (g ^ ((r16 >> 2) & 3)));
 #pragma unroll
                 for (int i = 0; i < NT; i++)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs, mo[i], acc[i][j], 0, 0, 0);
             }
         }
-        store_x((s + 1) & 1);
-        load_x(min(s + 2, slabs - 1));
-        lds_barrier();
+        loads_barrier();
     }
     if constexpr (RUN) {
 #pragma unroll
@@ -1749,7 +1862,7 @@ hipError_t gemm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, in
     return gemm<FMT, 4, 2, GLU>(a, l, pl, max_tiles, s);
 }
 
-template <int FMT, int TM, bool GLU>
+template <int FMT, int TM, bool GLU, bool TAIL>
 hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, hipStream_t s)
 {
     constexpr int NT = 4;
@@ -1768,10 +1881,10 @@ hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, 
     float *out = f32(GLU ? l.h32 : l.pd);
     const int64_t pitch = GLU ? l.fp : a.K;
     if constexpr (THIN)
-        moe_thin_kernel<FMT, TM, NT, GLU><<<dim3((unsigned)grid), GLU ? 256 : 512, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk,
+        moe_thin_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), GLU ? 256 : 512, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk,
                                                                                          a.act, out, pitch);
     else
-        moe_wide_kernel<FMT, TM, NT, GLU><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk, a.act, out,
+        moe_wide_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk, a.act, out,
                                                                               pitch);
     return hipGetLastError();
 }
@@ -1779,11 +1892,15 @@ hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, 
 template <int FMT, bool GLU>
 hipError_t mm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, int max_tiles, hipStream_t s)
 {
-    if (tm == 1)
-        return mm<FMT, 1, GLU>(a, l, pl, max_tiles, s);
-    if (tm == 2)
-        return mm<FMT, 2, GLU>(a, l, pl, max_tiles, s);
-    return mm<FMT, 4, GLU>(a, l, pl, max_tiles, s);
+    if constexpr (FMT == FMT_Q8_0) {
+        if ((GLU ? a.K : a.F) % 128 != 0)
+            return tm == 1   ? mm<FMT, 1, GLU, true>(a, l, pl, max_tiles, s)
+                   : tm == 2 ? mm<FMT, 2, GLU, true>(a, l, pl, max_tiles, s)
+                             : mm<FMT, 4, GLU, true>(a, l, pl, max_tiles, s);
+    }
+    return tm == 1   ? mm<FMT, 1, GLU, false>(a, l, pl, max_tiles, s)
+           : tm == 2 ? mm<FMT, 2, GLU, false>(a, l, pl, max_tiles, s)
+                     : mm<FMT, 4, GLU, false>(a, l, pl, max_tiles, s);
 }
 
 template <bool GLU>
@@ -1829,7 +1946,8 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
     const int max_tiles = P / BM + (P < a.E ? P : a.E);
     const Plan pl{reinterpret_cast<int32_t *>(a.ws + l.tiles), reinterpret_cast<int32_t *>(a.ws + l.pair),
                   reinterpret_cast<int32_t *>(a.ws + l.place)};
-    if (digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d)) {
+    // (offsets inside an expert's planes and inside X are 32 bits there)
+    if (digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d) && a.F * a.K < (int64_t(1) << 31) && 2 * a.T * l.kp < (int64_t(1) << 32)) {
         moe_prep_kernel<<<a.T + 1, 1024, 0, s>>>(
             a.ids, P, a.E, BM, pl, a.X, a.T, a.K, reinterpret_cast<uint16_t *>(a.ws + l.xh),
             reinterpret_cast<uint4 *>(a.ws + l.xsum), reinterpret_cast<float *>(a.ws + l.xunit), l.kp);
