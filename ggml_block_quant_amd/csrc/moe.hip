@@ -1052,14 +1052,18 @@ struct Acts16 {          // activations of a product
     const uint16_t *lo;  // H only
     const uint4 *sums;   // [rows][pitch / 32]: sum_entry of the blocks
     const float *unit;   // [rows]: 2^-e
-    int64_t pitch;       // a multiple of 128, zeros past the row's end
+    int64_t pitch;       // a multiple of 256, zeros past the row's end
 };
 
-// What a lane loads of one row tile and slab, and its operands.
-template <int FMT> struct Tile16;
-template <> struct Tile16<FMT_Q4K> { uint4 c, h; };
-template <> struct Tile16<FMT_Q6K> { uint4 c; uint2 hi; uint32_t sc, d; };
-template <> struct Tile16<FMT_Q8_0> { uint2 c[4]; uint32_t d[2]; };
+// What a lane loads of one row tile: the codes of a slab, and what a group of
+// 256 (two slabs) shares.
+template <int FMT> struct Codes16;
+template <> struct Codes16<FMT_Q4K> { uint4 c; };
+template <> struct Codes16<FMT_Q6K> { uint4 c; uint2 hi; uint32_t sc; };
+template <> struct Codes16<FMT_Q8_0> { uint2 c[4]; uint32_t d[2]; };
+template <int FMT> struct Head16 { };
+template <> struct Head16<FMT_Q4K> { uint4 h; };
+template <> struct Head16<FMT_Q6K> { uint32_t d; };
 
 // One expert's matrix: the planes at its first row (the same for the whole
 // wave) and 32-bit byte offsets of a lane's row in them, so that a slab's
@@ -1104,21 +1108,20 @@ __device__ __forceinline__ Row16 row_offsets(int K, int row, int g)
         return Row16{r * k + 8u * g, 0u, r * (k / 16)};
 }
 
-// TAIL: Q8_0 rows that end inside a slab (their last block again past it; X is
-// zero there)
+// slab 2 G + u.  Q8_0 rows may end before a whole group: the last slab again
+// past it, or, TAIL, where they end inside a slab, the last block (X is zero there)
 template <int FMT, bool TAIL>
-__device__ __forceinline__ void load_tile(const Planes16 &w, const Row16 &r, int s, int g, Tile16<FMT> &t)
+__device__ __forceinline__ void load_codes(const Planes16 &w, const Row16 &r, int G, int u, int g, Codes16<FMT> &t)
 {
     if constexpr (FMT == FMT_Q4K) {
-        t.c = stream16(w.codes + 64 * s + r.codes);
-        t.h = *reinterpret_cast<const uint4 *>(w.sc + 16 * (s >> 1) + r.sc);
+        t.c = *reinterpret_cast<const uint4 *>(w.codes + 128 * G + 64 * u + r.codes);
     } else if constexpr (FMT == FMT_Q6K) {
-        const uint8_t *c = w.codes + 192 * (s >> 1) + 64 * (s & 1), *h = w.codes + 192 * (s >> 1) + 128 + 32 * (s & 1);
-        t.c = stream16(c + (r.codes + 16u * g));
+        const uint8_t *c = w.codes + 192 * G + 64 * u, *h = w.codes + 192 * G + 128 + 32 * u;
+        t.c = *reinterpret_cast<const uint4 *>(c + (r.codes + 16u * g));
         t.hi = *reinterpret_cast<const uint2 *>(h + (r.codes + 8u * g));
-        t.sc = *reinterpret_cast<const uint16_t *>(w.sc + 16 * (s >> 1) + 8 * (s & 1) + r.sc);
-        t.d = *reinterpret_cast<const uint16_t *>(w.d + 2 * (s >> 1) + r.d);
+        t.sc = *reinterpret_cast<const uint16_t *>(w.sc + 16 * G + 8 * u + r.sc);
     } else if constexpr (!TAIL) {
+        const int s = min(2 * G + u, w.K / 128 - 1);
 #pragma unroll
         for (int i = 0; i < 4; i++)
             t.c[i] = *reinterpret_cast<const uint2 *>(w.codes + 128 * s + 32 * i + r.codes);
@@ -1128,12 +1131,20 @@ __device__ __forceinline__ void load_tile(const Planes16 &w, const Row16 &r, int
         uint32_t d[4];
 #pragma unroll
         for (int i = 0; i < 4; i++) {
-            const int b = min(4 * s + i, w.K / 32 - 1);
+            const int b = min(8 * G + 4 * u + i, w.K / 32 - 1);
             t.c[i] = *reinterpret_cast<const uint2 *>(w.codes + 32 * b + r.codes);
             d[i] = *reinterpret_cast<const uint16_t *>(w.d + 2 * b + r.d);
         }
         t.d[0] = d[0] | d[1] << 16, t.d[1] = d[2] | d[3] << 16;
     }
+}
+template <int FMT>
+__device__ __forceinline__ void load_head(const Planes16 &w, const Row16 &r, int G, Head16<FMT> &t)
+{
+    if constexpr (FMT == FMT_Q4K)
+        t.h = *reinterpret_cast<const uint4 *>(w.sc + 16 * G + r.sc);
+    else if constexpr (FMT == FMT_Q6K)
+        t.d = *reinterpret_cast<const uint16_t *>(w.d + 2 * G + r.d);
 }
 
 // (a & mask) | 0x64006400 in one instruction: the mask in a register, the
@@ -1159,12 +1170,12 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c
 // the fp16 operands of steps 2 h, 2 h + 1 of a slab (h = 0, 1)
 template <int FMT> constexpr int PER = FMT == FMT_Q6K ? 2 : 1;  // operands per step
 template <int FMT>
-__device__ __forceinline__ void decode_half(const Nibbles &nb, const Tile16<FMT> &t, int s, int g, int h,
-                                            f16x8_t (&o)[2][PER<FMT>])
+__device__ __forceinline__ void decode_half(const Nibbles &nb, const Codes16<FMT> &t, const Head16<FMT> &hd, int u, int g,
+                                            int h, f16x8_t (&o)[2][PER<FMT>])
 {
     if constexpr (FMT == FMT_Q4K) {
-        const int j = 4 * (s & 1) + g;
-        const uint32_t sc = __builtin_amdgcn_ubfe(t.h.y, 4 * j, 4) | (__builtin_amdgcn_ubfe(t.h.w, 2 * j, 2) << 4);
+        const int j = 4 * u + g;
+        const uint32_t sc = __builtin_amdgcn_ubfe(hd.h.y, 4 * j, 4) | (__builtin_amdgcn_ubfe(hd.h.w, 2 * j, 2) << 4);
         const _Float16 sh = (_Float16)(float)sc;
         const f16x2_t S = {sh, sh}, S16 = S * (_Float16)0.0625f, N = S * (_Float16)-1024.0f, N16 = S * (_Float16)-64.0f;
         const uint32_t cw[2] = {h ? t.c.z : t.c.x, h ? t.c.w : t.c.y};
@@ -1209,14 +1220,14 @@ __device__ __forceinline__ void decode_half(const Nibbles &nb, const Tile16<FMT>
     }
 }
 
-// scale of the slab's 256 (Q4K, Q6K) or of its block i (Q8_0)
+// scale of the group (Q4K, Q6K) or of the slab's block i (Q8_0)
 template <int FMT>
-__device__ __forceinline__ float scale_of(const Tile16<FMT> &t, int i)
+__device__ __forceinline__ float scale_of(const Codes16<FMT> &t, const Head16<FMT> &hd, int i)
 {
     if constexpr (FMT == FMT_Q4K)
-        return f16_bits_to_f32(t.h.x);
+        return f16_bits_to_f32(hd.h.x);
     else if constexpr (FMT == FMT_Q6K)
-        return f16_bits_to_f32(t.d);
+        return f16_bits_to_f32(hd.d);
     else
         return f16_bits_to_f32(t.d[i >> 1] >> (16 * (i & 1)));
 }
@@ -1226,10 +1237,10 @@ __device__ __forceinline__ bf16x8_t min_entry1(float v)
     const uint32_t h = __float_as_uint(v) >> 16;
     return __builtin_bit_cast(bf16x8_t, make_uint4(h, h, h << 16, 0u));
 }
-// Q4K: the 6-bit minimum of the lane's block
-__device__ __forceinline__ float min_code(const Tile16<FMT_Q4K> &t, int s, int g)
+// Q4K: the 6-bit minimum of the lane's block of slab u
+__device__ __forceinline__ float min_code(const Head16<FMT_Q4K> &t, int u, int g)
 {
-    const int j = 4 * (s & 1) + g;
+    const int j = 4 * u + g;
     return (float)(__builtin_amdgcn_ubfe(t.h.z, 4 * j, 4) | (__builtin_amdgcn_ubfe(t.h.w, 16 + 2 * j, 2) << 4));
 }
 
@@ -1254,11 +1265,14 @@ __device__ __forceinline__ void dma16(const void *base, uint32_t off, uint32_t l
                  : "memory", "m0");
 }
 #pragma clang diagnostic pop
-// every load of this wave is in, then the workgroup's
+// This wave's direct loads are in -- all its loads but the last AFTER, which
+// were issued after them (loads return in order) -- then the workgroup's.
+template <int AFTER>
 __device__ __forceinline__ void loads_barrier()
 {
+    static_assert(AFTER < 16, "low bits of vmcnt");
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt(0x0070 | AFTER);  // vmcnt AFTER, lgkmcnt 0
     __builtin_amdgcn_s_barrier();
     __atomic_signal_fence(__ATOMIC_SEQ_CST);
 }
@@ -1266,26 +1280,28 @@ __device__ __forceinline__ void loads_barrier()
 __device__ __forceinline__ f32x4_t mfma16(f16x8_t a, f16x8_t b, f32x4_t c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
 
 // Work order: the tiles of one expert share its weights and the blocks of one
-// tile its activations, so workgroups that run together take 8 tiles x 8
-// blocks, and each XCD (workgroup id modulo 8) takes a contiguous part.
-__device__ __forceinline__ bool place_of_block(int ntiles, int nblk, int &tile, int &blk)
+// tile its activations, so each XCD (workgroup id modulo 8) takes a contiguous
+// part of an order that walks `band` tiles across all blocks.
+struct Order {
+    int nblk, band;
+};
+__device__ __forceinline__ bool place_of_block(int ntiles, const Order &o, int &tile, int &blk)
 {
-    const int64_t total = (int64_t)ntiles * nblk, per = (total + 7) / 8;
+    const int64_t total = (int64_t)ntiles * o.nblk, per = (total + 7) / 8;
     const int64_t bid = blockIdx.x, at = (bid & 7) * per + (bid >> 3);
     if ((bid >> 3) >= per || at >= total)
         return false;
-    const int band = (int)(at / ((int64_t)nblk * 8));         // 8 tiles
-    const int tiles = min(8, ntiles - 8 * band);
-    const int in = (int)(at - (int64_t)band * nblk * 8);
+    const int band = (int)(at / ((int64_t)o.nblk * o.band));
+    const int tiles = min(o.band, ntiles - o.band * band);
+    const int in = (int)(at - (int64_t)band * o.nblk * o.band);
     blk = in / tiles;
-    tile = 8 * band + in % tiles;
+    tile = o.band * band + in % tiles;
     return true;
 }
 
-
 // What the two kernels share: the tile, the rows, the results.
 // GLU: row tiles i < NT / 2 are gate rows, the others the same rows of up;
-// H[place][column] = act(gate) * up in fp32 (columns past the row: 0).
+// H[place][column] = act(gate) * up in fp32.
 template <bool GLU, int NT, int TM>
 __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], const Acts16 &x, const Plan &pl, int k, int first,
                                               int count, int64_t n_wave, int64_t N, int64_t pitch, int act,
@@ -1306,8 +1322,8 @@ __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], cons
             for (int i = 0; i < NF; i++) {
                 const int64_t n = n_wave + 16 * i + r16;
                 if constexpr (GLU) {
-                    if (n < pitch)
-                        out[at * pitch + n] = n < N ? act_f32(act, acc[i][j][e] * u) * (acc[i + NF][j][e] * u) : 0.0f;
+                    if (n < N)
+                        out[at * pitch + n] = act_f32(act, acc[i][j][e] * u) * (acc[i + NF][j][e] * u);
                 } else {
                     if (n < N)
                         out[at * pitch + n] = acc[i][j][e] * u;
@@ -1318,13 +1334,13 @@ __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], cons
 
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
-                                                                  int nblk, int act, float *__restrict__ out,
+                                                                  Order order, int act, float *__restrict__ out,
                                                                   int64_t out_pitch)
 {
     constexpr int WAVES = GLU ? 4 : 8, NF = GLU ? NT / 2 : NT;
     __shared__ f32x4_t red[GLU ? 1 : WAVES * NT * TM * 64];
     int ti, blk;
-    if (!place_of_block(pl.tiles[0], nblk, ti, blk))
+    if (!place_of_block(pl.tiles[0], order, ti, blk))
         return;
     const int4 tile = reinterpret_cast<const int4 *>(pl.tiles + 4)[ti];
     const int expert = tile.x, first = tile.y, count = tile.z;
@@ -1345,11 +1361,14 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
         for (int j = 0; j < TM; j++)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const Nibbles nb = make_nibbles();
-    Tile16<FMT> raw[NT];
+    Codes16<FMT> raw[NT];
+    Head16<FMT> rawh[NT];
     auto load_w = [&](int s) {
 #pragma unroll
-        for (int i = 0; i < NT; i++)
-            load_tile<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s, g, raw[i]);
+        for (int i = 0; i < NT; i++) {
+            load_codes<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s >> 1, s & 1, g, raw[i]);
+            load_head<FMT>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s >> 1, rawh[i]);
+        }
     };
     // the lane's token of each tile (past the end: the last one)
     const uint16_t *ahi[TM], *alo[TM];
@@ -1385,10 +1404,13 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
     for (int s = s0; s < s1; s++) {
         f16x8_t xh[TM][4], xl[TM][4];
         bf16x8_t xs[TM];
-        Tile16<FMT> cur[NT];
+        Codes16<FMT> cur[NT];
+        Head16<FMT> hd[NT];
 #pragma unroll
-        for (int i = 0; i < NT; i++)
+        for (int i = 0; i < NT; i++) {
             cur[i] = raw[i];
+            hd[i] = rawh[i];
+        }
 #pragma unroll
         for (int j = 0; j < TM; j++) {
 #pragma unroll
@@ -1414,7 +1436,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 #pragma unroll
             for (int h = 0; h < 2; h++) {
                 f16x8_t o[2][PER<FMT>];
-                decode_half<FMT>(nb, cur[i], s, g, h, o);
+                decode_half<FMT>(nb, cur[i], hd[i], s & 1, g, h, o);
 #pragma unroll
                 for (int j = 0; j < TM; j++)
 #pragma unroll
@@ -1426,7 +1448,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
                                 p[j] = mfma16(xl[j][2 * h + q], o[q][c], p[j]);
                         }
                         if constexpr (FMT == FMT_Q8_0) {
-                            const float d = scale_of<FMT>(cur[i], 2 * h + q);
+                            const float d = scale_of<FMT>(cur[i], hd[i], 2 * h + q);
 #pragma unroll
                             for (int e = 0; e < 4; e++)
                                 acc[i][j][e] = fmaf(d, p[j][e], acc[i][j][e]);
@@ -1435,7 +1457,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
                     }
             }
             if constexpr (FMT != FMT_Q8_0) {
-                const float d = scale_of<FMT>(cur[i], 0);
+                const float d = scale_of<FMT>(cur[i], hd[i], 0);
 #pragma unroll
                 for (int j = 0; j < TM; j++)
 #pragma unroll
@@ -1443,8 +1465,8 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
                         acc[i][j][e] = fmaf(d, p[j][e], acc[i][j][e]);
             }
             if constexpr (FMT == FMT_Q4K) {
-                const float dm = f16_bits_to_f32(cur[i].h.x >> 16);
-                const bf16x8_t mo = min_entry1(min_code(cur[i], s, g));
+                const float dm = f16_bits_to_f32(hd[i].h.x >> 16);
+                const bf16x8_t mo = min_entry1(min_code(hd[i], s & 1, g));
 #pragma unroll
                 for (int j = 0; j < TM; j++) {
                     const f32x4_t q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[j], mo, zero, 0, 0, 0);
@@ -1482,7 +1504,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 // D), which needs no second set of accumulators; Q4K's minimums enter as
 // -(dmin / D) m.  Q8_0 adds each block's products times its scale.
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
-__global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, int nblk,
+__global__ __launch_bounds__(256, NT == 2 ? 3 : 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, Order order,
                                                           int act, float *__restrict__ out, int64_t out_pitch)
 {
     constexpr int BM = 16 * TM, PL = GLU ? 1 : 2, NF = GLU ? NT / 2 : NT;
@@ -1495,14 +1517,14 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
     constexpr int PLANE = BM * 256, BUF = PL * PLANE + (SUMS ? BM * 64 : 0);
     __shared__ __attribute__((aligned(16))) uint8_t smem[2 * BUF];
     int ti, blk;
-    if (!place_of_block(pl.tiles[0], nblk, ti, blk))
+    if (!place_of_block(pl.tiles[0], order, ti, blk))
         return;
     const int4 tile = reinterpret_cast<const int4 *>(pl.tiles + 4)[ti];
     const int expert = tile.x, first = tile.y, count = tile.z;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r16 = lane & 15;
     const int64_t K = w0.K, n_wave = (int64_t)blk * (64 * NF) + wave * 16 * NF;
-    const int slabs = (int)((K + 127) / 128);
+    const int groups = (int)((K + 255) / 256);
     const Planes16 e0 = expert_planes<FMT>(w0, expert * N), e1 = expert_planes<FMT>(w1, expert * N);
     Row16 wrow[NF];
 #pragma unroll
@@ -1519,11 +1541,19 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
     for (int i = 0; i < NT; i++)
         D[i] = 1.0f;
     const Nibbles nb = make_nibbles();
-    Tile16<FMT> raw[NT];
-    auto load_w = [&](int s) {
+    // two slabs of codes in flight where they fit the registers
+    constexpr int RAWS = FMT == FMT_Q4K || NT == 2 ? 2 : 1;
+    Codes16<FMT> raw[RAWS][NT];
+    Head16<FMT> hd[NT], nhd[NT];
+    auto load_c = [&](int G, int u) {
 #pragma unroll
         for (int i = 0; i < NT; i++)
-            load_tile<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s, g, raw[i]);
+            load_codes<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, u, g, raw[u % RAWS][i]);
+    };
+    auto load_h = [&](int G) {
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            load_head<FMT>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, nhd[i]);
     };
     // Wave w stages rows 16 w TM / 4 .., four rows of 256 bytes a load, and
     // the sums of as many rows, 16 rows a load.
@@ -1533,17 +1563,20 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
         const int in = min(m, count - 1);
         return (uint32_t)(GLU ? pl.pair[first + in] / k : in);
     };
-    uint32_t xo[TM], so = 0;
+    uint32_t xo[TM], so[TM / 4];
 #pragma unroll
     for (int t = 0; t < TM; t++) {
         const int m = 4 * (TM * wave + t) + (lane >> 4);
         xo[t] = row_of(m) * (uint32_t)(2 * x.pitch) + 16u * ((lane & 15) ^ (m & 15));
     }
+    static_assert(TM % 4 == 0, "a wave stages the sums of 4 TM rows, 16 a load");
     if constexpr (SUMS) {
-        const int m = 4 * TM * wave + (lane >> 2);
-        so = row_of(m) * (uint32_t)(x.pitch / 2) + 16u * ((lane & 3) ^ ((m >> 2) & 3));
+#pragma unroll
+        for (int t = 0; t < TM / 4; t++) {
+            const int m = 16 * (TM / 4 * wave + t) + (lane >> 2);
+            so[t] = row_of(m) * (uint32_t)(x.pitch / 2) + 16u * ((lane & 3) ^ ((m >> 2) & 3));
+        }
     }
-    static_assert(!SUMS || TM == 4, "a wave stages the sums of 16 rows");
     auto load_x = [&](int s, int buf) {
         const uint32_t at = lds_addr(smem + buf * BUF) + 1024 * TM * wave;
 #pragma unroll
@@ -1552,101 +1585,141 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
             if constexpr (!GLU)
                 dma16(xb1 + 128 * s, xo[t], at + PLANE + 1024 * t);
         }
-        if constexpr (SUMS)
-            dma16(xbs + 4 * s, so, lds_addr(smem + buf * BUF + PL * PLANE) + 1024 * wave);
+        if constexpr (SUMS) {
+#pragma unroll
+            for (int t = 0; t < TM / 4; t++)
+                dma16(xbs + 4 * s, so[t], lds_addr(smem + buf * BUF + PL * PLANE) + 1024 * (TM / 4 * wave + t));
+        }
+    };
+    // operand pieces of the activations: step 2 h + q, tile j of the slab in sx
+    struct Piece {
+        f16x8_t h[2], l[2];
+    };
+    auto load_piece = [&](const uint8_t *sx, int h, int j, Piece &f) {
+#pragma unroll
+        for (int q = 0; q < 2; q++) {
+            const uint8_t *p = sx + 256 * (16 * j + r16) + (slab_at<FMT>(2 * h + q, g) ^ (16 * r16));
+            f.h[q] = *reinterpret_cast<const f16x8_t *>(p);
+            if constexpr (!GLU)
+                f.l[q] = *reinterpret_cast<const f16x8_t *>(p + PLANE);
+        }
     };
     load_x(0, 0);
-    load_w(0);
-    loads_barrier();
-    for (int s = 0; s < slabs; s++) {
-        const uint8_t *sx = smem + (s & 1) * BUF;
-        Tile16<FMT> cur[NT];
-#pragma unroll
-        for (int i = 0; i < NT; i++)
-            cur[i] = raw[i];
-        if (s + 1 < slabs)
-            load_x(s + 1, (s + 1) & 1);
-        load_w(min(s + 1, slabs - 1));
-        __builtin_amdgcn_sched_barrier(0);
+    load_c(0, 0);
+    if constexpr (RAWS == 2)
+        load_c(0, 1);
+    load_h(0);
+    loads_barrier<0>();
+    // At least this many of a slab's weight loads are issued after its direct
+    // loads and may still be on the way at its end (Q4K: a 16-byte load a row
+    // tile, and the heads' in the first slab; the others have more).
+    constexpr int AFTER0 = 2 * NT, AFTER1 = FMT == FMT_Q4K ? NT : 2 * NT;
+    for (int G = 0; G < groups; G++) {
+        const int next = min(G + 1, groups - 1);
+        float rD[NT];  // 1 / D
         if constexpr (RUN) {
-            if ((s & 1) == 0) {
 #pragma unroll
-                for (int i = 0; i < NT; i++) {
-                    const float d = scale_of<FMT>(cur[i], 0), dn = d != 0.0f ? d : D[i];
-                    // D / dn to half a step: quotient and one correction
-                    const float rc = __builtin_amdgcn_rcpf(dn), q0 = D[i] * rc, rho = fmaf(fmaf(-dn, q0, D[i]), rc, q0);
-                    D[i] = dn;
+            for (int i = 0; i < NT; i++) {
+                hd[i] = nhd[i];
+                const float d = scale_of<FMT>(raw[0][i], hd[i], 0), dn = d != 0.0f ? d : D[i];
+                // D / dn to half a step: quotient and one correction
+                rD[i] = __builtin_amdgcn_rcpf(dn);
+                const float q0 = D[i] * rD[i], rho = fmaf(fmaf(-dn, q0, D[i]), rD[i], q0);
+                D[i] = dn;
 #pragma unroll
-                    for (int j = 0; j < TM; j++)
+                for (int j = 0; j < TM; j++)
 #pragma unroll
-                        for (int e = 0; e < 4; e++)
-                            acc[i][j][e] *= rho;
-                }
+                    for (int e = 0; e < 4; e++)
+                        acc[i][j][e] *= rho;
             }
         }
 #pragma unroll
-        for (int h = 0; h < 2; h++) {
-            f16x8_t o[NT][2][PER<FMT>];
+        for (int u = 0; u < 2; u++) {
+            const uint8_t *sx = smem + u * BUF;
+            // the next slab of X into the other buffer, whose readers are behind the
+            // last barrier (past the end the last one again)
+            load_x(min(2 * G + u + 1, 2 * groups - 1), 1 - u);
+            Piece f[2];
+            load_piece(sx, 0, 0, f[0]);
 #pragma unroll
-            for (int i = 0; i < NT; i++)
-                decode_half<FMT>(nb, cur[i], s, g, h, o[i]);
+            for (int h = 0; h < 2; h++) {
+                f16x8_t o[NT][2][PER<FMT>];
+                float sc[NT][2];
 #pragma unroll
-            for (int j = 0; j < TM; j++) {
+                for (int i = 0; i < NT; i++) {
+                    decode_half<FMT>(nb, raw[u % RAWS][i], hd[i], u, g, h, o[i]);
+                    if constexpr (!RUN) {
+                        sc[i][0] = scale_of<FMT>(raw[u % RAWS][i], hd[i], 2 * h);
+                        sc[i][1] = scale_of<FMT>(raw[u % RAWS][i], hd[i], 2 * h + 1);
+                    }
+                }
+                if (h == 1) {  // these codes are spent: later ones take their registers
+                    load_c(RAWS == 2 || u == 1 ? next : G, RAWS == 2 ? u : 1 - u);
+                    if (u == 0)
+                        load_h(next);
+                }
 #pragma unroll
-                for (int q = 0; q < 2; q++) {
-                    const uint8_t *p = sx + 256 * (16 * j + r16) + (slab_at<FMT>(2 * h + q, g) ^ (16 * r16));
-                    const f16x8_t xh = *reinterpret_cast<const f16x8_t *>(p);
-                    f16x8_t xl;
-                    if constexpr (!GLU)
-                        xl = *reinterpret_cast<const f16x8_t *>(p + PLANE);
+                for (int j = 0; j < TM; j++) {
+                    // the next piece is read before this one's products
+                    const int at = h * TM + j;
+                    if (at + 1 < 2 * TM)
+                        load_piece(sx, (at + 1) / TM, (at + 1) % TM, f[(at + 1) & 1]);
+                    if constexpr (!GLU)  // (GLU: fewer registers without it, 1.49 -> 1.41 ms at 2048 tokens)
+                        __builtin_amdgcn_sched_barrier(0x16);  // VALU, SALU and VMEM may move across
+                    const Piece &x16 = f[at & 1];
                     if constexpr (RUN) {
 #pragma unroll
-                        for (int c = 0; c < PER<FMT>; c++)
+                        for (int q = 0; q < 2; q++)
 #pragma unroll
-                            for (int i = 0; i < NT; i++)
-                                acc[i][j] = mfma16(xh, o[i][q][c], acc[i][j]);
-                        if constexpr (!GLU) {
-#pragma unroll
-                            for (int c = 0; c < PER<FMT>; c++)
+                            for (int c = 0; c < PER<FMT>; c++) {
 #pragma unroll
                                 for (int i = 0; i < NT; i++)
-                                    acc[i][j] = mfma16(xl, o[i][q][c], acc[i][j]);
-                        }
-                    } else {
-                        f32x4_t v[NT];
+                                    acc[i][j] = mfma16(x16.h[q], o[i][q][c], acc[i][j]);
+                                if constexpr (!GLU) {
 #pragma unroll
-                        for (int i = 0; i < NT; i++)
-                            v[i] = mfma16(xh, o[i][q][0], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
-                        if constexpr (!GLU) {
+                                    for (int i = 0; i < NT; i++)
+                                        acc[i][j] = mfma16(x16.l[q], o[i][q][c], acc[i][j]);
+                                }
+                            }
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; q++) {
+                            f32x4_t v[NT];
 #pragma unroll
                             for (int i = 0; i < NT; i++)
-                                v[i] = mfma16(xl, o[i][q][0], v[i]);
-                        }
+                                v[i] = mfma16(x16.h[q], o[i][q][0], f32x4_t{0.0f, 0.0f, 0.0f, 0.0f});
+                            if constexpr (!GLU) {
 #pragma unroll
-                        for (int i = 0; i < NT; i++) {
-                            const float d = scale_of<FMT>(cur[i], 2 * h + q);
+                                for (int i = 0; i < NT; i++)
+                                    v[i] = mfma16(x16.l[q], o[i][q][0], v[i]);
+                            }
 #pragma unroll
-                            for (int e = 0; e < 4; e++)
-                                acc[i][j][e] = fmaf(d, v[i][e], acc[i][j][e]);
+                            for (int i = 0; i < NT; i++)
+#pragma unroll
+                                for (int e = 0; e < 4; e++)
+                                    acc[i][j][e] = fmaf(sc[i][q], v[i][e], acc[i][j][e]);
                         }
                     }
                 }
             }
-        }
-        if constexpr (SUMS) {
-            bf16x8_t mo[NT];
-#pragma unroll
-            for (int i = 0; i < NT; i++)
-                mo[i] = min_entry(-f16_bits_to_f32(cur[i].h.x >> 16) * min_code(cur[i], s, g) * __builtin_amdgcn_rcpf(D[i]));
-#pragma unroll
-            for (int j = 0; j < TM; j++) {
-                const bf16x8_t xs = *reinterpret_cast<const bf16x8_t *>(sx + PL * PLANE + 64 * (16 * j + r16) + 16 * (g ^ ((r16 >> 2) & 3)));
+            if constexpr (SUMS) {
+                bf16x8_t mo[NT];
 #pragma unroll
                 for (int i = 0; i < NT; i++)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs, mo[i], acc[i][j], 0, 0, 0);
+                    mo[i] = min_entry(-f16_bits_to_f32(hd[i].h.x >> 16) * min_code(hd[i], u, g) * rD[i]);
+#pragma unroll
+                for (int j = 0; j < TM; j++) {
+                    const bf16x8_t xs = *reinterpret_cast<const bf16x8_t *>(sx + PL * PLANE + 64 * (16 * j + r16) + 16 * (g ^ ((r16 >> 2) & 3)));
+#pragma unroll
+                    for (int i = 0; i < NT; i++)
+                        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs, mo[i], acc[i][j], 0, 0, 0);
+                }
             }
+            if (u == 0)
+                loads_barrier<AFTER0>();
+            else
+                loads_barrier<AFTER1>();
         }
-        loads_barrier();
     }
     if constexpr (RUN) {
 #pragma unroll
@@ -1741,13 +1814,13 @@ __global__ __launch_bounds__(1024) void moe_prep_kernel(const int32_t *__restric
 }
 
 // H of the sorted pairs for the down product
-__global__ __launch_bounds__(512) void moe_h_kernel(const float *__restrict__ H, Plan pl, uint16_t *__restrict__ hi,
+__global__ __launch_bounds__(512) void moe_h_kernel(const float *__restrict__ H, Plan pl, int F, uint16_t *__restrict__ hi,
                                                     uint16_t *__restrict__ lo, uint4 *__restrict__ sums,
                                                     float *__restrict__ unit, int64_t pitch)
 {
     const int64_t at = blockIdx.x;
     if (at < pl.tiles[1])
-        row_to_f16<true>(H + at * pitch, (int)pitch, pitch, hi + at * pitch, lo + at * pitch, sums + at * (pitch / 32), unit + at);
+        row_to_f16<true>(H + at * pitch, F, pitch, hi + at * pitch, lo + at * pitch, sums + at * (pitch / 32), unit + at);
 }
 
 // ---------------------------------------------------------------------------
@@ -1758,7 +1831,7 @@ bool few(int T) { return T <= 4; }
 
 // Workspace, few tokens: H [T k][F] in 4 bytes a value (fp32; the digits take
 // 3.5).  Otherwise, P = T k pairs: the plan, Pd fp32 [P][K], and H: two planes
-// [P][F], and for the tuned formats F padded to 128, its sums and units, its
+// [P][F], and for the tuned formats F padded to 256, its sums and units, its
 // fp32 form, and X in fp16 with its sums and units.  One layout for every
 // format and tile size.
 struct Layout {
@@ -1774,8 +1847,8 @@ Layout layout_of(int T, int E, int k, int64_t F, int64_t K)
         return l;
     }
     const int64_t most = P / 16 + (P < E ? P : E) + 1;
-    l.fp = (F + 127) / 128 * 128;
-    l.kp = (K + 127) / 128 * 128;
+    l.fp = (F + 255) / 256 * 256;
+    l.kp = (K + 255) / 256 * 256;
     l.hlo = 2 * P * l.fp;
     l.hsum = l.hlo + 2 * P * l.fp;
     l.hunit = l.hsum + P * l.fp / 2;
@@ -1862,10 +1935,14 @@ hipError_t gemm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, in
     return gemm<FMT, 4, 2, GLU>(a, l, pl, max_tiles, s);
 }
 
-template <int FMT, int TM, bool GLU, bool TAIL>
+// Tiles of the products: 16 tm pairs, 16 nt rows a wave.
+struct Shape {
+    int tm, nt, max_tiles;
+};
+
+template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, hipStream_t s)
 {
-    constexpr int NT = 4;
     constexpr bool THIN = TM <= 2;
     const int64_t N = GLU ? a.F : a.K, K = GLU ? a.K : a.F, per = GLU ? 32 * NT : THIN ? 16 * NT : 64 * NT;
     const Planes p = planes_of(FMT, a.E * N, K);
@@ -1878,38 +1955,47 @@ hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, 
     const int64_t nblk = (N + per - 1) / per, grid = (nblk * max_tiles + 7) / 8 * 8;
     if (grid >= (int64_t(1) << 31))
         return hipErrorNotSupported;
+    const Order order{(int)nblk, 8};
     float *out = f32(GLU ? l.h32 : l.pd);
     const int64_t pitch = GLU ? l.fp : a.K;
     if constexpr (THIN)
-        moe_thin_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), GLU ? 256 : 512, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk,
+        moe_thin_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), GLU ? 256 : 512, 0, s>>>(w0, w1, x, pl, a.k, N, order,
                                                                                          a.act, out, pitch);
     else
-        moe_wide_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, (int)nblk, a.act, out,
+        moe_wide_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, order, a.act, out,
                                                                               pitch);
     return hipGetLastError();
 }
 
+template <int FMT, bool GLU, bool TAIL>
+hipError_t mm_shape(const MoeArgs &a, const Layout &l, const Plan &pl, const Shape &sh, hipStream_t s)
+{
+    if (sh.tm == 1)
+        return mm<FMT, 1, 4, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
+    if (sh.tm == 2)
+        return mm<FMT, 2, 4, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
+    if (sh.nt == 2)
+        return mm<FMT, 4, 2, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
+    return mm<FMT, 4, 4, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
+}
+
 template <int FMT, bool GLU>
-hipError_t mm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, int max_tiles, hipStream_t s)
+hipError_t mm_tail(const MoeArgs &a, const Layout &l, const Plan &pl, const Shape &sh, hipStream_t s)
 {
     if constexpr (FMT == FMT_Q8_0) {
         if ((GLU ? a.K : a.F) % 128 != 0)
-            return tm == 1   ? mm<FMT, 1, GLU, true>(a, l, pl, max_tiles, s)
-                   : tm == 2 ? mm<FMT, 2, GLU, true>(a, l, pl, max_tiles, s)
-                             : mm<FMT, 4, GLU, true>(a, l, pl, max_tiles, s);
+            return mm_shape<FMT, GLU, true>(a, l, pl, sh, s);
     }
-    return tm == 1   ? mm<FMT, 1, GLU, false>(a, l, pl, max_tiles, s)
-           : tm == 2 ? mm<FMT, 2, GLU, false>(a, l, pl, max_tiles, s)
-                     : mm<FMT, 4, GLU, false>(a, l, pl, max_tiles, s);
+    return mm_shape<FMT, GLU, false>(a, l, pl, sh, s);
 }
 
 template <bool GLU>
-hipError_t mm_fmt(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, int max_tiles, hipStream_t s)
+hipError_t mm_fmt(const MoeArgs &a, const Layout &l, const Plan &pl, const Shape &sh, hipStream_t s)
 {
     switch (GLU ? a.fmt_gu : a.fmt_d) {
-    case FMT_Q4K: return mm_tm<FMT_Q4K, GLU>(a, l, pl, tm, max_tiles, s);
-    case FMT_Q6K: return mm_tm<FMT_Q6K, GLU>(a, l, pl, tm, max_tiles, s);
-    default: return mm_tm<FMT_Q8_0, GLU>(a, l, pl, tm, max_tiles, s);
+    case FMT_Q4K: return mm_tail<FMT_Q4K, GLU>(a, l, pl, sh, s);
+    case FMT_Q6K: return mm_tail<FMT_Q6K, GLU>(a, l, pl, sh, s);
+    default: return mm_tail<FMT_Q8_0, GLU>(a, l, pl, sh, s);
     }
 }
 
@@ -1942,8 +2028,10 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
     }
     const int P = a.T * a.k;
     // tokens per tile: the expected number of an expert's pairs
-    const int per = P / a.E, tm = per <= 16 ? 1 : per <= 32 ? 2 : 4, BM = 16 * tm;
-    const int max_tiles = P / BM + (P < a.E ? P : a.E);
+    const int per = P / a.E;
+    Shape sh{per <= 16 ? 1 : per <= 32 ? 2 : 4, per <= 128 ? 2 : 4, 0};
+    const int BM = 16 * sh.tm, max_tiles = P / BM + (P < a.E ? P : a.E);
+    sh.max_tiles = max_tiles;
     const Plan pl{reinterpret_cast<int32_t *>(a.ws + l.tiles), reinterpret_cast<int32_t *>(a.ws + l.pair),
                   reinterpret_cast<int32_t *>(a.ws + l.place)};
     // (offsets inside an expert's planes and inside X are 32 bits there)
@@ -1951,12 +2039,12 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
         moe_prep_kernel<<<a.T + 1, 1024, 0, s>>>(
             a.ids, P, a.E, BM, pl, a.X, a.T, a.K, reinterpret_cast<uint16_t *>(a.ws + l.xh),
             reinterpret_cast<uint4 *>(a.ws + l.xsum), reinterpret_cast<float *>(a.ws + l.xunit), l.kp);
-        if ((e = hipGetLastError()) != hipSuccess || (e = mm_fmt<true>(a, l, pl, tm, max_tiles, s)) != hipSuccess)
+        if ((e = hipGetLastError()) != hipSuccess || (e = mm_fmt<true>(a, l, pl, sh, s)) != hipSuccess)
             return e;
-        moe_h_kernel<<<P, 512, 0, s>>>(reinterpret_cast<const float *>(a.ws + l.h32), pl, reinterpret_cast<uint16_t *>(a.ws),
+        moe_h_kernel<<<P, 512, 0, s>>>(reinterpret_cast<const float *>(a.ws + l.h32), pl, (int)a.F, reinterpret_cast<uint16_t *>(a.ws),
                                        reinterpret_cast<uint16_t *>(a.ws + l.hlo), reinterpret_cast<uint4 *>(a.ws + l.hsum),
                                        reinterpret_cast<float *>(a.ws + l.hunit), l.fp);
-        if ((e = hipGetLastError()) != hipSuccess || (e = mm_fmt<false>(a, l, pl, tm, max_tiles, s)) != hipSuccess)
+        if ((e = hipGetLastError()) != hipSuccess || (e = mm_fmt<false>(a, l, pl, sh, s)) != hipSuccess)
             return e;
     } else {
         moe_plan_kernel<<<1, 1024, 0, s>>>(a.ids, P, a.E, BM, pl);
@@ -1964,7 +2052,7 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
             return e;
         e = hipErrorNotSupported;
         switch (a.fmt_gu) {
-#define X(f) case f: e = gemm_tm<f, true>(a, l, pl, tm, max_tiles, s); break;
+#define X(f) case f: e = gemm_tm<f, true>(a, l, pl, sh.tm, max_tiles, s); break;
             QL_EACH_FMT(X)
 #undef X
         }
@@ -1972,7 +2060,7 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
             return e;
         e = hipErrorNotSupported;
         switch (a.fmt_d) {
-#define X(f) case f: e = gemm_tm<f, false>(a, l, pl, tm, max_tiles, s); break;
+#define X(f) case f: e = gemm_tm<f, false>(a, l, pl, sh.tm, max_tiles, s); break;
             QL_EACH_FMT(X)
 #undef X
         }
