@@ -15,24 +15,24 @@
 // x - m is clamped at -200 (e^-200 is 0 in fp32), which keeps (x - m) e^(x - m)
 // from becoming inf * 0 at masked places.
 //
-// Alternatives.  A workgroup walks its part of a row in tiles of 8192 (16
-// logits per thread, held in registers).  From the first tile it takes a
-// threshold: the tile is cut into 64 groups of 128, and the top-th largest of
-// the 64 group maxima is a value that at least `top` logits reach, so no logit
-// below it can be an alternative.  Only logits at or above the threshold (a
-// few hundred of 131072) are appended to a list in LDS, as 64-bit keys whose
-// order is the value's and then the lower index's; a key's position among the
-// list's keys is its rank.  When the list is half full it is cut to its `top`
-// best, whose last value is the new threshold; a tile that would overflow it
-// (a rising row, a row of ties) is taken again after such a cut and with a
-// threshold of its own, and if even that overflows (thousands of equal
-// logits), by `top` rounds of a maximum over the tile's registers.
+// Alternatives.  A workgroup walks its part of a row in tiles of 4096 (16
+// logits per thread, the next tile's on the way).  From the first tile it
+// takes a threshold: the tile is cut into 64 groups of 64, and the top-th
+// largest of the 64 group maxima is a value that at least `top` logits reach,
+// so no logit below it can be an alternative.  Logits at or above it are
+// appended to a list in LDS, as 64-bit keys whose order is the value's and
+// then the lower index's; a key's position among the list's keys is its rank.
+// A list past 4 top + 16 keys is cut to its `top` best, whose last value is
+// the new threshold, so that later tiles add ever fewer; a tile that would
+// overflow the list (a rising row, a row of ties) is taken again after such a
+// cut and with a threshold of its own, and if even that overflows (thousands
+// of equal logits), by `top` rounds of a maximum over the tile, read again.
 #include "logprobs.h"
 
 namespace ql {
 namespace {
 
-constexpr int NT = 512;            // threads of a workgroup
+constexpr int NT = 256;            // threads of a workgroup
 constexpr int NW = NT / 64;
 constexpr int QPT = 4;             // 16-byte quads per thread and tile
 constexpr int TILE = NT * QPT * 4; // logits per tile
@@ -102,6 +102,13 @@ __device__ __forceinline__ uint64_t wave_max(uint64_t v)
     return v;
 }
 
+// the partner's value, lane ^ 1 (0xB1) or lane ^ 2 (0x4E)
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v)
+{
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xF, 0xF, false));
+}
+
 struct Shared {
     uint64_t key[CAP];
     uint64_t best[64];     // the `top` best after a cut
@@ -156,16 +163,26 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
     if (tid == 0)
         sh.count = 0;
     auto load = [&](int64_t tile, float (&x)[4 * QPT]) {
+        const float4 *q4 = reinterpret_cast<const float4 *>(base + tile * TILE);  // uniform
+        if (tile * TILE >= lead && (tile + 1) * TILE - lead <= a.V) {             // all of the tile is in the row
+#pragma unroll
+            for (int q = 0; q < QPT; q++) {
+                const float4 v = q4[(uint32_t)(tid + NT * q)];
+                x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
+            }
+            return;
+        }
+        const int left = (int)(a.V + lead - tile * TILE), skip = tile == 0 ? lead : 0;  // of the tile: its end, its start
 #pragma unroll
         for (int q = 0; q < QPT; q++) {
-            const int64_t e = tile * TILE + 4 * (tid + NT * q) - lead;  // element index of the quad's first
-            if (e >= 0 && e + 4 <= a.V) {
-                const float4 v = *reinterpret_cast<const float4 *>(base + e + lead);
+            const int f = 4 * (tid + NT * q);
+            if (f >= skip && f + 4 <= left) {
+                const float4 v = q4[(uint32_t)(tid + NT * q)];
                 x[4 * q] = v.x, x[4 * q + 1] = v.y, x[4 * q + 2] = v.z, x[4 * q + 3] = v.w;
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    x[4 * q + i] = e + i >= 0 && e + i < a.V ? xr[e + i] : -INFINITY;
+                    x[4 * q + i] = f + i >= skip && f + i < left ? base[tile * TILE + f + i] : -INFINITY;
             }
         }
     };
@@ -173,6 +190,7 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
     Stat st{LOWEST, 0.0f, 0.0f};
     int above = 0;
     float thr = LOWEST;  // logits below it are no alternatives (inclusive)
+    const int full = 4 * a.top + 16;
     float x[4 * QPT], nx[4 * QPT];
     if (t0 < t1)
         load(t0, x);
@@ -194,24 +212,31 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
             above += x[i] > xt;
         }
         if constexpr (TOP) {
-            auto threshold = [&]() {  // from the tile's 64 group maxima
-                float g = tm;
-#pragma unroll
-                for (int s = 1; s < 8; s <<= 1)
-                    g = fmaxf(g, __shfl_xor(g, s));
-                if ((lane & 7) == 0)
-                    sh.group[wave * 8 + (lane >> 3)] = g;
-                __syncthreads();
-                const float v = sh.group[lane];
-                int r = 0;
-                for (int j = 0; j < 64; j++) {
-                    const float o = sh.group[j];
-                    r += o > v || (o == v && j < lane);
-                }
-                const uint64_t at = __ballot(r == a.top - 1);
-                const float f = __shfl(v, __ffsll((unsigned long long)at) - 1);
-                thr = fmaxf(thr, f);
+            // this thread's i-th logit of the tile, from memory, and its index
+            auto again = [&](int i, uint32_t &e) {
+                const int64_t at = t * TILE + 4 * (tid + NT * (i >> 2)) - lead + (i & 3);
+                e = (uint32_t)at;
+                return at >= 0 && at < a.V ? xr[at] : -INFINITY;
             };
+            auto threshold = [&]() {  // from the tile's 64 group maxima
+                float g = fmaxf(tm, dpp<0xB1>(tm));
+                g = fmaxf(g, dpp<0x4E>(g));
+                if ((lane & 3) == 0)
+                    sh.group[wave * 16 + (lane >> 2)] = g;
+                __syncthreads();
+                // the top-th largest: the largest number that at least `top` of
+                // them reach, bit by bit
+                const uint32_t u = order_of(sh.group[lane]);
+                uint32_t v = 0;
+#pragma unroll
+                for (int b = 31; b >= 0; b--) {
+                    const uint32_t c = v | 1u << b;
+                    if (__popcll(__ballot(u >= c)) >= a.top)
+                        v = c;
+                }
+                thr = fmaxf(thr, value_of(v));
+            };
+            const uint32_t e0 = (uint32_t)(t * TILE + 4 * tid - lead);  // (V is below 2^25)
             auto push = [&]() {
                 if (tm < thr)
                     return;
@@ -219,9 +244,8 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
                 for (int i = 0; i < 4 * QPT; i++) {
                     if (x[i] >= thr) {
                         const int at = atomicAdd(&sh.count, 1);
-                        const int64_t e = t * TILE + 4 * (tid + NT * (i / 4)) - lead + i % 4;
                         if (at < CAP)
-                            sh.key[at] = key_of(x[i], (uint32_t)e);
+                            sh.key[at] = key_of(x[i], e0 + 4 * NT * (i / 4) + i % 4);
                     }
                 }
             };
@@ -249,23 +273,24 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
             int n = sh.count;
             if (n > CAP) {  // the tile does not fit: again, with a tighter threshold
                 __syncthreads();
-                int kept = cut(before);
+                const int kept = cut(before);
                 threshold();
                 push();
                 __syncthreads();
                 n = sh.count;
                 if (n > CAP) {
                     // thousands of equal logits: the best keys one by one, from
-                    // the tile's registers and the kept keys (in key[0 .. kept))
+                    // the tile and the kept keys (in key[0 .. kept))
                     __syncthreads();
                     const uint64_t mine = tid < kept ? sh.key[tid] : 0;
                     uint64_t last = ~0ull;
                     for (int j = 0; j < a.top; j++) {
                         uint64_t b = mine < last ? mine : 0;
-#pragma unroll
+#pragma unroll 1
                         for (int i = 0; i < 4 * QPT; i++) {
-                            const int64_t e = t * TILE + 4 * (tid + NT * (i / 4)) - lead + i % 4;
-                            const uint64_t k = x[i] >= LOWEST ? key_of(x[i], (uint32_t)e) : 0;
+                            uint32_t e;
+                            const float v = again(i, e);
+                            const uint64_t k = v >= LOWEST ? key_of(v, e) : 0;
                             b = k < last && k > b ? k : b;
                         }
                         b = wave_max(b);
@@ -288,11 +313,11 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
                     if (tid == 0)
                         sh.count = a.top;
                     __syncthreads();
-                } else if (n > CAP / 2) {
+                } else if (n > full) {
                     __syncthreads();
                     cut(n);
                 }
-            } else if (n > CAP / 2) {
+            } else if (n > full) {
                 __syncthreads();
                 cut(n);
             }
@@ -391,19 +416,24 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a, int s
     }
 }
 
-// Parts per row: enough workgroups for the chip (about four per CU), at most
-// one per tile, and at most 1024 keys to join.
+// Parts per row: enough workgroups for the chip (two per CU), and, where a part
+// keeps at least 16 tiles, enough to even out the last round of them (six fit
+// a CU: 2048 rows of 131072 are 1.3 rounds whole and 2.7 in halves, 224 -> 183
+// us); at most 16 (more make the join longer than the pass) and 1024 keys to join.
 struct Split {
     int segs, per;
 };
 Split split_of(int64_t M, int64_t V, int top)
 {
     const int64_t tiles = (V + 3 + TILE - 1) / TILE;  // whatever the row's alignment
-    int64_t want = (1024 + M - 1) / M;
+    int64_t want = (512 + M - 1) / M;
     want = want < tiles ? want : tiles;
+    int64_t even = (4096 + M - 1) / M;
+    even = even < tiles / 16 ? even : tiles / 16;
+    want = want > even ? want : even;
     const int64_t most = top > 0 ? 1024 / top : 64;
     want = want < most ? want : most;
-    want = want < 64 ? want : 64;
+    want = want < 16 ? want : 16;
     const int64_t per = (tiles + want - 1) / want;
     return Split{(int)((tiles + per - 1) / per), (int)per};
 }

@@ -138,8 +138,8 @@ def test_wrappers_check_tensors():
         ql.qmatmul_moe("q4k", b, b, b, X, ids, w, 2, 256)
     with pytest.raises(ValueError, match="blocks is too small"):
         ql.qmatmul_logprobs("q4k", b, X, 1000)
-    with pytest.raises(ValueError, match="targets must be of shape"):
-        ql.qmatmul_logprobs("q4k", b, X, 512, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="X must be a device tensor"):
+        ql.qmatmul_logprobs("q4k", b, X, 512, torch.zeros(3, dtype=torch.int32))
 
 
 def test_python_constants_match():
