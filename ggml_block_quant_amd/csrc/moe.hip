@@ -39,7 +39,10 @@ __device__ __forceinline__ float dpp(float v)
 // Sums of V values over the 64 lanes (V a power of two <= 64): while more
 // than one is left a step keeps half of them, so V values cost about V + 4
 // additions.  Lanes 0 .. V-1 end with the total of value sum_index<V>(lane).
-// Step B pairs lanes that differ in bit B.
+// A halving step needs the lane that differs in bit B exactly; a plain sum
+// any lane with the same lower bits, which for bits 2 to 5 is a rotation
+// inside a row of 16 or a swap of rows: VALU instructions, where a shuffle
+// would go through LDS (~100 cycles each, one after the other).
 template <int B>
 __device__ __forceinline__ float partner(float x)
 {
@@ -49,6 +52,36 @@ __device__ __forceinline__ float partner(float x)
         return dpp<0x4E>(x);
     else
         return __shfl_xor(x, 1 << B);
+}
+// the two rows of 16 of each half (rows 0 1 and 2 3), or the halves of 32, as
+// two values every lane has: the lower one and the upper one
+__device__ __forceinline__ void swap_rows(float x, float &lo, float &hi)
+{
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    lo = __uint_as_float(r[0]), hi = __uint_as_float(r[1]);
+}
+__device__ __forceinline__ void swap_halves(float x, float &lo, float &hi)
+{
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    lo = __uint_as_float(r[0]), hi = __uint_as_float(r[1]);
+}
+template <int B>
+__device__ __forceinline__ float plain_sum(float x)
+{
+    float lo, hi;
+    if constexpr (B == 0)
+        return x + dpp<0xB1>(x);
+    else if constexpr (B == 1)
+        return x + dpp<0x4E>(x);
+    else if constexpr (B == 2)
+        return x + dpp<0x124>(x);  // row_ror:4
+    else if constexpr (B == 3)
+        return x + dpp<0x128>(x);  // row_ror:8
+    else if constexpr (B == 4)
+        swap_rows(x, lo, hi);
+    else
+        swap_halves(x, lo, hi);
+    return lo + hi;
 }
 template <int LEFT, int B, int V>
 __device__ __forceinline__ void sum_step(float (&v)[V], int lane)
@@ -61,7 +94,7 @@ __device__ __forceinline__ void sum_step(float (&v)[V], int lane)
             v[i] = keep + partner<B>(send);
         }
     } else {
-        v[0] += partner<B>(v[0]);
+        v[0] = plain_sum<B>(v[0]);
     }
     if constexpr (B < 5)
         sum_step<(LEFT > 1 ? LEFT / 2 : 1), B + 1>(v, lane);
@@ -100,6 +133,18 @@ __device__ __forceinline__ KT wave_max(KT v)
         v = o > v ? o : v;
     }
     return v;
+}
+
+__device__ __forceinline__ float wave_max(float v)
+{
+    float lo, hi;
+    v = fmaxf(v, dpp<0xB1>(v));
+    v = fmaxf(v, dpp<0x4E>(v));
+    v = fmaxf(v, dpp<0x124>(v));
+    v = fmaxf(v, dpp<0x128>(v));
+    swap_rows(v, lo, hi);
+    swap_halves(fmaxf(lo, hi), lo, hi);
+    return fmaxf(lo, hi);
 }
 
 // BIAS: the key is sigmoid(x) + bias in 64 bits (where 32 would let the
@@ -462,12 +507,14 @@ __device__ __forceinline__ int eo_place(int i)
 __device__ __forceinline__ void write_digits(float h, uint4 *__restrict__ out, bool eo)
 {
     const int i = threadIdx.x & 31;
-    float m = fabsf(h), sum = h;
-#pragma unroll
-    for (int s = 1; s < 32; s <<= 1) {
-        m = fmaxf(m, __shfl_xor(m, s));
-        sum += __shfl_xor(sum, s);
-    }
+    const float sum = plain_sum<4>(plain_sum<3>(plain_sum<2>(plain_sum<1>(plain_sum<0>(h)))));
+    float m = fabsf(h), lo, hi;
+    m = fmaxf(m, dpp<0xB1>(m));
+    m = fmaxf(m, dpp<0x4E>(m));
+    m = fmaxf(m, dpp<0x124>(m));
+    m = fmaxf(m, dpp<0x128>(m));
+    swap_rows(m, lo, hi);
+    m = fmaxf(lo, hi);
     int e = m > 0.0f ? 23 - __builtin_amdgcn_frexp_expf(m) : 0;  // m 2^e in [2^22, 2^23)
     if (__builtin_amdgcn_ldexpf(m, e) > 8355711.0f)              // 127 (65536 + 256 + 1): the largest v
         e--;
