@@ -1157,14 +1157,24 @@ __device__ __forceinline__ Row16 row_offsets(int K, int row, int g)
 
 // slab 2 G + u.  Q8_0 rows may end before a whole group: the last slab again
 // past it, or, TAIL, where they end inside a slab, the last block (X is zero there)
-template <int FMT, bool TAIL>
+// STREAM: read once (non-temporal), so that the lines of the scale planes, which
+// serve many groups, stay in the caches
+template <bool STREAM>
+__device__ __forceinline__ uint4 codes16(const uint8_t *p)
+{
+    if constexpr (STREAM)
+        return stream16(p);
+    else
+        return *reinterpret_cast<const uint4 *>(p);
+}
+template <int FMT, bool TAIL, bool STREAM>
 __device__ __forceinline__ void load_codes(const Planes16 &w, const Row16 &r, int G, int u, int g, Codes16<FMT> &t)
 {
     if constexpr (FMT == FMT_Q4K) {
-        t.c = *reinterpret_cast<const uint4 *>(w.codes + 128 * G + 64 * u + r.codes);
+        t.c = codes16<STREAM>(w.codes + 128 * G + 64 * u + r.codes);
     } else if constexpr (FMT == FMT_Q6K) {
         const uint8_t *c = w.codes + 192 * G + 64 * u, *h = w.codes + 192 * G + 128 + 32 * u;
-        t.c = *reinterpret_cast<const uint4 *>(c + (r.codes + 16u * g));
+        t.c = codes16<STREAM>(c + (r.codes + 16u * g));
         t.hi = *reinterpret_cast<const uint2 *>(h + (r.codes + 8u * g));
         t.sc = *reinterpret_cast<const uint16_t *>(w.sc + 16 * G + 8 * u + r.sc);
     } else if constexpr (!TAIL) {
@@ -1385,6 +1395,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
                                                                   int64_t out_pitch)
 {
     constexpr int WAVES = GLU ? 4 : 8, NF = GLU ? NT / 2 : NT;
+    constexpr bool AHEAD = GLU && TM == 1;  // X a slab ahead, where the registers allow
     __shared__ f32x4_t red[GLU ? 1 : WAVES * NT * TM * 64];
     int ti, blk;
     if (!place_of_block(pl.tiles[0], order, ti, blk))
@@ -1394,8 +1405,8 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r16 = lane & 15;
     const int64_t K = w0.K, n_wave = (int64_t)blk * (GLU ? 64 * NF : 16 * NF) + (GLU ? wave * 16 * NF : 0);
-    const int slabs = (int)((K + 127) / 128);
-    const int s0 = GLU ? 0 : slabs * wave / WAVES, s1 = GLU ? slabs : slabs * (wave + 1) / WAVES;
+    const int groups = (int)((K + 255) / 256);
+    const int g0 = GLU ? 0 : groups * wave / WAVES, g1 = GLU ? groups : groups * (wave + 1) / WAVES;
     const Planes16 e0 = expert_planes<FMT>(w0, expert * N), e1 = expert_planes<FMT>(w1, expert * N);
     Row16 wrow[NF];
 #pragma unroll
@@ -1408,14 +1419,16 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
         for (int j = 0; j < TM; j++)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const Nibbles nb = make_nibbles();
-    Codes16<FMT> raw[NT];
+    Codes16<FMT> raw[2][NT];
     Head16<FMT> rawh[NT];
-    auto load_w = [&](int s) {
+    // both slabs of a group at once: together they are whole cache lines of the
+    // codes, which are gone from the caches a slab later (fetching them one by
+    // one, and with the scale planes' lines evicted by them, read twice the bytes)
+    auto load_w = [&](int G, int i) {
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            load_codes<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s >> 1, s & 1, g, raw[i]);
-            load_head<FMT>(GLU && i >= NF ? e1 : e0, wrow[i % NF], s >> 1, rawh[i]);
-        }
+        for (int u = 0; u < 2; u++)
+            load_codes<FMT, TAIL, true>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, u, g, raw[u][i]);
+        load_head<FMT>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, rawh[i]);
     };
     // the lane's token of each tile (past the end: the last one)
     const uint16_t *ahi[TM], *alo[TM];
@@ -1428,100 +1441,98 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
         alo[j] = x.lo + row * x.pitch + slab_at<FMT>(0, g) / 2;
         asum[j] = x.sums + row * (x.pitch / 32) + g;
     }
-    f16x8_t nh[TM][4], nl[TM][4];
-    bf16x8_t ns[TM];
-    auto load_x = [&](int s) {
+    struct Piece {
+        f16x8_t h[TM][4], l[TM][4];
+        bf16x8_t s[TM];
+    };
+    auto load_x = [&](int s, Piece &x16) {
 #pragma unroll
         for (int j = 0; j < TM; j++) {
 #pragma unroll
             for (int t = 0; t < 4; t++) {
                 const int at = 128 * s + (slab_at<FMT>(t, 0) - slab_at<FMT>(0, 0)) / 2;
-                nh[j][t] = *reinterpret_cast<const f16x8_t *>(ahi[j] + at);
+                x16.h[j][t] = *reinterpret_cast<const f16x8_t *>(ahi[j] + at);
                 if constexpr (!GLU)
-                    nl[j][t] = *reinterpret_cast<const f16x8_t *>(alo[j] + at);
+                    x16.l[j][t] = *reinterpret_cast<const f16x8_t *>(alo[j] + at);
             }
             if constexpr (FMT == FMT_Q4K)
-                ns[j] = *reinterpret_cast<const bf16x8_t *>(asum[j] + 4 * s);
+                x16.s[j] = *reinterpret_cast<const bf16x8_t *>(asum[j] + 4 * s);
         }
     };
-    if (s0 < s1) {
-        load_w(s0);
-        load_x(s0);
+    Piece x16;
+    if (g0 < g1) {
+        load_x(2 * g0, x16);
+#pragma unroll
+        for (int i = 0; i < NT; i++)
+            load_w(g0, i);
     }
-    for (int s = s0; s < s1; s++) {
-        f16x8_t xh[TM][4], xl[TM][4];
-        bf16x8_t xs[TM];
-        Codes16<FMT> cur[NT];
-        Head16<FMT> hd[NT];
+    for (int G = g0; G < g1; G++) {
+        const int next = min(G + 1, g1 - 1);
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            cur[i] = raw[i];
-            hd[i] = rawh[i];
-        }
-#pragma unroll
-        for (int j = 0; j < TM; j++) {
-#pragma unroll
-            for (int t = 0; t < 4; t++) {
-                xh[j][t] = nh[j][t];
-                if constexpr (!GLU)
-                    xl[j][t] = nl[j][t];
+        for (int u = 0; u < 2; u++) {
+            Piece nx;
+            if constexpr (AHEAD) {
+                load_x(u == 0 ? 2 * G + 1 : 2 * next, nx);
+                __builtin_amdgcn_sched_barrier(0x81);  // loads stay before what follows
             }
-            if constexpr (FMT == FMT_Q4K)
-                xs[j] = ns[j];
-        }
-        // the next slab's loads go out before this one's products
-        load_w(min(s + 1, s1 - 1));
-        load_x(min(s + 1, s1 - 1));
-        __builtin_amdgcn_sched_barrier(0);
-        const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
+            const f32x4_t zero = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < NT; i++) {
-            f32x4_t p[TM];
+            for (int i = 0; i < NT; i++) {
+                f16x8_t o[2][2][PER<FMT>];
+                float d[4];
+                decode_half<FMT>(nb, raw[u][i], rawh[i], u, g, 0, o[0]);
+                decode_half<FMT>(nb, raw[u][i], rawh[i], u, g, 1, o[1]);
 #pragma unroll
-            for (int j = 0; j < TM; j++)
-                p[j] = zero;
+                for (int q = 0; q < (FMT == FMT_Q8_0 ? 4 : 1); q++)
+                    d[q] = scale_of<FMT>(raw[u][i], rawh[i], q);
+                float dm = 0.0f;
+                bf16x8_t mo;
+                if constexpr (FMT == FMT_Q4K) {
+                    dm = f16_bits_to_f32(rawh[i].h.x >> 16);
+                    mo = min_entry1(min_code(rawh[i], u, g));
+                }
+                // a tile's codes are spent once decoded: the next group's take
+                // their registers, and have the time of a slab or two to arrive
+                if (u == 1) {
+                    load_w(next, i);
+                    __builtin_amdgcn_sched_barrier(0x81);
+                }
+                f32x4_t p[TM];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                f16x8_t o[2][PER<FMT>];
-                decode_half<FMT>(nb, cur[i], hd[i], s & 1, g, h, o);
+                for (int j = 0; j < TM; j++) {
+                    p[j] = zero;
 #pragma unroll
-                for (int j = 0; j < TM; j++)
-#pragma unroll
-                    for (int q = 0; q < 2; q++) {
+                    for (int q = 0; q < 4; q++) {
 #pragma unroll
                         for (int c = 0; c < PER<FMT>; c++) {
-                            p[j] = mfma16(xh[j][2 * h + q], o[q][c], p[j]);
+                            p[j] = mfma16(x16.h[j][q], o[q >> 1][q & 1][c], p[j]);
                             if constexpr (!GLU)
-                                p[j] = mfma16(xl[j][2 * h + q], o[q][c], p[j]);
+                                p[j] = mfma16(x16.l[j][q], o[q >> 1][q & 1][c], p[j]);
                         }
                         if constexpr (FMT == FMT_Q8_0) {
-                            const float d = scale_of<FMT>(cur[i], hd[i], 2 * h + q);
 #pragma unroll
                             for (int e = 0; e < 4; e++)
-                                acc[i][j][e] = fmaf(d, p[j][e], acc[i][j][e]);
+                                acc[i][j][e] = fmaf(d[q], p[j][e], acc[i][j][e]);
                             p[j] = zero;
                         }
                     }
-            }
-            if constexpr (FMT != FMT_Q8_0) {
-                const float d = scale_of<FMT>(cur[i], hd[i], 0);
+                    if constexpr (FMT != FMT_Q8_0) {
 #pragma unroll
-                for (int j = 0; j < TM; j++)
+                        for (int e = 0; e < 4; e++)
+                            acc[i][j][e] = fmaf(d[0], p[j][e], acc[i][j][e]);
+                    }
+                    if constexpr (FMT == FMT_Q4K) {
+                        const f32x4_t q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x16.s[j], mo, zero, 0, 0, 0);
 #pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        acc[i][j][e] = fmaf(d, p[j][e], acc[i][j][e]);
-            }
-            if constexpr (FMT == FMT_Q4K) {
-                const float dm = f16_bits_to_f32(hd[i].h.x >> 16);
-                const bf16x8_t mo = min_entry1(min_code(hd[i], s & 1, g));
-#pragma unroll
-                for (int j = 0; j < TM; j++) {
-                    const f32x4_t q = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[j], mo, zero, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        acc[i][j][e] = fmaf(-dm, q[e], acc[i][j][e]);
+                        for (int e = 0; e < 4; e++)
+                            acc[i][j][e] = fmaf(-dm, q[e], acc[i][j][e]);
+                    }
                 }
             }
+            if constexpr (AHEAD)
+                x16 = nx;
+            else
+                load_x(u == 0 ? 2 * G + 1 : 2 * next, x16);
         }
     }
     if constexpr (!GLU) {  // the waves' sums, in order: wave w takes every WAVES-th tile of the result
@@ -1551,7 +1562,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 // D), which needs no second set of accumulators; Q4K's minimums enter as
 // -(dmin / D) m.  Q8_0 adds each block's products times its scale.
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
-__global__ __launch_bounds__(256, NT == 2 ? 3 : 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, Order order,
+__global__ __launch_bounds__(256, NT == 2 && GLU ? 3 : 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, Order order,
                                                           int act, float *__restrict__ out, int64_t out_pitch)
 {
     constexpr int BM = 16 * TM, PL = GLU ? 1 : 2, NF = GLU ? NT / 2 : NT;
@@ -1595,7 +1606,7 @@ __global__ __launch_bounds__(256, NT == 2 ? 3 : 2) void moe_wide_kernel(Mat w0, 
     auto load_c = [&](int G, int u) {
 #pragma unroll
         for (int i = 0; i < NT; i++)
-            load_codes<FMT, TAIL>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, u, g, raw[u % RAWS][i]);
+            load_codes<FMT, TAIL, false>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, u, g, raw[u % RAWS][i]);
     };
     auto load_h = [&](int G) {
 #pragma unroll
