@@ -1395,7 +1395,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
                                                                   int64_t out_pitch)
 {
     constexpr int WAVES = GLU ? 4 : 8, NF = GLU ? NT / 2 : NT;
-    constexpr bool AHEAD = GLU && TM == 1;  // X a slab ahead, where the registers allow
+    constexpr bool AHEAD = TM == 1;  // X a slab ahead, where the registers allow
     __shared__ f32x4_t red[GLU ? 1 : WAVES * NT * TM * 64];
     int ti, blk;
     if (!place_of_block(pl.tiles[0], order, ti, blk))
@@ -1419,16 +1419,23 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
         for (int j = 0; j < TM; j++)
             acc[i][j] = f32x4_t{0.0f, 0.0f, 0.0f, 0.0f};
     const Nibbles nb = make_nibbles();
-    Codes16<FMT> raw[2][NT];
+    // Q4K, Q6K: both slabs of a group at once, since only together are they whole
+    // cache lines of the codes, which are gone from the caches a slab later
+    // (fetching them one by one, and with the scale planes' lines evicted by
+    // them, read twice the bytes).  A slab of Q8_0 is whole lines by itself.
+    constexpr int RAWS = FMT == FMT_Q8_0 ? 1 : 2;
+    Codes16<FMT> raw[RAWS][NT];
     Head16<FMT> rawh[NT];
-    // both slabs of a group at once: together they are whole cache lines of the
-    // codes, which are gone from the caches a slab later (fetching them one by
-    // one, and with the scale planes' lines evicted by them, read twice the bytes)
-    auto load_w = [&](int G, int i) {
-#pragma unroll
-        for (int u = 0; u < 2; u++)
-            load_codes<FMT, TAIL, true>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, u, g, raw[u][i]);
-        load_head<FMT>(GLU && i >= NF ? e1 : e0, wrow[i % NF], G, rawh[i]);
+    // after slab u of group G has been decoded: what takes its registers
+    auto load_w = [&](int G, int next, int u, int i) {
+        const Planes16 &e = GLU && i >= NF ? e1 : e0;
+        if constexpr (RAWS == 1) {
+            load_codes<FMT, TAIL, true>(e, wrow[i % NF], u == 0 ? G : next, 1 - u, g, raw[0][i]);
+        } else if (u == 1) {
+            load_codes<FMT, TAIL, true>(e, wrow[i % NF], next, 0, g, raw[0][i]);
+            load_codes<FMT, TAIL, true>(e, wrow[i % NF], next, 1, g, raw[1][i]);
+            load_head<FMT>(e, wrow[i % NF], next, rawh[i]);
+        }
     };
     // the lane's token of each tile (past the end: the last one)
     const uint16_t *ahi[TM], *alo[TM];
@@ -1464,7 +1471,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
         load_x(2 * g0, x16);
 #pragma unroll
         for (int i = 0; i < NT; i++)
-            load_w(g0, i);
+            load_w(g0, g0, 1, i);
     }
     for (int G = g0; G < g1; G++) {
         const int next = min(G + 1, g1 - 1);
@@ -1480,23 +1487,21 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
             for (int i = 0; i < NT; i++) {
                 f16x8_t o[2][2][PER<FMT>];
                 float d[4];
-                decode_half<FMT>(nb, raw[u][i], rawh[i], u, g, 0, o[0]);
-                decode_half<FMT>(nb, raw[u][i], rawh[i], u, g, 1, o[1]);
+                decode_half<FMT>(nb, raw[u % RAWS][i], rawh[i], u, g, 0, o[0]);
+                decode_half<FMT>(nb, raw[u % RAWS][i], rawh[i], u, g, 1, o[1]);
 #pragma unroll
                 for (int q = 0; q < (FMT == FMT_Q8_0 ? 4 : 1); q++)
-                    d[q] = scale_of<FMT>(raw[u][i], rawh[i], q);
+                    d[q] = scale_of<FMT>(raw[u % RAWS][i], rawh[i], q);
                 float dm = 0.0f;
                 bf16x8_t mo;
                 if constexpr (FMT == FMT_Q4K) {
                     dm = f16_bits_to_f32(rawh[i].h.x >> 16);
                     mo = min_entry1(min_code(rawh[i], u, g));
                 }
-                // a tile's codes are spent once decoded: the next group's take
-                // their registers, and have the time of a slab or two to arrive
-                if (u == 1) {
-                    load_w(next, i);
-                    __builtin_amdgcn_sched_barrier(0x81);
-                }
+                // a tile's codes are spent once decoded: the next ones have the
+                // time of a slab or two to arrive
+                load_w(G, next, u, i);
+                __builtin_amdgcn_sched_barrier(0x81);
                 f32x4_t p[TM];
 #pragma unroll
                 for (int j = 0; j < TM; j++) {
@@ -1562,7 +1567,7 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 // D), which needs no second set of accumulators; Q4K's minimums enter as
 // -(dmin / D) m.  Q8_0 adds each block's products times its scale.
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
-__global__ __launch_bounds__(256, NT == 2 && GLU ? 3 : 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, Order order,
+__global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, Order order,
                                                           int act, float *__restrict__ out, int64_t out_pitch)
 {
     constexpr int BM = 16 * TM, PL = GLU ? 1 : 2, NF = GLU ? NT / 2 : NT;
@@ -1600,7 +1605,7 @@ __global__ __launch_bounds__(256, NT == 2 && GLU ? 3 : 2) void moe_wide_kernel(M
         D[i] = 1.0f;
     const Nibbles nb = make_nibbles();
     // two slabs of codes in flight where they fit the registers
-    constexpr int RAWS = FMT == FMT_Q4K || NT == 2 ? 2 : 1;
+    constexpr int RAWS = FMT == FMT_Q4K ? 2 : 1;
     Codes16<FMT> raw[RAWS][NT];
     Head16<FMT> hd[NT], nhd[NT];
     auto load_c = [&](int G, int u) {
@@ -1884,8 +1889,13 @@ __global__ __launch_bounds__(512) void moe_h_kernel(const float *__restrict__ H,
 // ---------------------------------------------------------------------------
 // Launches
 // ---------------------------------------------------------------------------
-// Few tokens: up to four, where the chosen experts hardly repeat.
-bool few(int T) { return T <= 4; }
+// The form for few tokens reads an expert's weights once per pair, the other
+// once per tile of pairs.  Measured (us, few against more): 8 experts of 14336 x
+// 4096 Q4K, two a token: 8 tokens 247 / 260, 12 tokens 356 / 276; 128 of 768 x
+// 2048 Q4K, eight a token: 32 tokens 118 / 152, 48 tokens 168 / 156; the same in
+// Q8_0: 32 tokens 231 / 251, 48 tokens 334 / 254.  So: up to two pairs an
+// expert; and up to four tokens always, whose products then stay in fp32.
+bool few(int T, int E, int k) { return T <= 4 || (int64_t)T * k <= 2 * (int64_t)E; }
 
 // Workspace, few tokens: H [T k][F] in 4 bytes a value (fp32; the digits take
 // 3.5).  Otherwise, P = T k pairs: the plan, Pd fp32 [P][K], and H: two planes
@@ -1900,7 +1910,7 @@ Layout layout_of(int T, int E, int k, int64_t F, int64_t K)
 {
     const int64_t P = (int64_t)T * k;
     Layout l{};
-    if (few(T)) {
+    if (few(T, E, k)) {
         l.total = up16(4 * P * F);
         return l;
     }
@@ -1988,20 +1998,18 @@ hipError_t gemm_tm(const MoeArgs &a, const Layout &l, const Plan &pl, int tm, in
 {
     if (tm == 1)
         return gemm<FMT, 1, 2, GLU>(a, l, pl, max_tiles, s);
-    if (tm == 2)
-        return gemm<FMT, 2, 2, GLU>(a, l, pl, max_tiles, s);
     return gemm<FMT, 4, 2, GLU>(a, l, pl, max_tiles, s);
 }
 
-// Tiles of the products: 16 tm pairs, 16 nt rows a wave.
+// Tiles of the products: 16 tm pairs.
 struct Shape {
-    int tm, nt, max_tiles;
+    int tm, max_tiles;
 };
 
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, hipStream_t s)
 {
-    constexpr bool THIN = TM <= 2;
+    constexpr bool THIN = TM == 1;
     const int64_t N = GLU ? a.F : a.K, K = GLU ? a.K : a.F, per = GLU ? 32 * NT : THIN ? 16 * NT : 64 * NT;
     const Planes p = planes_of(FMT, a.E * N, K);
     const Mat w0{GLU ? a.gate : a.down, p, K}, w1{GLU ? a.up : a.down, p, K};
@@ -2030,10 +2038,6 @@ hipError_t mm_shape(const MoeArgs &a, const Layout &l, const Plan &pl, const Sha
 {
     if (sh.tm == 1)
         return mm<FMT, 1, 4, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
-    if (sh.tm == 2)
-        return mm<FMT, 2, 4, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
-    if (sh.nt == 2)
-        return mm<FMT, 4, 2, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
     return mm<FMT, 4, 4, GLU, TAIL>(a, l, pl, sh.max_tiles, s);
 }
 
@@ -2069,7 +2073,7 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
 {
     const Layout l = layout_of(a.T, a.E, a.k, a.F, a.K);
     hipError_t e = hipErrorNotSupported;
-    if (few(a.T)) {
+    if (few(a.T, a.E, a.k)) {
         switch (a.fmt_gu) {
 #define X(f) case f: e = glu_few<f>(a, s); break;
             QL_EACH_FMT(X)
@@ -2085,15 +2089,25 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
         return hipErrorNotSupported;
     }
     const int P = a.T * a.k;
-    // tokens per tile: the expected number of an expert's pairs
+    // (offsets inside an expert's planes and inside X are 32 bits there)
+    const bool tuned =
+        digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d) && a.F * a.K < (int64_t(1) << 31) && 2 * a.T * l.kp < (int64_t(1) << 32);
+    // Pairs per tile, 16 or 64, from the mean number of an expert's pairs.  Tuned
+    // formats (thin against wide, us): 8 experts of 14336 x 4096 Q4K, 12 pairs
+    // each 384 / 441, 16 pairs 480 / 446; 8 of 4096 x 4096 Q8_0, 12 pairs 234 /
+    // 263, 16 pairs 301 / 266.  The thin kernel's down product splits rows of F
+    // over eight waves, which short rows do not feed: 128 of 768 x 2048, 3 pairs
+    // each 176 / 156, 64 of 1536 x 2048, 3 pairs each 191 / 198, 9 pairs 228 / 195.
+    // Other formats (16 against 64 pairs): 8 of 4096 x 4096 Q4_0, 16 pairs 274 /
+    // 310, 32 pairs 370 / 277; 32 of 768 x 2048 Q5K, 8 pairs 118 / 121, 16 pairs
+    // 153 / 123.
     const int per = P / a.E;
-    Shape sh{per <= 16 ? 1 : per <= 32 ? 2 : 4, per <= 128 ? 2 : 4, 0};
+    Shape sh{per <= 12 && (!tuned || a.F >= 4096) ? 1 : 4, 0};
     const int BM = 16 * sh.tm, max_tiles = P / BM + (P < a.E ? P : a.E);
     sh.max_tiles = max_tiles;
     const Plan pl{reinterpret_cast<int32_t *>(a.ws + l.tiles), reinterpret_cast<int32_t *>(a.ws + l.pair),
                   reinterpret_cast<int32_t *>(a.ws + l.place)};
-    // (offsets inside an expert's planes and inside X are 32 bits there)
-    if (digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d) && a.F * a.K < (int64_t(1) << 31) && 2 * a.T * l.kp < (int64_t(1) << 32)) {
+    if (tuned) {
         moe_prep_kernel<<<a.T + 1, 1024, 0, s>>>(
             a.ids, P, a.E, BM, pl, a.X, a.T, a.K, reinterpret_cast<uint16_t *>(a.ws + l.xh),
             reinterpret_cast<uint4 *>(a.ws + l.xsum), reinterpret_cast<float *>(a.ws + l.xunit), l.kp);

@@ -122,6 +122,91 @@ def test_moe_shapes(fmt, fmt_down, E, F, K, k, Ts, act):
         L.check(synth.activations_bf16(42100 + T, T, K), ids, w, act, f"moe {fmt}/{fmt_down} {act} T={T}")
 
 
+@pytest.mark.parametrize("fmt,fmt_down,F,K", [
+    ("q4k", "q6k", 4096, 256),
+    ("q6k", "q4k", 4352, 512),
+    ("q8_0", "q8_0", 4128, 288),   # row lengths no multiple of a slab
+    ("q8_0", "q4k", 4096, 32),
+    ("q4k", "q8_0", 5152, 768),
+])
+def test_moe_tiles_of_sixteen(fmt, fmt_down, F, K):
+    """Long rows of F and up to twelve pairs an expert (tiles of 16 pairs), and
+    just above (tiles of 64)."""
+    L = Layer(fmt, fmt_down, 3, F, K, 46000)
+    for T in (5, 8, 18, 21):
+        ids, w = choice(300 + T, T, 3, 2)
+        L.check(synth.activations_bf16(46100 + T, T, K), ids, w, "silu", f"moe {fmt}/{fmt_down} F={F} T={T}")
+
+
+@pytest.mark.parametrize("fmt", ("q8_0", "q4k", "q6k", "q5k", "q4_0"))
+@pytest.mark.parametrize("F", (512, 4096))
+def test_moe_scales_of_zero_and_wide_ranges(fmt, F):
+    """Blocks, groups and rows of zeros, constants and offsets far above their
+    spread (scales of 0, minimums of many scales), first in a row, inside and
+    last; tokens of zeros, of one value, and over thirty binades."""
+    E, K, k = 4, 768, 2
+    L = Layer.__new__(Layer)
+    L.fmt, L.fmt_down, L.E, L.F, L.K, L.dev, L.W, L.A = fmt, fmt, E, F, K, [], [], []
+    for i, (n, kk) in enumerate(((E * F, K), (E * F, K), (E * K, F))):
+        w = synth.weights_bf16(47000 + i, n, kk, outliers=False).reshape(n, kk)
+        one = np.float32(1 / 64).view(np.uint32) >> 16
+        w[0::16, :256] = 0                   # a group of zeros first,
+        w[1::16, 256:512] = 0                # inside
+        w[2::16, -256:] = 0                  # and last
+        w[3::16] = 0                         # nothing but zeros
+        w[4::16] = one                       # a constant row
+        w[5::16, 32:64] = one                # a constant block
+        w[6::16] = one + (w[6::16] & 1)      # the spread far below the offset
+        w[7::16, :256] = one | 0x8000
+        w[8::16, 64:] = 0                    # two blocks alone
+        L.dev.append(ql.isq(fmt, to_dev_bf16(w)))
+        W = oracle.dequant(fmt, oracle.quantize(fmt, w), n, kk)
+        L.W.append(W.reshape(E, n // E, kk))
+        A = np.repeat(np.abs(W).reshape(n, kk // 32, 32).max(2), 32, 1)
+        L.A.append(A.reshape(E, n // E, kk))
+    for T in (2, 6, 9, 20, 60):
+        x = synth.activations_bf16(47100 + T, T, K).reshape(T, K)
+        x[0] = 0
+        if T > 2:
+            x[1] = 0x3F80
+            e = np.random.default_rng(T).integers(-15, 16, K)
+            x[2] = (x[2] & 0x807F) | ((127 + e) << 7).astype(np.uint16)
+        ids, w = choice(400 + T, T, E, k, holes=False)
+        L.check(x, ids, w, "relu", f"moe {fmt} F={F} T={T}")
+
+
+@pytest.mark.parametrize("T", (2, 9, 40))
+def test_moe_two_streams_at_once(T):
+    """Two calls in flight, each with its own workspace and stream, give what
+    they give alone."""
+    E, F, K, k = 8, 4096, 512, 2
+    L = Layer("q4k", "q6k", E, F, K, 48000)
+    args = []
+    for i in range(2):
+        ids, w = choice(500 + i, T, E, k, holes=False)
+        args.append((to_dev_bf16(synth.activations_bf16(48100 + i, T, K)), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()))
+    n = ql.moe_workspace_bytes("q4k", "q6k", T, E, k, F, K)
+    bufs = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    outs = [[torch.zeros((T, K), device="cuda") for _ in range(8)] for _ in range(2)]
+
+    def call(i, out):
+        ql.qmatmul_moe("q4k", *L.dev, *args[i], E, F, fmt_down="q6k", out=out, workspace=bufs[i])
+
+    alone = [torch.zeros((T, K), device="cuda") for _ in range(2)]
+    for i in range(2):
+        call(i, alone[i])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for r in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(i, outs[i][r])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in range(8):
+            assert torch.equal(outs[i][r], alone[i])
+
+
 def test_moe_long_rows():
     """Rows long enough for every wave of a workgroup and a second pass (K =
     18432: 576 chunks), and a down product over eight choices (2048 chunks)."""
