@@ -3,13 +3,12 @@
 // and the router's choice that produces ids and w.
 //
 // Two forms.
-//   Few tokens: two kernels.  moe_glu_kernel computes H[t][j] = act(g) * u, a
+//   Few pairs an expert: two kernels.  moe_glu_kernel computes H[t][j] = act(g) * u, a
 //   workgroup per (token, choice) and group of rows; moe_down_kernel computes
 //   Y, a workgroup per token and group of output rows, whose lanes walk the
 //   chunks of all k chosen experts' rows at once, so the join over the
 //   choices is the reduction over the lanes and no partial result is stored.
-//   More tokens: the (token, choice) pairs are sorted by expert
-//   (moe_plan_kernel), two grouped matrix-core products run over tiles of one
+//   More: the (token, choice) pairs are sorted by expert, two grouped matrix-core products run over tiles of one
 //   expert's pairs, and moe_join_kernel adds each token's k results in the
 //   order of its choices.
 //
@@ -322,7 +321,6 @@ __device__ __forceinline__ void load_raw(const Mat &w, const At<FMT> &p, int64_t
     }
 }
 
-__device__ __forceinline__ float ub(uint32_t w, int b) { return (float)((w >> (8 * b)) & 0xffu); }
 __device__ __forceinline__ float sb(uint32_t w, int b) { return (float)(int8_t)(w >> (8 * b)); }
 
 // Q6K: byte b of lo (hi): four times the signed code of elements 0, 4, 1, 5
@@ -338,37 +336,12 @@ __device__ __forceinline__ void q6k_bytes(uint32_t lw, uint32_t H, uint32_t &lo,
     hi = (((lw >> 2) & 0x3C3C3C3Cu) | (t1 << 6)) ^ 0x80808080u;
 }
 
-// sum over the chunk of w * a; asum = sum of a over the chunk (Q4K's mins)
+// sum over the chunk of w * a (every format but Q4K, whose activations are
+// bf16 pairs or digits)
 template <int FMT>
-__device__ __forceinline__ float dot32(const Mat &w, const Raw<FMT> &r, int c, const float (&a)[32], float asum)
+__device__ __forceinline__ float dot32(const Mat &w, const Raw<FMT> &r, const float (&a)[32])
 {
-    if constexpr (FMT == FMT_Q4K) {
-        const int h = (int)r.h, j = c & 7;
-        const uint32_t h0 = __builtin_amdgcn_update_dpp(0, h, 0x00, 0xF, 0xF, false);
-        const uint32_t h1 = __builtin_amdgcn_update_dpp(0, h, 0x55, 0xF, 0xF, false);
-        const uint32_t h2 = __builtin_amdgcn_update_dpp(0, h, 0xAA, 0xF, 0xF, false);
-        const uint32_t h3 = __builtin_amdgcn_update_dpp(0, h, 0xFF, 0xF, 0xF, false);
-        const uint32_t sc = ((h1 >> (4 * j)) & 15u) | ((h3 >> (2 * j)) & 3u) << 4;
-        const uint32_t mq = ((h2 >> (4 * j)) & 15u) | ((h3 >> (16 + 2 * j)) & 3u) << 4;
-        const float S = f16_bits_to_f32(h0) * (float)sc, Mn = f16_bits_to_f32(h0 >> 16) * (float)mq;
-        const uint32_t cw[4] = {r.c.x, r.c.y, r.c.z, r.c.w};
-        float d0 = 0.0f, d1 = 0.0f;
-#pragma unroll
-        for (int q = 0; q < 4; q++) {
-            // bytes of the low nibbles: elements 0, 4, 1, 5; of the high ones: 2, 6, 3, 7
-            const uint32_t lo = cw[q] & 0x0F0F0F0Fu, hi = (cw[q] >> 4) & 0x0F0F0F0Fu;
-            const float *x = a + 8 * q;
-            d0 = fmaf(ub(lo, 0), x[0], d0);
-            d1 = fmaf(ub(lo, 1), x[4], d1);
-            d0 = fmaf(ub(lo, 2), x[1], d0);
-            d1 = fmaf(ub(lo, 3), x[5], d1);
-            d0 = fmaf(ub(hi, 0), x[2], d0);
-            d1 = fmaf(ub(hi, 1), x[6], d1);
-            d0 = fmaf(ub(hi, 2), x[3], d0);
-            d1 = fmaf(ub(hi, 3), x[7], d1);
-        }
-        return fmaf(S, d0 + d1, -Mn * asum);
-    } else if constexpr (FMT == FMT_Q6K) {
+    if constexpr (FMT == FMT_Q6K) {
         const float d = f16_bits_to_f32(r.d);
         const uint32_t lw[4] = {r.lo.x, r.lo.y, r.lo.z, r.lo.w};
         const uint32_t hw[2] = {r.hi.x, r.hi.y};
@@ -424,7 +397,6 @@ template <> struct Acts<true> {
 };
 template <> struct Acts<false> {
     float a[32];
-    float sum;  // Q4K only
 };
 
 typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
@@ -475,7 +447,7 @@ __device__ __forceinline__ float dot(const Mat &w, const Raw<FMT> &r, int c, con
         }
         return fmaf(S, d0 + d1, -Mn * x.sum);
     } else {
-        return dot32<FMT>(w, r, c, x.a, x.sum);
+        return dot32<FMT>(w, r, x.a);
     }
 }
 
@@ -525,8 +497,10 @@ __device__ __forceinline__ void write_digits(float h, uint4 *__restrict__ out, b
     b[0] = (int8_t)d0;
     b[32] = (int8_t)d1;
     b[64] = (int8_t)d2;
+    // whole numbers hold no infinity and no NaN: the chunk's unit does
+    const bool finite = m < INFINITY && sum == sum;
     if (i == 0)
-        *reinterpret_cast<float2 *>(out + 6) = make_float2(__builtin_amdgcn_ldexpf(1.0f, -e), sum);
+        *reinterpret_cast<float2 *>(out + 6) = make_float2(finite ? __builtin_amdgcn_ldexpf(1.0f, -e) : NAN, sum);
 }
 
 struct Digits {
@@ -667,7 +641,8 @@ __global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint
                         }
                     }
                 }
-                x.sum = sum;
+                if constexpr (PAIRS)
+                    x.sum = sum;
             }
         };
         auto use = [&](int g, const Rows &w) {
@@ -752,7 +727,6 @@ __global__ __launch_bounds__(512) void moe_down_kernel(Mat wd, const void *__res
                     x.unit = live ? __uint_as_float(hq[6].x) * wt : 0.0f;
                     x.sum = live ? __uint_as_float(hq[6].y) * wt : 0.0f;
                 } else {
-                    x.sum = 0.0f;
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         x.a[4 * i] = live ? __uint_as_float(hq[i].x) * wt : 0.0f;
@@ -1054,11 +1028,11 @@ __global__ __launch_bounds__(256) void moe_gemm_kernel(Mat w0, Mat w1, const uin
 // D[m = 4 g + i][n = r]: tokens are the A operand, so that a lane's results
 // belong to the row whose scales it holds.
 //
-// Two kernels.  moe_thin_kernel, up to 32 pairs an expert (TM <= 2 tiles of 16):
-// the waves read X from the caches straight into operands, there is no barrier
+// Two kernels.  moe_thin_kernel, tiles of 16 pairs, for few pairs an expert: the
+// waves read X from the caches straight into operands, there is no barrier
 // in the loop, and the weights stream; in the down product the eight waves of
-// a workgroup split the row and add their sums through LDS.  moe_wide_kernel,
-// more pairs: tiles of 64 pairs whose slabs are staged in LDS, double
+// a workgroup split the row and add their sums through LDS.  moe_wide_kernel:
+// tiles of 64 pairs whose slabs are staged in LDS, double
 // buffered, and shared by four waves of 64 rows each, so that a weight is
 // decoded once per 64 pairs.
 // ---------------------------------------------------------------------------

@@ -273,10 +273,14 @@ int q_moe_route(const float *logits, int64_t T, int64_t E, int top_k, int score,
  * token without any gives a row of zeros), the same expert twice counts
  * twice.  weights: device fp32 [T][top_k].  Y_fp32: device [T][K],
  * overwritten.  act as in qmatmul_glu.  ids and weights 4-byte aligned.
- * The products between the two weights stay in fp32 for up to four tokens;
- * for more they enter the second product as a pair of bf16 values (16
- * significant bits).  Accuracy: within 1e-3 of the magnitudes summed, as
- * qmatmul.  Results do not depend on the order in which workgroups run.
+ * The values between the two weights, act(g) * u: where the experts are
+ * shared by few tokens (always up to four) they keep fp32 or, for Q4K, Q6K and
+ * Q8_0, 23 bits below the largest of each 32; with more tokens 22 bits (those
+ * three formats; X then keeps every value down to 2^-32 of its token's
+ * largest) or 16 bits (the others).  An infinity or a NaN in a token's X makes
+ * that token's row not finite, and no other.  Accuracy: within 1e-3 of the
+ * magnitudes summed, as qmatmul.  Results do not depend on the order in which
+ * workgroups run.
  * workspace: device, qmatmul_moe_workspace_bytes() bytes, 16-byte aligned,
  * overwritten (nothing in it needs to start at zero); calls that can overlap
  * in time need one each.  T == 0 launches nothing; 0 <= T <= QLINEAR_MAX_M. */

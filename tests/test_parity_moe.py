@@ -175,6 +175,28 @@ def test_moe_scales_of_zero_and_wide_ranges(fmt, F):
         L.check(x, ids, w, "relu", f"moe {fmt} F={F} T={T}")
 
 
+@pytest.mark.parametrize("fmt", ("q8_0", "q4k", "q6k", "q5k"))
+@pytest.mark.parametrize("F,T", ((512, 3), (4096, 9), (512, 40)))
+def test_moe_infinities_and_nan_stay_in_their_token(fmt, F, T):
+    """A token whose X holds an infinity or a NaN has no finite output; the
+    other tokens', which share its experts, are bit for bit what they were.
+    (Every row of the weights meets the value: a product with 0 is NaN.)"""
+    E, K, k = 3, 512, 2
+    L = Layer(fmt, fmt, E, F, K, 49000)
+    ids, w = choice(600 + T, T, E, k, holes=False)
+    x = synth.activations_bf16(49100 + T, T, K).reshape(T, K)
+    want = L.run(x, ids, w, "silu").cpu().numpy()
+    bad = {0: 0x7FC0, T - 1: 0xFF80} if T > 1 else {0: 0x7FC0}
+    for t, v in bad.items():
+        x[t, 37 + t] = v
+    got = L.run(x, ids, w, "silu").cpu().numpy()
+    for t in range(T):
+        if t in bad:
+            assert not np.isfinite(got[t]).any(), t
+        else:
+            assert np.array_equal(got[t], want[t]), t
+
+
 @pytest.mark.parametrize("T", (2, 9, 40))
 def test_moe_two_streams_at_once(T):
     """Two calls in flight, each with its own workspace and stream, give what
