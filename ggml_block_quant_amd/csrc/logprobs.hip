@@ -27,6 +27,12 @@
 // overflow the list (a rising row, a row of ties) is taken again after such a
 // cut and with a threshold of its own, and if even that overflows (thousands
 // of equal logits), by `top` rounds of a maximum over the tile, read again.
+//
+// Bound by the logits' bytes where there are many rows: 2048 of 131072 with eight
+// alternatives 207 us, 5.2 TB/s (a plain read reaches 6.9; the exponentials and
+// the comparisons of 16 logits a thread run beside the next tile's loads).  One
+// row is cut into 11 parts and is all latency: 10 us and 4 us for the join.
+// Measured and not kept: 512 threads with two tiles on their way (136 registers, slower).
 #include "logprobs.h"
 
 namespace ql {
@@ -368,7 +374,8 @@ __global__ __launch_bounds__(NT) void logprobs_kernel(LogprobArgs a, int segs, i
     }
 }
 
-// Joins the parts of a row (a workgroup per row).
+// Joins the parts of a row (a workgroup per row): 4 to 6 us, a launch, the parts'
+// (m, z, w) in order and the rank of every part's keys among all.
 __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a, int segs, const float4 *__restrict__ pstat,
                                                             const uint64_t *__restrict__ pkeys)
 {

@@ -148,7 +148,10 @@ __device__ __forceinline__ float wave_max(float v)
 
 // BIAS: the key is sigmoid(x) + bias in 64 bits (where 32 would let the
 // rounding of e^-x decide between close experts); otherwise it is x itself,
-// in whose order both scores are.
+// in whose order both scores are.  A wave per token, its logits in registers.
+// Few tokens: the launch (3.5 us for one token of 128 experts); many: the k
+// rounds of a maximum over the wave (4096 tokens of 256 experts, k = 8, with
+// bias: 12 us for 4 MB of logits).
 template <int VPT, bool BIAS>
 __global__ __launch_bounds__(256) void moe_route_kernel(const float *__restrict__ logits, int T, int E, int k, int score,
                                                         const float *__restrict__ bias, int renorm, float scale,
@@ -581,6 +584,11 @@ __device__ __forceinline__ void walk(int groups, L load, P ready, U use)
 // A workgroup computes the 32 values of one chunk of H: KS waves along a row
 // (each a chunk of the row per lane and pass) times RW waves of 32 / RW rows.
 // HMODE: 0 fp32, 1 digits in natural order, 2 digits in eo order.
+// Bound by the weights' bytes.  One token, two experts of 14336 x 4096 Q4K (132
+// MB): 26 us, 5.0 TB/s (a plain read of that size reaches 6.9); eight of 768 x
+// 2048 Q8_0 (27 MB): 11 us, of which launch, ramp and the sums across lanes are
+// most.  A wave keeps its chunk of X in registers over all its rows and has the
+// next two rows' loads in flight; with four rows in flight registers spill.
 template <int FMT, int R, int HMODE>
 __global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint16_t *__restrict__ X,
                                                        const int32_t *__restrict__ ids, void *__restrict__ H, int E, int k,
@@ -677,7 +685,11 @@ __global__ __launch_bounds__(512) void moe_glu_kernel(Mat wg, Mat wu, const uint
 }
 
 // Rows n0 .. of Y for token blockIdx.y: lane l of a wave holds chunks l, l +
-// 64 KS, .. of the k choices' rows laid end to end.
+// 64 KS, .. of the k choices' rows laid end to end, so that short rows of F
+// still fill whole waves and no partial result goes through memory.  Bound by
+// the weights' bytes and, near them, by the decode (digits: 122 -> 65 VALU
+// instructions a chunk, 47 -> 17 us): two experts of 4096 x 14336 Q4K (66 MB)
+// 16.5 us, 4.0 TB/s; eight of 2048 x 768 Q8_0 (13 MB) 6 us.
 template <int FMT, int R>
 __global__ __launch_bounds__(512) void moe_down_kernel(Mat wd, const void *__restrict__ H,
                                                         const int32_t *__restrict__ ids, const float *__restrict__ weights,
@@ -767,7 +779,8 @@ __global__ __launch_bounds__(512) void moe_down_kernel(Mat wd, const void *__res
 // ---------------------------------------------------------------------------
 // More tokens: sort the pairs by expert.  One workgroup; counts and cursors
 // in LDS.  The order of an expert's pairs varies from run to run, but a
-// pair's results do not depend on its place.
+// pair's results do not depend on its place.  4.7 us for 48 pairs, 18 us for
+// 4096 (beside the preparation of X).
 // ---------------------------------------------------------------------------
 struct Plan {
     int32_t *tiles;   // [4]: numbers of tiles and of pairs with an expert; then {expert, first, count, 0} per tile
@@ -827,7 +840,8 @@ __global__ __launch_bounds__(1024) void moe_plan_kernel(const int32_t *__restric
     plan_block(ids, P, E, BM, pl);
 }
 
-// Y[t] = sum_j w[t][j] * P[place of (t, j)], in the order of j
+// Y[t] = sum_j w[t][j] * P[place of (t, j)], in the order of j.  Bytes: 2048
+// tokens of 4096, two choices: 101 MB in 18 us, 5.5 TB/s.
 __global__ __launch_bounds__(256) void moe_join_kernel(const float *__restrict__ Pd, const int32_t *__restrict__ place,
                                                        const float *__restrict__ weights, float *__restrict__ Y, int k,
                                                        int64_t K)
@@ -860,7 +874,9 @@ __global__ __launch_bounds__(256) void moe_join_kernel(const float *__restrict__
 // whose k order inside the slab is the same on both operands.  Each fp32
 // value enters as a bf16 pair hi + lo (16 bits of it): weights as hi and lo,
 // X is bf16 already, H as hi and lo, dropping lo * lo; error at most about
-// 2^-16 of sum |w||x|.
+// 2^-16 of sum |w||x|.  Bound by the decode (dequant8 and the bf16 split of
+// every weight): 32 experts of 768 x 2048 Q5K, four a token, 256 tokens: 127 us
+// for the whole layer; 8 of 4096 x 4096 Q4_0, two a token, 32 tokens: 204 us.
 // ---------------------------------------------------------------------------
 constexpr int SLAB = 128, PITCH = 2 * SLAB + 16;
 
@@ -1363,6 +1379,13 @@ __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], cons
         }
 }
 
+// GLU: four waves of 16 NT / 2 rows of gate and of up each, over the whole row.
+// Otherwise eight waves share 16 NT rows, each an eighth of them: the rows of
+// a down product are few and long, and one wave a row would leave most of the
+// chip without loads in flight.  Bound by the weights' loads, which the decode
+// of one slab only partly covers: 21 tokens, two of 8 experts of 14336 x 4096,
+// gate and up in Q4K (528 MB) 173 us, 3.1 TB/s; down in Q6K (385 MB) 172 us,
+// 2.2 TB/s, where each weight also takes four products (two operands, H a pair).
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
                                                                   Order order, int act, float *__restrict__ out,
@@ -1540,6 +1563,13 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
 // group of 256 they are multiplied by D_old / D_new (a group of scale 0 keeps
 // D), which needs no second set of accumulators; Q4K's minimums enter as
 // -(dmin / D) m.  Q8_0 adds each block's products times its scale.
+// Bound by the decode and the products sharing the SIMDs' issue: 2048 tokens,
+// two of 8 experts of 14336 x 4096 Q4K: gate and up 1.41 ms (0.68 PFLOP/s), down
+// 1.09 ms (two products per weight, H being a pair: 0.88 PFLOP/s of them).  515
+// tokens, six of 64 experts of 1408 x 2048 Q8_0 (48 pairs an expert): 221 and 132
+// us, half of it waits for weights and barriers.  Measured and not kept: tiles
+// of 32 and of 128 pairs, 32 rows a wave, three buffers of X, streaming weight
+// loads (the tiles of an expert share them in the caches).
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N, Order order,
                                                           int act, float *__restrict__ out, int64_t out_pitch)
@@ -1837,7 +1867,8 @@ __device__ void row_to_f16(const void *__restrict__ src, int n, int64_t pitch, u
     }
 }
 
-// Block T sorts the pairs; block t < T prepares X[t].
+// Block T sorts the pairs; block t < T prepares X[t].  2048 tokens of 4096: 18 us,
+// the sort of their 4096 pairs.
 __global__ __launch_bounds__(1024) void moe_prep_kernel(const int32_t *__restrict__ ids, int P, int E, int BM, Plan pl,
                                                         const uint16_t *__restrict__ X, int T, int64_t K,
                                                         uint16_t *__restrict__ xh, uint4 *__restrict__ sums,
@@ -1850,7 +1881,9 @@ __global__ __launch_bounds__(1024) void moe_prep_kernel(const int32_t *__restric
         row_to_f16<false>(X + t * K, (int)K, pitch, xh + t * pitch, nullptr, sums + t * (pitch / 32), unit + t);
 }
 
-// H of the sorted pairs for the down product
+// H of the sorted pairs for the down product.  Bytes: 4096 pairs of 14336 (235 MB
+// in, 264 MB out) 108 us, 4.6 TB/s.  (The gate and up product cannot write this
+// form itself: the unit needs the maximum over the whole row.)
 __global__ __launch_bounds__(512) void moe_h_kernel(const float *__restrict__ H, Plan pl, int F, uint16_t *__restrict__ hi,
                                                     uint16_t *__restrict__ lo, uint4 *__restrict__ sums,
                                                     float *__restrict__ unit, int64_t pitch)
