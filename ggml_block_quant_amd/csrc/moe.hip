@@ -173,7 +173,10 @@ __global__ __launch_bounds__(256) void moe_route_kernel(const float *__restrict_
         x[i] = v;
         m = fmaxf(m, v);
         if constexpr (BIAS)
-            key[i] = v > -INFINITY ? 1.0 / (1.0 + exp(-(double)v)) + (double)bias[e] : -(double)INFINITY;
+        {
+            const double b = v > -INFINITY ? (double)bias[e] : -(double)INFINITY;
+            key[i] = b == b ? 1.0 / (1.0 + exp(-(double)v)) + b : -(double)INFINITY;
+        }
         else
             key[i] = v;
     }
@@ -1046,8 +1049,8 @@ __global__ __launch_bounds__(256) void moe_gemm_kernel(Mat w0, Mat w1, const uin
 //
 // Two kernels.  moe_thin_kernel, tiles of 16 pairs, for few pairs an expert: the
 // waves read X from the caches straight into operands, there is no barrier
-// in the loop, and the weights stream; in the down product the eight waves of
-// a workgroup split the row and add their sums through LDS.  moe_wide_kernel:
+// in the loop, and the weights stream; waves split a row and add their sums
+// through LDS.  moe_wide_kernel:
 // tiles of 64 pairs whose slabs are staged in LDS, double
 // buffered, and shared by four waves of 64 rows each, so that a weight is
 // decoded once per 64 pairs.
@@ -1379,21 +1382,27 @@ __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], cons
         }
 }
 
-// GLU: four waves of 16 NT / 2 rows of gate and of up each, over the whole row.
-// Otherwise eight waves share 16 NT rows, each an eighth of them: the rows of
-// a down product are few and long, and one wave a row would leave most of the
-// chip without loads in flight.  Bound by the weights' loads, which the decode
-// of one slab only partly covers: 21 tokens, two of 8 experts of 14336 x 4096,
-// gate and up in Q4K (528 MB) 173 us, 3.1 TB/s; down in Q6K (385 MB) 172 us,
-// 2.2 TB/s, where each weight also takes four products (two operands, H a pair).
+// Four waves: in the gate and up product two along a row times two of 16 NT / 2
+// rows of gate and of up each, in the down product, whose rows are few and long,
+// four along a row of the same 16 NT; their sums meet in LDS.  Bound by the
+// weights' loads, which the decode of one slab only partly covers: 21 tokens,
+// two of 8 experts of 14336 x 4096, gate and up in Q4K (528 MB) 176 us, 3.0
+// TB/s; down in Q6K (385 MB) 163 us, 2.4 TB/s, where each weight also takes four
+// products (two operands, H a pair).  Eight waves along a row of down: 182 us (a
+// CU then holds one workgroup, and its start and end lie bare).  Gate and up with
+// one, two, four waves along a row, 8 of 4096 x 4096 Q8_0, 48 tokens, whole
+// layer: 244, 215, 207 us; 8 of 14336 x 4096 Q4K, 24 tokens: 293, 289, 306 us.
+constexpr int thin_kw(bool glu) { return glu ? 2 : 4; }
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
-__global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
+__global__ __launch_bounds__(256) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
                                                                   Order order, int act, float *__restrict__ out,
                                                                   int64_t out_pitch)
 {
-    constexpr int WAVES = GLU ? 4 : 8, NF = GLU ? NT / 2 : NT;
-    constexpr bool AHEAD = TM == 1;  // X a slab ahead, where the registers allow
-    __shared__ f32x4_t red[GLU ? 1 : WAVES * NT * TM * 64];
+    constexpr int KW = thin_kw(GLU), RW = 4 / KW, NF = GLU ? NT / 2 : NT;
+    // X a slab ahead; Q8_0's down product keeps its registers for the weights (8
+    // experts of 4096 x 4096, 24 tokens: 168 -> 160 us without)
+    constexpr bool AHEAD = GLU || FMT != FMT_Q8_0;
+    __shared__ f32x4_t red[4 * NT * TM * 64];
     int ti, blk;
     if (!place_of_block(pl.tiles[0], order, ti, blk))
         return;
@@ -1401,9 +1410,9 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
     const int expert = tile.x, first = tile.y, count = tile.z;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, r16 = lane & 15;
-    const int64_t K = w0.K, n_wave = (int64_t)blk * (GLU ? 64 * NF : 16 * NF) + (GLU ? wave * 16 * NF : 0);
+    const int64_t K = w0.K, n_wave = ((int64_t)blk * RW + wave / KW) * (16 * NF);
     const int groups = (int)((K + 255) / 256);
-    const int g0 = GLU ? 0 : groups * wave / WAVES, g1 = GLU ? groups : groups * (wave + 1) / WAVES;
+    const int g0 = groups * (wave % KW) / KW, g1 = groups * (wave % KW + 1) / KW;
     const Planes16 e0 = expert_planes<FMT>(w0, expert * N), e1 = expert_planes<FMT>(w1, expert * N);
     Row16 wrow[NF];
 #pragma unroll
@@ -1537,23 +1546,29 @@ __global__ __launch_bounds__(GLU ? 256 : 512) void moe_thin_kernel(Mat w0, Mat w
                 load_x(u == 0 ? 2 * G + 1 : 2 * next, x16);
         }
     }
-    if constexpr (!GLU) {  // the waves' sums, in order: wave w takes every WAVES-th tile of the result
+    // the sums of the waves along a row, in order
 #pragma unroll
-        for (int i = 0; i < NT; i++)
+    for (int i = 0; i < NT; i++)
 #pragma unroll
-            for (int j = 0; j < TM; j++)
-                red[((wave * NT + i) * TM + j) * 64 + lane] = acc[i][j];
-        __syncthreads();
-        static_assert(NT * TM <= WAVES, "a tile per wave");
-        if (wave >= NT * TM)
-            return;
+        for (int j = 0; j < TM; j++)
+            red[((wave * NT + i) * TM + j) * 64 + lane] = acc[i][j];
+    __syncthreads();
+    if constexpr (!GLU) {  // wave w takes the result's w-th tile
+        static_assert(KW == 4 && NT * TM == 4, "a tile per wave");
         f32x4_t v[1][1] = {{red[wave * 64 + lane]}};
 #pragma unroll
-        for (int w = 1; w < WAVES; w++)
+        for (int w = 1; w < KW; w++)
             v[0][0] += red[(w * NT * TM + wave) * 64 + lane];
         const int i = wave / TM, j = wave % TM;
         store_results<false, 1, 1>(v, x, pl, k, first + 16 * j, count - 16 * j, n_wave + 16 * i, N, out_pitch, act, out);
-    } else {
+    } else if (wave % KW == 0) {
+#pragma unroll
+        for (int w = 1; w < KW; w++)
+#pragma unroll
+            for (int i = 0; i < NT; i++)
+#pragma unroll
+                for (int j = 0; j < TM; j++)
+                    acc[i][j] += red[(((wave + w) * NT + i) * TM + j) * 64 + lane];
         store_results<GLU, NT, TM>(acc, x, pl, k, first, count, n_wave, N, out_pitch, act, out);
     }
 }
@@ -2017,7 +2032,7 @@ template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, hipStream_t s)
 {
     constexpr bool THIN = TM == 1;
-    const int64_t N = GLU ? a.F : a.K, K = GLU ? a.K : a.F, per = GLU ? 32 * NT : THIN ? 16 * NT : 64 * NT;
+    const int64_t N = GLU ? a.F : a.K, K = GLU ? a.K : a.F, per = (THIN ? 4 / thin_kw(GLU) : 4) * 16 * (GLU ? NT / 2 : NT);
     const Planes p = planes_of(FMT, a.E * N, K);
     const Mat w0{GLU ? a.gate : a.down, p, K}, w1{GLU ? a.up : a.down, p, K};
     const auto u16 = [&](int64_t at) { return reinterpret_cast<const uint16_t *>(a.ws + at); };
@@ -2032,7 +2047,7 @@ hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, 
     float *out = f32(GLU ? l.h32 : l.pd);
     const int64_t pitch = GLU ? l.fp : a.K;
     if constexpr (THIN)
-        moe_thin_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), GLU ? 256 : 512, 0, s>>>(w0, w1, x, pl, a.k, N, order,
+        moe_thin_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, order,
                                                                                          a.act, out, pitch);
     else
         moe_wide_kernel<FMT, TM, NT, GLU, TAIL><<<dim3((unsigned)grid), 256, 0, s>>>(w0, w1, x, pl, a.k, N, order, a.act, out,
@@ -2101,15 +2116,17 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
         digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d) && a.F * a.K < (int64_t(1) << 31) && 2 * a.T * l.kp < (int64_t(1) << 32);
     // Pairs per tile, 16 or 64, from the mean number of an expert's pairs.  Tuned
     // formats (thin against wide, us): 8 experts of 14336 x 4096 Q4K, 12 pairs
-    // each 384 / 441, 16 pairs 480 / 446; 8 of 4096 x 4096 Q8_0, 12 pairs 234 /
-    // 263, 16 pairs 301 / 266.  The thin kernel's down product splits rows of F
-    // over eight waves, which short rows do not feed: 128 of 768 x 2048, 3 pairs
-    // each 176 / 156, 64 of 1536 x 2048, 3 pairs each 191 / 198, 9 pairs 228 / 195.
+    // each 336 / 443, 16 pairs 487 / 447; 8 of 4096 x 4096 Q8_0, 12 pairs 184 /
+    // 263, 20 pairs 303 / 267.  The thin kernel's down product splits rows of F
+    // over four waves, which short rows feed less: 16 of 2048 x 4096 Q4K, 6 pairs
+    // 114 / 151, 12 pairs 159 / 154; 64 of 1536 x 2048, 6 pairs 183 / 188, 9 pairs
+    // 204 / 190; 128 of 768 x 2048, 3 pairs 181 / 150.
     // Other formats (16 against 64 pairs): 8 of 4096 x 4096 Q4_0, 16 pairs 274 /
     // 310, 32 pairs 370 / 277; 32 of 768 x 2048 Q5K, 8 pairs 118 / 121, 16 pairs
     // 153 / 123.
     const int per = P / a.E;
-    Shape sh{per <= 12 && (!tuned || a.F >= 4096) ? 1 : 4, 0};
+    const int most = !tuned || a.F >= 4096 ? 12 : a.F >= 1536 ? 8 : 0;
+    Shape sh{per <= most ? 1 : 4, 0};
     const int BM = 16 * sh.tm, max_tiles = P / BM + (P < a.E ? P : a.E);
     sh.max_tiles = max_tiles;
     const Plan pl{reinterpret_cast<int32_t *>(a.ws + l.tiles), reinterpret_cast<int32_t *>(a.ws + l.pair),

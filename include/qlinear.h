@@ -251,7 +251,8 @@ int qmatmul_glu(int fmt, const void *gate_blocks, const void *up_blocks, const v
  * weights: device fp32 [T][top_k], p of the chosen, divided by their sum when
  * renorm != 0, times `scale`.
  * A logit of -inf (or NaN) switches an expert off for that token: it is
- * never chosen and adds nothing to the softmax.  Where fewer than top_k are
+ * never chosen and adds nothing to the softmax; so does a bias of -inf (or
+ * NaN) for every token.  Where fewer than top_k are
  * left the last ids are -1 with weight 0.  +inf counts as the largest finite
  * value.  All pointers 4-byte aligned.  T == 0 launches nothing. */
 enum { QSCORE_SOFTMAX = 0, QSCORE_SIGMOID = 1 };

@@ -428,3 +428,24 @@ def test_route_into_given_buffers_and_empty():
     assert torch.allclose(w.sum(1), torch.ones(5, device="cuda"), atol=5 * 2.0 ** -23)
     ids, w = ql.moe_route(x[:0], 4)
     assert ids.shape == (0, 4) and w.shape == (0, 4)
+
+
+def test_route_bias_that_switches_off():
+    """A bias of -inf or NaN: the expert is never chosen, by any token; one of
+    +inf: always, the lowest such expert first."""
+    T, E, k = 9, 130, 8
+    x = np.random.default_rng(5).standard_normal((T, E)).astype(np.float32)
+    b = np.zeros(E, np.float32)
+    b[[0, 64, 129]] = np.nan
+    b[[1, 63, 128]] = -np.inf
+    b[[70, 5]] = np.inf
+    ids, w = ql.moe_route(torch.from_numpy(x).cuda(), k, score="sigmoid", bias=torch.from_numpy(b).cuda())
+    ids, w = ids.cpu().numpy(), w.cpu().numpy()
+    off = (0, 64, 129, 1, 63, 128)
+    for t in range(T):
+        rest = sorted((e for e in range(E) if e not in off and e not in (5, 70)), key=lambda e: (-np.float64(x[t, e]), e))
+        assert list(ids[t]) == [5, 70] + rest[:k - 2]
+    assert np.isfinite(w).all()
+    b[:] = np.nan
+    ids, w = ql.moe_route(torch.from_numpy(x).cuda(), k, score="sigmoid", bias=torch.from_numpy(b).cuda())
+    assert (ids == -1).all() and (w == 0).all()
