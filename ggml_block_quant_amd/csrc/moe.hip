@@ -2041,8 +2041,6 @@ hipError_t mm(const MoeArgs &a, const Layout &l, const Plan &pl, int max_tiles, 
     const Acts16 x = GLU ? Acts16{u16(l.xh), nullptr, u4(l.xsum), f32(l.xunit), l.kp}
                          : Acts16{u16(0), u16(l.hlo), u4(l.hsum), f32(l.hunit), l.fp};
     const int64_t nblk = (N + per - 1) / per, grid = (nblk * max_tiles + 7) / 8 * 8;
-    if (grid >= (int64_t(1) << 31))
-        return hipErrorNotSupported;
     const Order order{(int)nblk, 8};
     float *out = f32(GLU ? l.h32 : l.pd);
     const int64_t pitch = GLU ? l.fp : a.K;

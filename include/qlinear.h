@@ -284,7 +284,8 @@ int q_moe_route(const float *logits, int64_t T, int64_t E, int top_k, int score,
  * workgroups run.
  * workspace: device, qmatmul_moe_workspace_bytes() bytes, 16-byte aligned,
  * overwritten (nothing in it needs to start at zero); calls that can overlap
- * in time need one each.  T == 0 launches nothing; 0 <= T <= QLINEAR_MAX_M. */
+ * in time need one each.  T == 0 launches nothing; 0 <= T <= QLINEAR_MAX_M,
+ * T * top_k * F and T * top_k * K at most 2^36. */
 size_t qmatmul_moe_workspace_bytes(int fmt_gate_up, int fmt_down, int64_t T, int64_t E, int top_k, int64_t F, int64_t K);
 int qmatmul_moe(int fmt_gate_up, const void *gate_blocks, const void *up_blocks, int fmt_down, const void *down_blocks,
                 const void *X_bf16, const int32_t *ids, const float *weights, float *Y_fp32, int64_t T, int64_t E,

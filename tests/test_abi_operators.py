@@ -145,3 +145,14 @@ def test_wrappers_check_tensors():
 def test_python_constants_match():
     assert ctypes.sizeof(ctypes.c_void_p) == 8
     assert ql.MAX_TOP_N == 64 and ql.SCORE == {"softmax": 0, "sigmoid": 1}
+
+
+def test_moe_size_limit():
+    """T * top_k * F and T * top_k * K up to 2^36: one more token is refused
+    before any launch, with or without a size for its workspace."""
+    size = ql.lib().qmatmul_moe_workspace_bytes
+    assert size(0, 0, 32768, 16, 32, 1 << 16, 32) > 0            # 2^36 values of H
+    assert size(0, 0, 32769, 16, 32, 1 << 16, 32) == 0
+    assert size(0, 0, 32769, 8, 32, 32, 1 << 16) == 0
+    assert moe(fmt=0, fd=0, T=32769, E=16, k=32, F=1 << 16, K=32) == ESHAPE
+    assert moe(fmt=0, fd=0, T=32769, E=8, k=32, F=32, K=1 << 16) == ESHAPE
