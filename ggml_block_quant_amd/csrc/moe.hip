@@ -1217,15 +1217,22 @@ __device__ __forceinline__ uint32_t and_or(uint32_t a, uint32_t mask, uint32_t c
     return r;
 }
 
-// the fp16 operands of steps 2 h, 2 h + 1 of a slab (h = 0, 1)
+// The fp16 operands of steps 2 h, 2 h + 1 of a slab (h = 0, 1).  DROP (Q4K): where
+// the group's scale is 0 its sub-scales count as 0 too, whatever they and the
+// codes hold: the wide kernel's sums are multiplied by the last scale that is
+// not 0.  2048 tokens, two of 8 experts of 14336 x 4096, whole layer: 2.68 ms
+// with and without (boxes in turn, to 2 %); done in the head's dwords, once per
+// group, 2.82 (spills), behind a branch 2.75.
 template <int FMT> constexpr int PER = FMT == FMT_Q6K ? 2 : 1;  // operands per step
-template <int FMT>
+template <int FMT, bool DROP>
 __device__ __forceinline__ void decode_half(const Nibbles &nb, const Codes16<FMT> &t, const Head16<FMT> &hd, int u, int g,
                                             int h, f16x8_t (&o)[2][PER<FMT>])
 {
     if constexpr (FMT == FMT_Q4K) {
         const int j = 4 * u + g;
-        const uint32_t sc = __builtin_amdgcn_ubfe(hd.h.y, 4 * j, 4) | (__builtin_amdgcn_ubfe(hd.h.w, 2 * j, 2) << 4);
+        uint32_t sc = __builtin_amdgcn_ubfe(hd.h.y, 4 * j, 4) | (__builtin_amdgcn_ubfe(hd.h.w, 2 * j, 2) << 4);
+        if constexpr (DROP)
+            sc = (hd.h.x & 0x7FFFu) ? sc : 0u;
         const _Float16 sh = (_Float16)(float)sc;
         const f16x2_t S = {sh, sh}, S16 = S * (_Float16)0.0625f, N = S * (_Float16)-1024.0f, N16 = S * (_Float16)-64.0f;
         const uint32_t cw[2] = {h ? t.c.z : t.c.x, h ? t.c.w : t.c.y};
@@ -1494,8 +1501,8 @@ __global__ __launch_bounds__(256) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x,
             for (int i = 0; i < NT; i++) {
                 f16x8_t o[2][2][PER<FMT>];
                 float d[4];
-                decode_half<FMT>(nb, raw[u % RAWS][i], rawh[i], u, g, 0, o[0]);
-                decode_half<FMT>(nb, raw[u % RAWS][i], rawh[i], u, g, 1, o[1]);
+                decode_half<FMT, false>(nb, raw[u % RAWS][i], rawh[i], u, g, 0, o[0]);
+                decode_half<FMT, false>(nb, raw[u % RAWS][i], rawh[i], u, g, 1, o[1]);
 #pragma unroll
                 for (int q = 0; q < (FMT == FMT_Q8_0 ? 4 : 1); q++)
                     d[q] = scale_of<FMT>(raw[u % RAWS][i], rawh[i], q);
@@ -1576,9 +1583,10 @@ __global__ __launch_bounds__(256) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x,
 
 // Four waves of 16 NT rows over a tile of 16 TM pairs.  The accumulators hold
 // the sum in units of the current scale D of each row (Q4K, Q6K): at a new
-// group of 256 they are multiplied by D_old / D_new (a group of scale 0 keeps
-// D), which needs no second set of accumulators; Q4K's minimums enter as
-// -(dmin / D) m.  Q8_0 adds each block's products times its scale.
+// group of 256 they are multiplied by D_old / D_new, which needs no second set
+// of accumulators; a group of scale 0 keeps D, and its sub-scales count as 0.
+// Q4K's minimums enter as -(dmin / D) m.  Q8_0 adds each block's products times
+// its scale.
 // Bound by the decode and the products sharing the SIMDs' issue: 2048 tokens,
 // two of 8 experts of 14336 x 4096 Q4K: gate and up 1.41 ms (0.68 PFLOP/s), down
 // 1.09 ms (two products per weight, H being a pair: 0.88 PFLOP/s of them).  515
@@ -1730,7 +1738,11 @@ __global__ __launch_bounds__(256, 2) void moe_wide_kernel(Mat w0, Mat w1, Acts16
                 float sc[NT][2];
 #pragma unroll
                 for (int i = 0; i < NT; i++) {
-                    decode_half<FMT>(nb, raw[u % RAWS][i], hd[i], u, g, h, o[i]);
+                    if constexpr (FMT == FMT_Q6K) {  // (as DROP, once per slab)
+                        if (h == 0)
+                            raw[0][i].sc = (hd[i].d & 0x7FFFu) ? raw[0][i].sc : 0u;
+                    }
+                    decode_half<FMT, FMT == FMT_Q4K>(nb, raw[u % RAWS][i], hd[i], u, g, h, o[i]);
                     if constexpr (!RUN) {
                         sc[i][0] = scale_of<FMT>(raw[u % RAWS][i], hd[i], 2 * h);
                         sc[i][1] = scale_of<FMT>(raw[u % RAWS][i], hd[i], 2 * h + 1);
