@@ -374,7 +374,9 @@ def qmatmul_moe(fmt, gate_blocks: torch.Tensor, up_blocks: torch.Tensor, down_bl
     """Mixture-of-experts layer as fp32 [T][K]: sum over j of weights[t][j] *
     Wd[e] . (act(Wg[e] . x) * (Wu[e] . x)), e = ids[t][j], for the blocks of the
     experts' stacked [E*F][K] gate and up weights (``fmt``) and [E*K][F] down
-    weights (``fmt_down``, by default ``fmt``).  ids outside [0, E) add nothing."""
+    weights (``fmt_down``, by default ``fmt``).  ids outside [0, E) add nothing.
+    How the values between the two weights are held, and the accuracy that
+    follows, is stated at qmatmul_moe in include/qlinear.h."""
     if X.dim() != 2 or ids.dim() != 2:
         raise ValueError("X must be 2-D [T][K] and ids 2-D [T][top_k]")
     T, K = X.shape

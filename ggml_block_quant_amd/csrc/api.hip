@@ -77,7 +77,8 @@ int moe_shape(int fmt_gu, int fmt_d, int64_t T, int64_t E, int64_t k, int64_t F,
         return Q_ESHAPE;
     if (check_tensor(fmt_gu, E * F, K, QLINEAR_MAX_N) != Q_OK || check_tensor(fmt_d, E * K, F, QLINEAR_MAX_N) != Q_OK)
         return Q_ESHAPE;
-    // (a workspace of 256 GiB; launches stay below 2^32 threads)
+    // (a workspace below 2^40 bytes: 8.5 per value of H, 4 per value of the
+    // down product, X; launches stay below 2^32 threads in each dimension)
     if (T * k * F > (int64_t(1) << 36) || T * k * K > (int64_t(1) << 36))
         return Q_ESHAPE;
     return Q_OK;

@@ -1037,8 +1037,10 @@ __global__ __launch_bounds__(256) void moe_gemm_kernel(Mat w0, Mat w1, const uin
 // So X costs one product per weight (Q6K two) where a bf16 pair per weight
 // costs two, and only sums round.
 // Activations are fp16 times a power of two per row (row maximum in [2^14,
-// 2^15)): every bf16 value of X down to 2^-32 of its token's largest is exact;
-// H is a pair of fp16, 22 significant bits.
+// 2^15)): every bf16 value of X down to 2^-31 of its token's largest is exact
+// (its last bit is at least fp16's 2^-24), a smaller one is off by at most 2^-25,
+// 2^-39 of that largest; H is a pair of fp16, 22 significant bits, and the same
+// 2^-39 of the row's largest.
 //
 // k order: for Q4K and Q6K lane (g, r) holds block 4 s + g of row r in slab s
 // (one 16-byte load of codes) and step t multiplies octet t of the four
@@ -2122,7 +2124,8 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
         return hipErrorNotSupported;
     }
     const int P = a.T * a.k;
-    // (offsets inside an expert's planes and inside X are 32 bits there)
+    // (offsets inside an expert's planes and inside X are 32 bits there; past
+    // that, and for a pair of formats of which only one is tuned, bf16 pairs)
     const bool tuned =
         digits_fmt(a.fmt_gu) && digits_fmt(a.fmt_d) && a.F * a.K < (int64_t(1) << 31) && 2 * a.T * l.kp < (int64_t(1) << 32);
     // Pairs per tile, 16 or 64, from the mean number of an expert's pairs.  Tuned

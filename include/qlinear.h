@@ -274,14 +274,24 @@ int q_moe_route(const float *logits, int64_t T, int64_t E, int top_k, int score,
  * token without any gives a row of zeros), the same expert twice counts
  * twice.  weights: device fp32 [T][top_k].  Y_fp32: device [T][K],
  * overwritten.  act as in qmatmul_glu.  ids and weights 4-byte aligned.
- * The values between the two weights, act(g) * u: where the experts are
- * shared by few tokens (always up to four) they keep fp32 or, for Q4K, Q6K and
- * Q8_0, 23 bits below the largest of each 32; with more tokens 22 bits (those
- * three formats; X then keeps every value down to 2^-32 of its token's
- * largest) or 16 bits (the others).  An infinity or a NaN in a token's X makes
- * that token's row not finite, and no other.  Accuracy: within 1e-3 of the
- * magnitudes summed, as qmatmul.  Results do not depend on the order in which
- * workgroups run.
+ * The values h = act(g) * u between the two weights are held as follows
+ * (h beside its form: the largest error of one value):
+ *   T <= 4 or T * top_k <= 2 E:
+ *     fp32, or for Q4K, Q6K and Q8_0 down weights whole numbers: 2^-22 of the
+ *     largest of its 32;
+ *   more, both formats of Q4K, Q6K and Q8_0, F * K < 2^31 and T * K' < 2^31
+ *   (K' = K rounded up to 256):
+ *     a pair of fp16: 2^-23 of h plus 2^-39 of the largest of its F.  X is held
+ *     in fp16 times a power of two per token as well: exact down to 2^-31 of
+ *     the token's largest value, below it an error of 2^-39 of that largest;
+ *   more, any other formats or sizes:
+ *     a pair of bf16: 2^-16 of h; the weights too: 2^-16 of each.
+ * Everything else is fp32 sums.  Accuracy: within 1e-3 of the magnitudes
+ * summed, as qmatmul, where h counts as at least 2^-12 of the largest of its
+ * 32 in the first form, and in the second h and x as at least 2^-29 of the
+ * largest of their row, also where that largest meets weights of 0.
+ * An infinity or a NaN in a token's X makes that token's row not finite, and
+ * no other.  Results do not depend on the order in which workgroups run.
  * workspace: device, qmatmul_moe_workspace_bytes() bytes, 16-byte aligned,
  * overwritten (nothing in it needs to start at zero); calls that can overlap
  * in time need one each.  T == 0 launches nothing; 0 <= T <= QLINEAR_MAX_M,

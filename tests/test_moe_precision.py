@@ -38,11 +38,12 @@ TUNED = ("q8_0", "q4k", "q6k")
 LEG = ("q4_0", "q4_1", "q5_0", "q5_1")
 
 
-def form_of(fmt, fmt_down, T, E, k):
+def form_of(fmt, fmt_down, T, E, k, F=0, K=0):
     """How H is held between the two products (include/qlinear.h)."""
     if T <= 4 or T * k <= 2 * E:
         return "digits" if fmt_down in TUNED else "fp32"
-    return "fp16" if fmt in TUNED and fmt_down in TUNED else "bf16"
+    fits = F * K < 2 ** 31 and T * ((K + 255) // 256 * 256) < 2 ** 31
+    return "fp16" if fmt in TUNED and fmt_down in TUNED and fits else "bf16"
 
 
 def h_error(form, h):
@@ -117,9 +118,11 @@ def one_hot(fmt, seed, rows, cols, pos, any_scale=False):
     return f, w[np.arange(rows), pos]
 
 
-def one_hot_layer(fmt, fmt_down, E, F, K, seed, any_scale=False):
+def one_hot_layer(fmt, fmt_down, E, F, K, seed, any_scale=False, first=0):
+    """The layer's (fields, column per row, value per row) of gate, up and down;
+    gate and up leave the columns before `first` zero."""
     rng = np.random.default_rng(seed)
-    gp, up = rng.integers(0, K, (E, F)), rng.integers(0, K, (E, F))
+    gp, up = rng.integers(first, K, (E, F)), rng.integers(first, K, (E, F))
     dp = np.stack([(rng.permutation(max(F, K)) % F)[:K] for _ in range(E)])  # every column where K >= F
     out = []
     for i, (f, rows, cols, pos) in enumerate(((fmt, E * F, K, gp), (fmt, E * F, K, up), (fmt_down, E * K, F, dp))):
@@ -174,7 +177,7 @@ def run_one_hot(fmt, fmt_down, E, F, K, k, T, any_scale=False):
     layer = one_hot_layer(fmt, fmt_down, E, F, K, 61000 + F + T, any_scale)
     x, ids, w = one_hot_inputs(61100 + T, T, E, K, k)
     h = one_hot_h(layer, synth.bf16_bits_to_f32(x).astype(np.float64), ids)
-    form = form_of(fmt, fmt_down, T, E, k)
+    form = form_of(fmt, fmt_down, T, E, k, F, K)
     y, bar = one_hot_bar(layer, form, h, ids, w.astype(np.float64))
     dev = [pack(f, fl[0], E * n, c) for f, fl, n, c in zip((fmt, fmt, fmt_down), layer, (F, F, K), (K, K, F))]
     got = ql.qmatmul_moe(fmt, *dev, to_dev_bf16(x), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), E, F,
@@ -195,6 +198,87 @@ def test_scales_of_any_size_and_sign(fmt, fmt_down, E, F, K, k, T):
     """Scales from the smallest fp16 to the largest powers of two, of either
     sign, side by side in a row.  (Powers of two: a change of units is exact.)"""
     run_one_hot(fmt, fmt_down, E, F, K, k, T, any_scale=True)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt,fmt_down,E,F,K,k,T", [
+    ("q4k", "q4k", 3, 512, 512, 2, 3), ("q8_0", "q8_0", 3, 512, 512, 2, 40), ("q4k", "q6k", 3, 512, 512, 2, 40),
+    ("q6k", "q4k", 4, 4096, 512, 2, 17), ("q5k", "q5k", 3, 256, 512, 2, 24), ("q8_0", "q4_0", 3, 256, 512, 2, 24)])
+@pytest.mark.parametrize("below", (20, 31, 33, 36, 45))
+def test_largest_values_of_x_that_meet_zeros(fmt, fmt_down, E, F, K, k, T, below):
+    """A token whose largest values, 2^below times the others, meet weights of 0:
+    exact but for the fp16 form, and there down to 2^-31 of the largest; below
+    it within 2^-39 of the largest.  That keeps the accuracy of the header: 1e-3
+    where x counts as at least 2^-29 of the largest."""
+    layer = one_hot_layer(fmt, fmt_down, E, F, K, 64000 + F, first=8)
+    x, ids, w = one_hot_inputs(64100 + T, T, E, K, k)
+    v = np.random.default_rng(64200).uniform(1, 2, (T, K))
+    v[:, :8] = 2.0 ** below
+    x = synth.bf16_bits_from_f32((v * 0.25).astype(np.float32))
+    v = synth.bf16_bits_to_f32(x).astype(np.float64)
+    form = form_of(fmt, fmt_down, T, E, k, F, K)
+    h = one_hot_h(layer, v, ids)
+    big = v[:, 0].max()
+    ex = 2.0 ** -39 * big if form == "fp16" and below > 31 else 0.0
+    t = np.arange(T)[:, None, None]
+    (_, gp, gv), (_, up, uv), _ = layer
+    eh = gv[ids] * uv[ids] * (ex * v[t, gp[ids]] + ex * v[t, up[ids]] + ex * ex)
+    y, bar = one_hot_bar(layer, form, h, ids, w.astype(np.float64))
+    bar = bar + one_hot_terms(layer, eh * (1 + 2.0 ** -20) + h_error(form, eh), ids, w.astype(np.float64)).sum(1)
+    counted = np.maximum(v, 2.0 ** -29 * big) if form == "fp16" else v
+    said = 1e-3 * one_hot_terms(layer, one_hot_h(layer, counted, ids), ids, w.astype(np.float64)).sum(1)
+    dev = [pack(f, fl[0], E * n, c) for f, fl, n, c in zip((fmt, fmt, fmt_down), layer, (F, F, K), (K, K, F))]
+    got = ql.qmatmul_moe(fmt, *dev, to_dev_bf16(x), torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(), E, F,
+                         act="relu", fmt_down=fmt_down).cpu().numpy().astype(np.float64)
+    err = np.abs(got - y)
+    assert (err <= bar).all(), f"{form}: {np.max(err / bar):.2f} of the bar"
+    assert (bar <= said).all()
+
+
+def device_one_hot(rows, cols, pos, seed):
+    """A [rows][cols] Q8_0 weight on the device, zero but for column pos[n] of
+    row n, as (block buffer, value per row): codes 64 to 127, scales of 2^-6."""
+    n = rows * cols
+    buf = torch.zeros(n + n // 16, dtype=torch.uint8, device="cuda")
+    code = torch.randint(64, 128, (rows,), device="cuda", generator=torch.Generator("cuda").manual_seed(seed))
+    at = torch.arange(rows, device="cuda") * cols + pos
+    buf[at] = code.to(torch.uint8)
+    assert torch.equal(buf[at].long(), code)
+    buf[n:].view(torch.float16).fill_(2.0 ** -6)
+    return buf, code.double() * 2.0 ** -6
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("F,K,T", [
+    (32768 - 32, 65536, 5), (32768, 65536, 5),      # F * K: the last below 2^31 and 2^31, tiles of 16 pairs
+    (32768 - 32, 65536, 24), (32768, 65536, 24),    # the same, tiles of 64
+    (65536, 32768 - 32, 24), (65536, 32768, 24),
+    (32, 65536, 32767), (32, 65536, 32768),         # T * K
+])
+def test_sizes_on_both_sides_of_the_fp16_form(F, K, T):
+    """The largest sizes whose offsets are 32 bits, and the first past them,
+    where H is held in bf16 pairs: each within the bar of its form."""
+    g = torch.Generator("cuda").manual_seed(65000 + T)
+    pos = [torch.randint(0, c, (r,), device="cuda", generator=g) for r, c in ((F, K), (F, K), (K, F))]
+    for p, c in zip(pos, (K, K, F)):
+        p[-1], p[0] = c - 1, 0   # the last value of the last row
+    (gate, gv), (up, uv), (down, dv) = (device_one_hot(r, c, p, 65100 + i) for i, (r, c, p) in enumerate(zip((F, F, K), (K, K, F), pos)))
+    x = torch.empty((T, K), dtype=torch.bfloat16, device="cuda").uniform_(0.5, 2.0, generator=g)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    w = torch.ones((T, 1), device="cuda")
+    form = form_of("q8_0", "q8_0", T, 1, 1, F, K)
+    assert form == ("fp16" if F * K < 2 ** 31 and T * K < 2 ** 31 else "bf16")
+    got = ql.qmatmul_moe("q8_0", gate, up, down, x, ids, w, 1, F, act="relu")
+    rel = 2.0 ** -23 if form == "fp16" else 2.0 ** -17
+    for a in range(0, T, 2048):
+        xa = x[a:a + 2048].double()
+        h = (xa[:, pos[0]] * gv) * (xa[:, pos[1]] * uv)
+        bar = rel * h + 2.0 ** -39 * h.amax(1, keepdim=True)
+        for c in range(0, K, 8192):
+            p, d = pos[2][c:c + 8192], dv[c:c + 8192]
+            y = h[:, p] * d
+            err = (got[a:a + 2048, c:c + 8192].double() - y).abs()
+            assert (err <= bar[:, p] * d + 9 * U * y).all(), (form, a, c)
 
 
 def round_bits(a, bits):
