@@ -432,6 +432,8 @@ def _logprob_out(out, M, targets, top, like, dev):
 
 
 def logprobs_workspace_bytes(M: int, V: int, top: int = 0) -> int:
+    """Bytes of a workspace for ``logprobs`` of up to M rows of V logits and up
+    to ``top`` alternatives."""
     return int(lib().q_logprobs_workspace_bytes(M, V, top))
 
 
@@ -461,6 +463,8 @@ def logprobs(logits: torch.Tensor, targets: torch.Tensor | None = None, top: int
 
 
 def head_workspace_bytes(fmt, M: int, N: int, K: int, top: int = 0) -> int:
+    """Bytes of a workspace for ``qmatmul_logprobs`` of up to M rows and up
+    to ``top`` alternatives on an [N][K] head."""
     return int(lib().qmatmul_logprobs_workspace_bytes(_fmt(fmt), M, N, K, top))
 
 

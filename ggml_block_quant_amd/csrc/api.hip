@@ -113,10 +113,10 @@ int64_t head_rows(int64_t M, int64_t N)
 }
 size_t head_logits_bytes(int64_t rows, int64_t N) { return (size_t)ql::up16(4 * rows * N); }
 // partial results of the full chunks and of the last, shorter one
-int64_t head_parts_bytes(int64_t M, int64_t rows, int64_t N, int top_n)
+int64_t head_parts_need(int64_t M, int64_t rows, int64_t N, int top_n)
 {
-    const int64_t a = ql::logprobs_workspace(rows, N, top_n), last = M % rows;
-    const int64_t b = last ? ql::logprobs_workspace(last, N, top_n) : 0;
+    const int64_t a = ql::logprobs_need(rows, N, top_n), last = M % rows;
+    const int64_t b = last ? ql::logprobs_need(last, N, top_n) : 0;
     return a > b ? a : b;
 }
 
@@ -440,7 +440,7 @@ int q_logprobs(const float *logits, int64_t M, int64_t V, int64_t ld, const int3
         return Q_ESHAPE;
     if (M == 0)
         return Q_OK;
-    const size_t need = q_logprobs_workspace_bytes(M, V, top_n);
+    const size_t need = (size_t)ql::logprobs_need(M, V, top_n);
     if (need) {
         if (!workspace)
             return Q_EINVAL;
@@ -462,7 +462,7 @@ size_t qmatmul_logprobs_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K
         M * K > kMaxElems || top_n < 0 || top_n > QLINEAR_MAX_TOP_N)
         return 0;
     const int64_t rows = head_rows(M, N);
-    return head_logits_bytes(rows, N) + ql::up16(head_parts_bytes(M, rows, N, top_n));
+    return head_logits_bytes(rows, N) + ql::up16(ql::logprobs_workspace(rows, N, top_n));
 }
 
 int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M, int64_t N, int64_t K,
@@ -481,10 +481,10 @@ int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M,
         return st;
     if (M < 1)
         return Q_ESHAPE;
-    if (workspace_bytes < qmatmul_logprobs_workspace_bytes(fmt, M, N, K, top_n))
-        return Q_EINVAL;
     const int64_t rows = head_rows(M, N);
     const size_t logits_bytes = head_logits_bytes(rows, N);
+    if (workspace_bytes < logits_bytes + ql::up16(head_parts_need(M, rows, N, top_n)))
+        return Q_EINVAL;
     float *logits = static_cast<float *>(workspace);
     uint8_t *parts = static_cast<uint8_t *>(workspace) + logits_bytes;
     const auto *X = static_cast<const uint16_t *>(X_bf16);

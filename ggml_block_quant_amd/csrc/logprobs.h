@@ -18,6 +18,9 @@ struct LogprobArgs {
     uint8_t *ws;
 };
 
+// Bytes of one call, and the most that a call with up to M rows and up to `top`
+// alternatives needs.
+int64_t logprobs_need(int64_t M, int64_t V, int top);
 int64_t logprobs_workspace(int64_t M, int64_t V, int top);
 
 hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s);

@@ -447,10 +447,26 @@ Split split_of(int64_t M, int64_t V, int top)
 
 }  // namespace
 
-int64_t logprobs_workspace(int64_t M, int64_t V, int top)
+int64_t logprobs_need(int64_t M, int64_t V, int top)
 {
     const Split s = split_of(M, V, top);
     return s.segs > 1 ? M * s.segs * (16 + 8 * (int64_t)top) : 0;
+}
+
+// More rows take fewer parts each, so the bytes of a call fall again as M grows;
+// this is the most that any of 1 .. M rows needs.  split_of wants at least w
+// parts a row up to ceil(512 / M) >= w, M <= 511 / (w - 1), or likewise with 4096
+// where w parts keep 16 tiles; w parts wanted are ceil(tiles / ceil(tiles / w)).
+int64_t logprobs_workspace(int64_t M, int64_t V, int top)
+{
+    const int64_t tiles = (V + 3 + TILE - 1) / TILE;
+    int64_t parts = 0;
+    for (int64_t w = 2; w <= 16 && w <= tiles; w++) {
+        const int64_t rows = (w <= tiles / 16 ? 4095 : 511) / (w - 1), per = (tiles + w - 1) / w;
+        const int64_t p = (M < rows ? M : rows) * ((tiles + per - 1) / per);
+        parts = parts > p ? parts : p;
+    }
+    return parts * (16 + 8 * (int64_t)top);
 }
 
 hipError_t launch_logprobs(const LogprobArgs &a, hipStream_t s)

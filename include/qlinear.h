@@ -319,7 +319,8 @@ int qmatmul_moe(int fmt_gate_up, const void *gate_blocks, const void *up_blocks,
  * NaN and +inf break the precondition: the row's values are unspecified, its
  * top_ids stay within [-1, V).  workspace: device,
  * q_logprobs_workspace_bytes() bytes (0: may be NULL), 16-byte aligned,
- * overwritten; calls that can overlap in time need one each.  0 <= M <=
+ * overwritten; that size also serves calls with fewer rows or alternatives of
+ * the same V.  Calls that can overlap in time need one each.  0 <= M <=
  * QLINEAR_MAX_M, 1 <= V <= QLINEAR_MAX_N, 0 <= top_n <= QLINEAR_MAX_TOP_N;
  * M == 0 launches nothing. */
 #define QLINEAR_MAX_TOP_N 64
@@ -332,7 +333,8 @@ int q_logprobs(const float *logits, int64_t M, int64_t V, int64_t ld, const int3
  * holding them: rows go through qmatmul (AUTO path) and q_logprobs in chunks
  * whose logits (at most 2^26, or one row) stay in the workspace.  blocks,
  * X_bf16, N, K as in qmatmul (the [N][K] head), the rest as in q_logprobs
- * with V = N.  The workspace is always needed for M > 0. */
+ * with V = N.  The workspace is always needed for M > 0; the size for M rows
+ * also serves fewer rows or alternatives of the same head. */
 size_t qmatmul_logprobs_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int top_n);
 int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M, int64_t N, int64_t K,
                      const int32_t *targets, int top_n, float *logprob, int32_t *rank, float *entropy, int32_t *top_ids,
