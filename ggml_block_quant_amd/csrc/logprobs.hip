@@ -13,7 +13,9 @@
 //
 // x = -inf is a masked token: e^(x - m) = 0 and it is never an alternative.
 // x - m is clamped at -200 (e^-200 is 0 in fp32), which keeps (x - m) e^(x - m)
-// from becoming inf * 0 at masked places.
+// from becoming inf * 0 at masked places.  e^(x - m) is v_exp_f32 of (x - m) log2 e
+// rounded once to fp32: with the constant's own rounding less than 2 |x - m| 2^-24
+// of the term, which is below 2^-24 of the largest one for every x.
 //
 // Alternatives.  A workgroup walks its part of a row in tiles of 4096 (16
 // logits per thread, the next tile's on the way).  From the first tile it
@@ -29,9 +31,10 @@
 // of equal logits), by `top` rounds of a maximum over the tile, read again.
 //
 // Bound by the logits' bytes where there are many rows: 2048 of 131072 with eight
-// alternatives 207 us, 5.2 TB/s (a plain read reaches 6.9; the exponentials and
-// the comparisons of 16 logits a thread run beside the next tile's loads).  One
-// row is cut into 11 parts and is all latency: 10 us and 4 us for the join.
+// alternatives, a pass of 194 to 205 us from box to box, 5.2 to 5.5 TB/s (a plain
+// read reaches 6.9; the exponentials and the comparisons of 16 logits a thread run
+// beside the next tile's loads).  One row is cut into 11 parts and is all latency:
+// 10 us and 4 us for the join.
 // Measured and not kept: 512 threads with two tiles on their way (136 registers, slower).
 #include "logprobs.h"
 
@@ -425,8 +428,9 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobArgs a, int s
 
 // Parts per row: enough workgroups for the chip (two per CU), and, where a part
 // keeps at least 16 tiles, enough to even out the last round of them (six fit
-// a CU: 2048 rows of 131072 are 1.3 rounds whole and 2.7 in halves, 224 -> 183
-// us); at most 16 (more make the join longer than the pass) and 1024 keys to join.
+// a CU: 2048 rows of 131072 are 1.3 rounds whole and 2.7 in halves, a pass of 217
+// and 205 us on one box); at most 16 (more make the join longer than the pass)
+// and 1024 keys to join.
 struct Split {
     int segs, per;
 };

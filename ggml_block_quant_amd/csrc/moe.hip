@@ -516,7 +516,10 @@ struct Digits {
 
 __device__ __forceinline__ int dot4(uint32_t a, uint32_t b, int c) { return __builtin_amdgcn_sdot4((int)a, (int)b, c, false); }
 
-// 65536 s2 + 256 s1 + s0: the first two exact (below 2^24), one rounding
+// 65536 s2 + 256 s1 + s0.  256 s2 + s1 is a whole number below 2^24 for Q4K (32
+// products of 4 and 8 bits), exact in fp32, so that only the sum rounds; for Q6K
+// (16 of 8 and 8 bits) and Q8_0 (32 of them) it reaches 2^26 and 2^27 and its
+// conversion rounds as well, by 2^-24 of the value.
 __device__ __forceinline__ float digit_sum(int s2, int s1, int s0) { return fmaf((float)((s2 << 8) + s1), 256.0f, (float)s0); }
 
 template <int FMT>
@@ -783,7 +786,8 @@ __global__ __launch_bounds__(512) void moe_down_kernel(Mat wd, const void *__res
 // More tokens: sort the pairs by expert.  One workgroup; counts and cursors
 // in LDS.  The order of an expert's pairs varies from run to run, but a
 // pair's results do not depend on its place.  4.7 us for 48 pairs, 18 us for
-// 4096 (beside the preparation of X).
+// 4096 (beside the preparation of X), and in proportion beyond, where the
+// products grow as fast.
 // ---------------------------------------------------------------------------
 struct Plan {
     int32_t *tiles;   // [4]: numbers of tiles and of pairs with an expert; then {expert, first, count, 0} per tile
@@ -1406,6 +1410,8 @@ __device__ __forceinline__ void store_results(const f32x4_t (&acc)[NT][TM], cons
 // CU then holds one workgroup, and its start and end lie bare).  Gate and up with
 // one, two, four waves along a row, 8 of 4096 x 4096 Q8_0, 48 tokens, whole
 // layer: 244, 215, 207 us; 8 of 14336 x 4096 Q4K, 24 tokens: 293, 289, 306 us.
+// The down product in Q4K, 21 tokens of the same (264 MB): 111 us, 2.4 TB/s; it
+// takes 264 registers, so a CU holds one workgroup of it (Q6K: 220, two).
 constexpr int thin_kw(bool glu) { return glu ? 2 : 4; }
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
 __global__ __launch_bounds__(256) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x, Plan pl, int k, int64_t N,
@@ -1597,7 +1603,10 @@ __global__ __launch_bounds__(256) void moe_thin_kernel(Mat w0, Mat w1, Acts16 x,
 // two of 8 experts of 14336 x 4096 Q4K: gate and up 1.41 ms (0.68 PFLOP/s), down
 // 1.09 ms (two products per weight, H being a pair: 0.88 PFLOP/s of them).  515
 // tokens, six of 64 experts of 1408 x 2048 Q8_0 (48 pairs an expert): 221 and 132
-// us, half of it waits for weights and barriers.  Measured and not kept: tiles
+// us, half of it waits for weights and barriers.  Rows of Q8_0 that end inside a
+// slab of 128 take the TAIL form, whose down product spills 220 bytes a lane and
+// waits for them in the loop: the same with 1376 columns of H, 264 us (219 us
+// gate and up, as with 1408).  Measured and not kept: tiles
 // of 32 and of 128 pairs, 32 rows a wave, three buffers of X, streaming weight
 // loads (the tiles of an expert share them in the caches).
 template <int FMT, int TM, int NT, bool GLU, bool TAIL>
@@ -1939,7 +1948,9 @@ __global__ __launch_bounds__(512) void moe_h_kernel(const float *__restrict__ H,
 // 4096 Q4K, two a token: 8 tokens 247 / 260, 12 tokens 356 / 276; 128 of 768 x
 // 2048 Q4K, eight a token: 32 tokens 118 / 152, 48 tokens 168 / 156; the same in
 // Q8_0: 32 tokens 231 / 251, 48 tokens 334 / 254.  So: up to two pairs an
-// expert; and up to four tokens always, whose products then stay in fp32.
+// expert; and up to four tokens always, whose products then stay in fp32.  (The
+// host knows T k, not how many of the ids stand for an expert or how evenly they
+// fall: a call most of whose ids stand for none is taken for a larger one.)
 bool few(int T, int E, int k) { return T <= 4 || (int64_t)T * k <= 2 * (int64_t)E; }
 
 // Workspace, few tokens: H [T k][F] in 4 bytes a value (fp32; the digits take
@@ -2145,7 +2156,8 @@ hipError_t launch_moe(const MoeArgs &a, hipStream_t s)
     // 204 / 190; 128 of 768 x 2048, 3 pairs 181 / 150.
     // Other formats (16 against 64 pairs): 8 of 4096 x 4096 Q4_0, 16 pairs 274 /
     // 310, 32 pairs 370 / 277; 32 of 768 x 2048 Q5K, 8 pairs 118 / 121, 16 pairs
-    // 153 / 123.
+    // 153 / 123.  The two cross on either side of sixteen pairs; twelve for both
+    // costs the wide experts 36 us there and spares the narrow ones 30.
     const int per = P / a.E;
     const int most = !tuned || a.F >= 4096 ? 12 : a.F >= 1536 ? 8 : 0;
     Shape sh{per <= most ? 1 : 4, 0};

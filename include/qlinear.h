@@ -249,7 +249,7 @@ int qmatmul_glu(int fmt, const void *gate_blocks, const void *up_blocks, const v
  * between close experts); ties go to the lower expert.  The bias takes part
  * in the choice only.  ids: device int32 [T][top_k], in the order of choice.
  * weights: device fp32 [T][top_k], p of the chosen, divided by their sum when
- * renorm != 0, times `scale`.
+ * renorm != 0 (0 where that sum is 0), times `scale`.
  * A logit of -inf (or NaN) switches an expert off for that token: it is
  * never chosen and adds nothing to the softmax; so does a bias of -inf (or
  * NaN) for every token.  Where fewer than top_k are
