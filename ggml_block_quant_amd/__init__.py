@@ -4,8 +4,9 @@ A thin Python binding over the C ABI of ``libqlinear.so`` (declared in
 ``include/qlinear.h``): in-situ quantization of bf16 weights into Q8_0, Q4K
 or Q6K blocks (and Q5K, Q3K, Q2K, Q4_0, Q4_1, Q5_0, Q5_1), the fused
 dequantize-matmul that consumes them, the gated feed-forward projection, the
-mixture-of-experts layer and its router, the quantized embedding lookup and
-the output head's log probabilities.  Every
+mixture-of-experts layer and its router, the quantized embedding lookup, the
+output head's log probabilities, and the gradients through frozen quantized
+weights (linear layer, gated projection, the head's cross entropy).  Every
 step of the computation runs in the library's HIP kernels; this module only
 checks tensors and passes pointers, sizes and the current HIP stream.
 PyTorch provides device memory and streams.
@@ -33,6 +34,7 @@ FMT_NAME = {v: k for k, v in FMT.items()}
 PATH = {"auto": 0, "gemv": 1, "mfma_bf16": 2, "mfma_i8": 3, "mfma_fp8": 4}
 ACT = {"silu": 0, "relu": 1, "sigmoid": 2}
 SCORE = {"softmax": 0, "sigmoid": 1}
+GRAD_TYPE = {torch.float32: 0, torch.bfloat16: 1}  # QTYPE_F32, QTYPE_BF16
 MAX_TOP_N = 64  # QLINEAR_MAX_TOP_N
 
 Q_OK, Q_EINVAL, Q_ESHAPE, Q_EALIGN, Q_ENOTSUP, Q_EHIP, Q_ESCRATCH = 0, -1, -2, -3, -4, -5, -6
@@ -59,6 +61,12 @@ SIGNATURES = {
     "q_logprobs": (_INT, [_P, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "qmatmul_logprobs_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _INT]),
     "qmatmul_logprobs": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _INT, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "qmatmul_grad_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64]),
+    "qmatmul_grad": (_INT, [_INT, _P, _P, _INT, _P, _I64, _I64, _I64, _P, _SZ, _P]),
+    "qmatmul_glu_grad_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64]),
+    "qmatmul_glu_grad": (_INT, [_INT, _P, _P, _P, _P, _INT, _P, _P, _P, _I64, _I64, _I64, _INT, _P, _SZ, _P]),
+    "qmatmul_xent_workspace_bytes": (_SZ, [_INT, _I64, _I64, _I64, _INT]),
+    "qmatmul_xent": (_INT, [_INT, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "q_dequantize": (_INT, [_INT, _P, _I64, _I64, _P, _P]),
     "isq_resolve_level": (_INT, [_INT, _IP]),
     "isq_sensitive_fmt": (_INT, [_INT, _IP]),
@@ -487,6 +495,134 @@ def qmatmul_logprobs(fmt, blocks: torch.Tensor, X: torch.Tensor, N: int, targets
     b, x = _ptr(blocks, "blocks", torch.uint8, dev), _ptr(X, "X", torch.bfloat16, dev)
     if M:
         _call("qmatmul_logprobs", dev, f, b, x, M, N, K, *args, ws, 0 if workspace is None else workspace.numel())
+    return out
+
+
+# ----------------------------------------------------------------------------
+# gradients through frozen quantized weights
+# ----------------------------------------------------------------------------
+
+def _grad_type(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in GRAD_TYPE:
+        raise ValueError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    return GRAD_TYPE[t.dtype]
+
+
+def grad_workspace_bytes(fmt, M: int, N: int, K: int) -> int:
+    """Bytes of a workspace for ``qmatmul_grad`` of up to M rows."""
+    return int(lib().qmatmul_grad_workspace_bytes(_fmt(fmt), M, N, K))
+
+
+def qmatmul_grad(fmt, blocks: torch.Tensor, dY: torch.Tensor, K: int, out: torch.Tensor | None = None,
+                 workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of ``qmatmul``'s result with respect to X: dX = dY . deq(W) as
+    bf16 [M][K], for dY fp32 or bf16 [M][N] and the blocks of the [N][K]
+    weight.  The accuracy is stated at qmatmul_grad in include/qlinear.h."""
+    if dY.dim() != 2:
+        raise ValueError("dY must be 2-D [M][N]")
+    M, N = dY.shape
+    f, t = _fmt(fmt), _grad_type(dY, "dY")
+    _blocks_fit(blocks, "blocks", f, N, K)
+    dev, u8, bf = _device_of(dY, "dY"), torch.uint8, torch.bfloat16
+    out = _out(out, "dX", (M, K), bf, dY)
+    if workspace is None:
+        workspace = dY.new_empty(lib().qmatmul_grad_workspace_bytes(f, M, N, K), dtype=u8)
+    args = (f, _ptr(blocks, "blocks", u8, dev), _ptr(dY, "dY", dY.dtype, dev), t, _ptr(out, "dX", bf, dev), M, N, K,
+            _ptr(workspace, "workspace", u8, dev), workspace.numel())
+    if M:
+        _call("qmatmul_grad", dev, *args)
+    return out
+
+
+class GluGrad(NamedTuple):
+    """Results of ``qmatmul_glu_grad``, bf16: dX [M][K]; dG and dU [M][F]
+    (None where not wanted)."""
+    dX: torch.Tensor
+    dG: torch.Tensor | None
+    dU: torch.Tensor | None
+
+
+def glu_grad_workspace_bytes(fmt, M: int, F: int, K: int) -> int:
+    """Bytes of a workspace for ``qmatmul_glu_grad`` of up to M rows."""
+    return int(lib().qmatmul_glu_grad_workspace_bytes(_fmt(fmt), M, F, K))
+
+
+def qmatmul_glu_grad(fmt, gate_blocks: torch.Tensor, up_blocks: torch.Tensor, X: torch.Tensor, dH: torch.Tensor,
+                     act="silu", parts: bool = False, out: GluGrad | None = None,
+                     workspace: torch.Tensor | None = None) -> GluGrad:
+    """Backward pass of ``qmatmul_glu`` from X bf16 [M][K] and dH fp32 or bf16
+    [M][F]: dX = dG . deq(Wg) + dU . deq(Wu) with dG = dH * U * act'(G) and dU =
+    dH * act(G); G and U are computed again.  ``parts``: dG and dU are wanted
+    too.  ``out``: a GluGrad whose tensors are overwritten (dG and dU that are
+    None are not stored)."""
+    if X.dim() != 2 or dH.dim() != 2:
+        raise ValueError("X must be 2-D [M][K] and dH 2-D [M][F]")
+    M, K = X.shape
+    F = dH.shape[1]
+    _shaped(dH, "dH", (M, F))
+    f, t = _fmt(fmt), _grad_type(dH, "dH")
+    _blocks_fit(gate_blocks, "gate_blocks", f, F, K)
+    _blocks_fit(up_blocks, "up_blocks", f, F, K)
+    dev, u8, bf = _device_of(X, "X"), torch.uint8, torch.bfloat16
+    if out is None:
+        out = GluGrad(X.new_empty((M, K), dtype=bf), X.new_empty((M, F), dtype=bf) if parts else None,
+                      X.new_empty((M, F), dtype=bf) if parts else None)
+    else:
+        for v, name, shape in ((out.dX, "dX", (M, K)), (out.dG, "dG", (M, F)), (out.dU, "dU", (M, F))):
+            _shaped(v, name, shape)
+    a = ACT[act] if isinstance(act, str) else int(act)
+    if workspace is None:
+        workspace = X.new_empty(lib().qmatmul_glu_grad_workspace_bytes(f, M, F, K), dtype=u8)
+    args = (f, _ptr(gate_blocks, "gate_blocks", u8, dev), _ptr(up_blocks, "up_blocks", u8, dev), _ptr(X, "X", bf, dev),
+            _ptr(dH, "dH", dH.dtype, dev), t, _ptr(out.dX, "dX", bf, dev), _ptr(out.dG, "dG", bf, dev),
+            _ptr(out.dU, "dU", bf, dev), M, F, K, a, _ptr(workspace, "workspace", u8, dev), workspace.numel())
+    if M:
+        _call("qmatmul_glu_grad", dev, *args)
+    return out
+
+
+class Xent(NamedTuple):
+    """Results of ``qmatmul_xent``: loss [M] fp32, lse [M] fp32, dX [M][K] bf16
+    (lse and dX None where not wanted)."""
+    loss: torch.Tensor
+    lse: torch.Tensor | None
+    dX: torch.Tensor | None
+
+
+def xent_workspace_bytes(fmt, M: int, N: int, K: int, grad: bool = True) -> int:
+    """Bytes of a workspace for ``qmatmul_xent`` of up to M rows."""
+    return int(lib().qmatmul_xent_workspace_bytes(_fmt(fmt), M, N, K, 1 if grad else 0))
+
+
+def qmatmul_xent(fmt, blocks: torch.Tensor, X: torch.Tensor, N: int, targets: torch.Tensor,
+                 weights: torch.Tensor | None = None, grad: bool = True, out: Xent | None = None,
+                 workspace: torch.Tensor | None = None) -> Xent:
+    """Softmax cross entropy of ``targets`` (int32 [M]; outside [0, N): not
+    scored, loss 0) behind a quantized [N][K] output head, for X bf16 [M][K],
+    and its gradient dX = weights[m] * (softmax - onehot) . deq(W) (``weights``:
+    fp32 [M], by default 1; they enter dX alone), without holding the logits.
+    ``grad=False``: the loss alone.  ``out``: an Xent whose tensors are
+    overwritten (lse and dX that are None are not computed)."""
+    if X.dim() != 2:
+        raise ValueError("X must be 2-D [M][K]")
+    M, K = X.shape
+    f = _fmt(fmt)
+    _blocks_fit(blocks, "blocks", f, N, K)
+    _shaped(targets, "targets", (M,))
+    _shaped(weights, "weights", (M,))
+    dev, u8, bf, f32 = _device_of(X, "X"), torch.uint8, torch.bfloat16, torch.float32
+    if out is None:
+        out = Xent(X.new_empty(M, dtype=f32), X.new_empty(M, dtype=f32), X.new_empty((M, K), dtype=bf) if grad else None)
+    else:
+        for v, name, shape in ((out.loss, "loss", (M,)), (out.lse, "lse", (M,)), (out.dX, "dX", (M, K))):
+            _shaped(v, name, shape)
+    if workspace is None:
+        workspace = X.new_empty(lib().qmatmul_xent_workspace_bytes(f, M, N, K, 0 if out.dX is None else 1), dtype=u8)
+    args = (f, _ptr(blocks, "blocks", u8, dev), _ptr(X, "X", bf, dev), M, N, K, _ptr(targets, "targets", torch.int32, dev),
+            _ptr(weights, "weights", f32, dev), _ptr(out.loss, "loss", f32, dev), _ptr(out.lse, "lse", f32, dev),
+            _ptr(out.dX, "dX", bf, dev), _ptr(workspace, "workspace", u8, dev), workspace.numel())
+    if M:
+        _call("qmatmul_xent", dev, *args)
     return out
 
 

@@ -18,7 +18,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libqlinear.so")
 OBJDIR = os.path.join(HERE, "_build")
 SOURCES = ["api.hip", "isq.hip", "gemv.hip", "gemv_fp8.hip", "gemm.hip", "moe.hip", "logprobs.hip",
-           "probe.hip"]
+           "grad.hip", "product_q8_0.hip", "product_q4k.hip", "product_q6k.hip", "product_kquants.hip",
+           "product_legacy.hip", "probe.hip"]
 ARCH = os.environ.get("QLINEAR_ARCH", "gfx950")
 
 FLAGS = [

@@ -3,6 +3,7 @@
 // argument error never launches anything.
 #include "../../include/qlinear.h"
 #include "gemv_fp8.h"
+#include "grad.h"
 #include "logprobs.h"
 #include "moe.h"
 #include "qlinear_internal.h"
@@ -118,6 +119,26 @@ int64_t head_parts_need(int64_t M, int64_t rows, int64_t N, int top_n)
     const int64_t a = ql::logprobs_need(rows, N, top_n), last = M % rows;
     const int64_t b = last ? ql::logprobs_need(last, N, top_n) : 0;
     return a > b ? a : b;
+}
+
+// shapes of a gradient call on one or two [rows][K] weights
+int grad_shape(int fmt, int64_t M, int64_t rows, int64_t K)
+{
+    const int st = check_tensor(fmt, rows, K, QLINEAR_MAX_N);
+    if (st != Q_OK)
+        return st;
+    if (M < 0 || M > QLINEAR_MAX_M || M * K > kMaxElems || M * rows > kMaxElems)
+        return Q_ESHAPE;
+    return Q_OK;
+}
+
+int workspace_args(const void *workspace, size_t have, size_t need)
+{
+    if (!workspace)
+        return Q_EINVAL;
+    if (!aligned16(workspace))
+        return Q_EALIGN;
+    return have < need ? Q_EINVAL : Q_OK;
 }
 
 // the GEMV of a format: FP8 one- and two-token shapes on their own one-shot
@@ -501,6 +522,105 @@ int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M,
             return st;
     }
     return Q_OK;
+}
+
+size_t qmatmul_grad_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K)
+{
+    if (!implemented(fmt) || M < 1 || grad_shape(fmt, M, N, K) != Q_OK)
+        return 0;
+    return (size_t)ql::grad_workspace(fmt, M, N, K);
+}
+
+int qmatmul_grad(int fmt, const void *blocks, const void *dY, int dy_type, void *dX_bf16, int64_t M, int64_t N,
+                 int64_t K, void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!known(fmt))
+        return Q_EINVAL;
+    if (!implemented(fmt))
+        return Q_ENOTSUP;
+    if (!blocks || !dY || !dX_bf16 || (dy_type != QTYPE_F32 && dy_type != QTYPE_BF16))
+        return Q_EINVAL;
+    if (!aligned16(blocks) || !aligned16(dY) || !aligned16(dX_bf16))
+        return Q_EALIGN;
+    int st = grad_shape(fmt, M, N, K);
+    if (st != Q_OK || M == 0)
+        return st;
+    st = workspace_args(workspace, workspace_bytes, qmatmul_grad_workspace_bytes(fmt, M, N, K));
+    if (st != Q_OK)
+        return st;
+    ql::GradArgs a;
+    a.fmt = fmt, a.W = static_cast<const uint8_t *>(blocks), a.dY = dY, a.dy_bf16 = dy_type == QTYPE_BF16;
+    a.dX = static_cast<uint16_t *>(dX_bf16), a.M = M, a.N = N, a.K = K, a.ws = static_cast<uint8_t *>(workspace);
+    return status_of(ql::launch_grad(a, as_stream(stream)));
+}
+
+size_t qmatmul_glu_grad_workspace_bytes(int fmt, int64_t M, int64_t F, int64_t K)
+{
+    if (!implemented(fmt) || M < 1 || grad_shape(fmt, M, F, K) != Q_OK)
+        return 0;
+    return (size_t)ql::glu_grad_workspace(fmt, M, F, K);
+}
+
+int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, const void *X_bf16, const void *dH,
+                     int dh_type, void *dX_bf16, void *dG_bf16, void *dU_bf16, int64_t M, int64_t F, int64_t K, int act,
+                     void *workspace, size_t workspace_bytes, void *stream)
+{
+    if (!known(fmt))
+        return Q_EINVAL;
+    if (!implemented(fmt))
+        return Q_ENOTSUP;
+    if (!gate_blocks || !up_blocks || !X_bf16 || !dH || !dX_bf16 || (dh_type != QTYPE_F32 && dh_type != QTYPE_BF16) ||
+        act < QACT_SILU || act > QACT_SIGMOID)
+        return Q_EINVAL;
+    if (!aligned16(gate_blocks) || !aligned16(up_blocks) || !aligned16(X_bf16) || !aligned16(dH) || !aligned16(dX_bf16) ||
+        !aligned16(dG_bf16) || !aligned16(dU_bf16))
+        return Q_EALIGN;
+    int st = grad_shape(fmt, M, F, K);
+    if (st != Q_OK || M == 0)
+        return st;
+    st = workspace_args(workspace, workspace_bytes, qmatmul_glu_grad_workspace_bytes(fmt, M, F, K));
+    if (st != Q_OK)
+        return st;
+    ql::GluGradArgs a;
+    a.fmt = fmt, a.act = act;
+    a.gate = static_cast<const uint8_t *>(gate_blocks), a.up = static_cast<const uint8_t *>(up_blocks);
+    a.X = static_cast<const uint16_t *>(X_bf16), a.dH = dH, a.dh_bf16 = dh_type == QTYPE_BF16;
+    a.dX = static_cast<uint16_t *>(dX_bf16), a.dG = static_cast<uint16_t *>(dG_bf16), a.dU = static_cast<uint16_t *>(dU_bf16);
+    a.M = M, a.F = F, a.K = K, a.ws = static_cast<uint8_t *>(workspace);
+    return status_of(ql::launch_glu_grad(a, as_stream(stream)));
+}
+
+size_t qmatmul_xent_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int grad)
+{
+    if (!implemented(fmt) || M < 1 || grad_shape(fmt, M, N, K) != Q_OK)
+        return 0;
+    return (size_t)ql::xent_workspace(fmt, M, N, K, grad != 0);
+}
+
+int qmatmul_xent(int fmt, const void *blocks, const void *X_bf16, int64_t M, int64_t N, int64_t K,
+                 const int32_t *targets, const float *weights, float *loss, float *lse, void *dX_bf16, void *workspace,
+                 size_t workspace_bytes, void *stream)
+{
+    if (!known(fmt))
+        return Q_EINVAL;
+    if (!implemented(fmt))
+        return Q_ENOTSUP;
+    if (!blocks || !X_bf16 || !targets || !loss)
+        return Q_EINVAL;
+    if (!aligned16(blocks) || !aligned16(X_bf16) || !aligned16(dX_bf16) || !aligned4(targets) || !aligned4(weights) ||
+        !aligned4(loss) || !aligned4(lse))
+        return Q_EALIGN;
+    int st = grad_shape(fmt, M, N, K);
+    if (st != Q_OK || M == 0)
+        return st;
+    st = workspace_args(workspace, workspace_bytes, qmatmul_xent_workspace_bytes(fmt, M, N, K, dX_bf16 != nullptr));
+    if (st != Q_OK)
+        return st;
+    ql::XentArgs a;
+    a.fmt = fmt, a.W = static_cast<const uint8_t *>(blocks), a.X = static_cast<const uint16_t *>(X_bf16);
+    a.targets = targets, a.weights = weights, a.loss = loss, a.lse = lse, a.dX = static_cast<uint16_t *>(dX_bf16);
+    a.M = M, a.N = N, a.K = K, a.ws = static_cast<uint8_t *>(workspace);
+    return status_of(ql::launch_xent(a, as_stream(stream)));
 }
 
 int q_dequantize(int fmt, const void *blocks, int64_t N, int64_t K, float *W_fp32, void *stream)

@@ -1,0 +1,11 @@
+// product_q8_0.hip -- instances of product.h for Q8_0.
+#include "product.h"
+
+namespace ql {
+
+hipError_t launch_product_q8_0(int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s)
+{
+    return launch_fmt<FMT_Q8_0>(mode, tile, a, grid, s);
+}
+
+}  // namespace ql

@@ -1,0 +1,258 @@
+// units.h -- 32 consecutive weights of a row (a "unit"), for every implemented
+// format: the raw bytes held in registers between their loads and their
+// decode, so that a kernel can keep a tile's loads in flight while it works on
+// the tile before.
+//
+// Unit b is elements 32 b .. 32 b + 31 of the flattened [N][K] tensor; K is a
+// multiple of 32, so a unit never crosses a row or a block.  decode(t, w)
+// gives its elements 8 t .. 8 t + 7 with the values of dequant8 (decode.h):
+// exact in fp32, the affine formats rounded once.  FP8 gives the codes'
+// values without the row's scale (the kernels apply it elsewhere).
+#pragma once
+
+#include "decode.h"
+
+namespace ql {
+
+// the four bytes of a dword as fp32 (v_cvt_f32_ubyte0 .. 3)
+__device__ __forceinline__ float byte_f32(uint32_t d, int i) { return (float)((d >> (8 * i)) & 255u); }
+
+// 6-bit scale and min j (of 8) of a Q4K / Q5K header, times d and dmin
+__device__ __forceinline__ void header_scales(uint4 h, int j, float &S, float &T)
+{
+    const uint32_t sc = ((h.y >> (4 * j)) & 15u) | ((h.w >> (2 * j)) & 3u) << 4;
+    const uint32_t mq = ((h.z >> (4 * j)) & 15u) | ((h.w >> (16 + 2 * j)) & 3u) << 4;
+    S = f16_bits_to_f32(h.x) * (float)sc;
+    T = -(f16_bits_to_f32(h.x >> 16) * (float)mq);
+}
+
+// Codes in bytes u of two dwords, element 2 i of the task in byte i of `a`...:
+// every unit ends in w = S u + T, one fused multiply-add per weight.
+__device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+__device__ __forceinline__ uint32_t word(const uint2 &v, int i) { return i == 0 ? v.x : v.y; }
+
+template <int FMT> struct Unit;
+
+// S (u - 128) with the signed code's sign bit flipped: S u - 128 S is exact
+// before its one rounding, which S times the code needs none of
+template <> struct Unit<FMT_Q8_0> {
+    uint4 c0, c1;
+    uint32_t d;
+    float S, T;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        c0 = reinterpret_cast<const uint4 *>(B)[2 * b];
+        c1 = reinterpret_cast<const uint4 *>(B)[2 * b + 1];
+        d = reinterpret_cast<const uint16_t *>(B + p.scales)[b];
+    }
+    __device__ __forceinline__ void begin() { S = f16_bits_to_f32(d), T = -128.0f * S; }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const uint32_t x = word(t < 2 ? c0 : c1, 2 * (t & 1)) ^ 0x80808080u;
+        const uint32_t y = word(t < 2 ? c0 : c1, 2 * (t & 1) + 1) ^ 0x80808080u;
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            w[i] = fmaf(S, byte_f32(x, i), T);
+            w[i + 4] = fmaf(S, byte_f32(y, i), T);
+        }
+    }
+};
+
+template <> struct Unit<FMT_Q4K> {
+    uint4 c, h;
+    int j;
+    float S, T;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        c = reinterpret_cast<const uint4 *>(B)[b];
+        h = reinterpret_cast<const uint4 *>(B + p.scales)[b >> 3];
+        j = (int)(b & 7);
+    }
+    __device__ __forceinline__ void begin() { header_scales(h, j, S, T); }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        // even nibbles n0 n2 n4 n6 are elements 0 4 1 5, odd ones 2 6 3 7
+        const uint32_t e = word(c, t) & 0x0f0f0f0fu, o = (word(c, t) >> 4) & 0x0f0f0f0fu;
+        constexpr int at[4] = {0, 4, 1, 5};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            w[at[i]] = fmaf(S, byte_f32(e, i), T);
+            w[at[i] + 2] = fmaf(S, byte_f32(o, i), T);
+        }
+    }
+};
+
+template <> struct Unit<FMT_Q6K> {
+    uint4 lo;
+    uint2 hi;
+    uint32_t sc, d;
+    float S, S1;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        const int64_t g = b >> 3;
+        const int c = (int)(b & 7);
+        lo = *reinterpret_cast<const uint4 *>(B + 192 * g + 16 * c);
+        hi = *reinterpret_cast<const uint2 *>(B + 192 * g + 128 + 8 * c);
+        sc = *reinterpret_cast<const uint16_t *>(B + p.scales + 16 * g + 2 * c);
+        d = reinterpret_cast<const uint16_t *>(B + p.d)[g];
+    }
+    __device__ __forceinline__ void begin()
+    {
+        const float f = f16_bits_to_f32(d);
+        S = f * (float)(int8_t)sc, S1 = f * (float)(int8_t)(sc >> 8);
+    }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const uint32_t e = word(lo, t) & 0x0f0f0f0fu, o = (word(lo, t) >> 4) & 0x0f0f0f0fu;
+        // byte a of `h` holds the high bits of elements 0 2 4 6, byte a + 2 of
+        // 1 3 5 7: laid under the nibbles' order 0 4 1 5 | 2 6 3 7
+        const uint32_t h = word(hi, t >> 1) >> (8 * (t & 1));
+        const uint32_t a = h & 0x00ff00ffu;                      // x0: bits of 0 2 4 6, x2: of 1 3 5 7
+        const uint32_t eh = ((a << 4) & 0x00300030u) | ((a << 8) & 0x30003000u);   // 0 4 1 5
+        const uint32_t oh = ((a << 2) & 0x00300030u) | ((a << 6) & 0x30003000u);   // 2 6 3 7
+        const uint32_t x = e | eh, y = o | oh;
+        const float s = t < 2 ? S : S1, z = -32.0f * s;
+        constexpr int at[4] = {0, 4, 1, 5};
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            w[at[i]] = fmaf(s, byte_f32(x, i), z);
+            w[at[i] + 2] = fmaf(s, byte_f32(y, i), z);
+        }
+    }
+};
+
+// Natural order (all formats below): element k of a task at field k of its
+// word, the top bit (where there is one) at bit k of its byte.
+template <> struct Unit<FMT_Q5K> {
+    uint4 c, h;
+    uint32_t hi;
+    int j;
+    float S, T;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        c = reinterpret_cast<const uint4 *>(B)[b];
+        hi = *reinterpret_cast<const uint32_t *>(B + p.hi + 4 * b);
+        h = reinterpret_cast<const uint4 *>(B + p.scales)[b >> 3];
+        j = (int)(b & 7);
+    }
+    __device__ __forceinline__ void begin() { header_scales(h, j, S, T); }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const uint32_t lo = word(c, t), hb = hi >> (8 * t);
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            w[k] = fmaf(S, (float)(((lo >> (4 * k)) & 15u) | ((hb >> k) & 1u) << 4), T);
+    }
+};
+
+template <> struct Unit<FMT_Q3K> {
+    uint2 c;
+    uint32_t hi, s0, s2, d;
+    int j;
+    float S, S1;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        const int64_t g = b >> 3;
+        j = (int)(b & 7);
+        c = reinterpret_cast<const uint2 *>(B)[b];
+        hi = *reinterpret_cast<const uint32_t *>(B + p.hi + 4 * b);
+        const uint32_t *s3 = reinterpret_cast<const uint32_t *>(B + p.scales + 12 * g);
+        s0 = s3[j >> 2], s2 = s3[2];
+        d = reinterpret_cast<const uint16_t *>(B + p.d)[g];
+    }
+    __device__ __forceinline__ void begin()
+    {
+        // sub-blocks 2 j and 2 j + 1 of 16
+        const int i = (2 * j) & 7;
+        const uint32_t a = ((s0 >> (4 * i)) & 15u) | ((s2 >> (4 * j)) & 3u) << 4;
+        const uint32_t b = ((s0 >> (4 * i + 4)) & 15u) | ((s2 >> (4 * j + 2)) & 3u) << 4;
+        const float f = f16_bits_to_f32(d);
+        S = f * (float)a, S1 = f * (float)b;
+    }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const uint32_t lo = word(c, t >> 1) >> (16 * (t & 1)), hb = hi >> (8 * t);
+        const float s = t < 2 ? S : S1;
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            w[k] = s * (float)((int)(((lo >> (2 * k)) & 3u) | ((hb >> k) & 1u) << 2) - 4);
+    }
+};
+
+template <> struct Unit<FMT_Q2K> {
+    uint2 c;
+    uint32_t sm, dd;
+    float S, T, S1, T1;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        c = reinterpret_cast<const uint2 *>(B)[b];
+        sm = *reinterpret_cast<const uint16_t *>(B + p.scales + 2 * b);
+        dd = reinterpret_cast<const uint32_t *>(B + p.d)[b >> 3];
+    }
+    __device__ __forceinline__ void begin()
+    {
+        const float d = f16_bits_to_f32(dd), m = -f16_bits_to_f32(dd >> 16);
+        S = d * (float)(sm & 15u), T = m * (float)((sm >> 4) & 15u);
+        S1 = d * (float)((sm >> 8) & 15u), T1 = m * (float)(sm >> 12);
+    }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const uint32_t lo = word(c, t >> 1) >> (16 * (t & 1));
+        const float s = t < 2 ? S : S1, z = t < 2 ? T : T1;
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            w[k] = fmaf(s, (float)((lo >> (2 * k)) & 3u), z);
+    }
+};
+
+// E4M3 codes as their values
+template <> struct Unit<FMT_FP8> {
+    uint4 c0, c1;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &, int64_t b)
+    {
+        c0 = reinterpret_cast<const uint4 *>(B)[2 * b];
+        c1 = reinterpret_cast<const uint4 *>(B)[2 * b + 1];
+    }
+    __device__ __forceinline__ void begin() {}
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const int x = (int)word(t < 2 ? c0 : c1, 2 * (t & 1)), y = (int)word(t < 2 ? c0 : c1, 2 * (t & 1) + 1);
+        w[0] = __builtin_amdgcn_cvt_f32_fp8(x, 0), w[1] = __builtin_amdgcn_cvt_f32_fp8(x, 1);
+        w[2] = __builtin_amdgcn_cvt_f32_fp8(x, 2), w[3] = __builtin_amdgcn_cvt_f32_fp8(x, 3);
+        w[4] = __builtin_amdgcn_cvt_f32_fp8(y, 0), w[5] = __builtin_amdgcn_cvt_f32_fp8(y, 1);
+        w[6] = __builtin_amdgcn_cvt_f32_fp8(y, 2), w[7] = __builtin_amdgcn_cvt_f32_fp8(y, 3);
+    }
+};
+
+// the 32-element blocks: Q4_0, Q5_0 (symmetric), Q4_1, Q5_1 (with a minimum)
+template <int FMT> struct Unit {
+    static constexpr bool five = FMT == FMT_Q5_0 || FMT == FMT_Q5_1;
+    static constexpr bool affine = FMT == FMT_Q4_1 || FMT == FMT_Q5_1;
+    static_assert(FMT == FMT_Q4_0 || five || affine, "a 32-element block format");
+    uint4 c;
+    uint32_t hi, d, m;
+    float S, T;
+    __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
+    {
+        c = reinterpret_cast<const uint4 *>(B)[b];
+        d = reinterpret_cast<const uint16_t *>(B + p.d)[b];
+        if constexpr (five)
+            hi = *reinterpret_cast<const uint32_t *>(B + p.hi + 4 * b);
+        if constexpr (affine)
+            m = reinterpret_cast<const uint16_t *>(B + p.m)[b];
+    }
+    __device__ __forceinline__ void begin()
+    {
+        S = f16_bits_to_f32(d);
+        T = affine ? f16_bits_to_f32(m) : -(FMT == FMT_Q4_0 ? 8.0f : 16.0f) * S;
+    }
+    __device__ __forceinline__ void decode(int t, float w[8]) const
+    {
+        const uint32_t lo = word(c, t), hb = five ? hi >> (8 * t) : 0u;
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            w[k] = fmaf(S, (float)(((lo >> (4 * k)) & 15u) | ((hb >> k) & 1u) << 4), T);
+    }
+};
+
+}  // namespace ql

@@ -340,6 +340,77 @@ int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M,
                      const int32_t *targets, int top_n, float *logprob, int32_t *rank, float *entropy, int32_t *top_ids,
                      float *top_logprobs, void *workspace, size_t workspace_bytes, void *stream);
 
+/* Gradients through frozen quantized weights: what a training step on a
+ * quantized model needs from its linear layers when only other parameters (or
+ * the inputs themselves) are trained.
+ *
+ * Input gradient of a linear layer Y = X . deq(W)^T:
+ *   dX[m][k] = sum_n dY[m][n] * deq(W)[n][k].
+ * blocks: device, isq_quantize(fmt, W, N, K).  dY: device [M][N], fp32 or bf16
+ * (dy_type).  dX_bf16: device [M][K] bf16, the type of X, overwritten.
+ * Accuracy: each gradient value enters as fp16 times a power of two of its
+ * row (2^-11 of the value, and 2^-39 of the row's largest), each weight as
+ * fp16 (2^-11 of the weight), sums are fp32, and the result is rounded to bf16:
+ * |dX - exact| <= (2^-9.99 + N * 2^-24) * sum_n |dY||w| + 2^-7.99 |dX|
+ *                 + 2^-38 * max_n |dY| * sum_n |w|.
+ * A weight above 65504 is taken as infinite (FP8: a code times its row's scale
+ * may be any size; dY times that scale takes dY's part above).  A row of dY
+ * that is not finite makes its row of dX not finite, and no other.  Results do
+ * not depend on the order in which workgroups run.
+ * workspace: device, qmatmul_grad_workspace_bytes() bytes, 16-byte aligned,
+ * overwritten (nothing in it needs to start at zero); the size for M rows also
+ * serves fewer.  Calls that can overlap in time need one each.  M == 0 launches
+ * nothing; 0 <= M <= QLINEAR_MAX_M. */
+enum { QTYPE_F32 = 0, QTYPE_BF16 = 1 };
+size_t qmatmul_grad_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K);
+int qmatmul_grad(int fmt, const void *blocks, const void *dY, int dy_type, void *dX_bf16, int64_t M, int64_t N,
+                 int64_t K, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward pass of the gated feed-forward projection (qmatmul_glu)
+ * H = act(G) * U, G = X . deq(Wg)^T, U = X . deq(Wu)^T, from X and dH:
+ *   dG = dH * U * act'(G),  dU = dH * act(G),
+ *   dX = dG . deq(Wg) + dU . deq(Wu).
+ * G and U are computed again (nothing but X is kept from the forward pass).
+ * X_bf16: device [M][K] bf16; dH: device [M][F], fp32 or bf16 (dh_type).
+ * dX_bf16: device [M][K] bf16; dG_bf16, dU_bf16: device [M][F] bf16, each may
+ * be NULL (not wanted); they are what the gate's and the up projection's own
+ * adapters need.  act as in qmatmul_glu; ReLU's derivative at 0 is 0.
+ * G and U are fp32 sums with the weights in fp16 and X as it is (down to 2^-31
+ * of its row's largest), so each is within 2^-11 + K * 2^-23 of its magnitudes
+ * summed; dX adds up dG and dU before their rounding to bf16, as fp16 times one
+ * power of two for both rows (2^-11 of the value, and 2^-39 of the larger of
+ * the two rows' largest).  The rest as in
+ * qmatmul_grad. */
+size_t qmatmul_glu_grad_workspace_bytes(int fmt, int64_t M, int64_t F, int64_t K);
+int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, const void *X_bf16, const void *dH,
+                     int dh_type, void *dX_bf16, void *dG_bf16, void *dU_bf16, int64_t M, int64_t F, int64_t K, int act,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* Softmax cross entropy over a quantized output head, and its gradient with
+ * respect to the head's input, without holding the logits z = X . deq(W)^T:
+ *   loss[m] = lse[m] - z[m][targets[m]],  lse[m] = ln sum_n e^z[m][n],
+ *   dX[m] = weights[m] * sum_n (e^(z[m][n] - lse[m]) - [n = targets[m]]) * deq(W)[n].
+ * blocks, X_bf16, N, K as in qmatmul (the [N][K] head).  targets: device int32
+ * [M]; a target outside [0, N) is not scored: loss 0, dX a row of zeros (lse is
+ * the row's all the same).  weights: device fp32 [M] or NULL (all 1): each
+ * token's share in the step's loss (such as 1 / scored tokens); it enters dX,
+ * not loss, and a row of weight 0 has a dX of zeros.  loss: device fp32 [M].
+ * lse: device fp32 [M] or NULL.  dX_bf16: device [M][K] bf16, or NULL (the loss
+ * alone).  targets, weights, loss and lse 4-byte aligned.
+ * The logits take each weight as a pair of fp16 (2^-22 of the weight) and sums
+ * in fp32; 1 - p of the given token is formed as the others' share, so neither
+ * a loss nor a gradient near 0 is a difference of nearly equal numbers.  The
+ * gradient's product is held as in qmatmul_grad, with p - [n = t] in place of
+ * dY.  Rows go through in chunks of at most 2^26 logits (or 32 rows), which
+ * stay in the workspace.  A row of X that is not finite makes its own loss, lse
+ * and dX not finite.  workspace: qmatmul_xent_workspace_bytes() (grad: whether
+ * dX is wanted), 16-byte aligned; the size for M rows also serves fewer, and
+ * that with grad the loss alone.  M == 0 launches nothing. */
+size_t qmatmul_xent_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int grad);
+int qmatmul_xent(int fmt, const void *blocks, const void *X_bf16, int64_t M, int64_t N, int64_t K,
+                 const int32_t *targets, const float *weights, float *loss, float *lse, void *dX_bf16, void *workspace,
+                 size_t workspace_bytes, void *stream);
+
 /* Quantized embedding lookup (page "Quantization types", section
  * "Sensitive tensor precision": token embeddings are stored quantized, and
  * a tied output head reuses the embedding instead of a second copy -- the
