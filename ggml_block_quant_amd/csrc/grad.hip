@@ -55,8 +55,59 @@ __device__ __forceinline__ int row_exponent(float v)
     return 15 - __builtin_amdgcn_frexp_expf(v);
 }
 
-__device__ __forceinline__ float load_value(const float *p) { return *p; }
-__device__ __forceinline__ float load_value(const uint16_t *p) { return __builtin_bit_cast(float, (uint32_t)*p << 16); }
+// Eight neighbouring values of a row of n from i on, zeros behind its end.
+// VEC: rows of whole groups of eight, 16-byte aligned.
+template <bool VEC> __device__ __forceinline__ void load8(const float *row, int64_t i, int64_t n, float v[8])
+{
+    if constexpr (VEC) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + i), b = *reinterpret_cast<const float4 *>(row + i + 4);
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[j] = i + j < n ? row[i + j] : 0.0f;
+    }
+}
+template <bool VEC> __device__ __forceinline__ void load8(const uint16_t *row, int64_t i, int64_t n, float v[8])
+{
+    if constexpr (VEC) {
+        const uint4 a = *reinterpret_cast<const uint4 *>(row + i);
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
+            v[2 * j + 1] = __builtin_bit_cast(float, w[j] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            v[j] = i + j < n ? __builtin_bit_cast(float, (uint32_t)row[i + j] << 16) : 0.0f;
+    }
+}
+template <bool VEC> __device__ __forceinline__ void store8(uint16_t *row, int64_t i, int64_t n, const float v[8])
+{
+    if constexpr (VEC) {
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            h[j] = bf16_bits(v[2 * j]) | (uint32_t)bf16_bits(v[2 * j + 1]) << 16;
+        *reinterpret_cast<uint4 *>(row + i) = make_uint4(h[0], h[1], h[2], h[3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (i + j < n)
+                row[i + j] = bf16_bits(v[j]);
+    }
+}
+
+// largest magnitude of eight values; infinite where one is not finite
+__device__ __forceinline__ float size8(const float v[8], float big)
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        big = !(fabsf(v[j]) <= 3.4e38f) ? INFINITY : fmaxf(big, fabsf(v[j]));
+    return big;
+}
 
 // chunk c (8 columns) of row m into its place
 template <int PK>
@@ -71,36 +122,73 @@ __device__ __forceinline__ void store_a(uint8_t *A, int64_t Mp, int64_t m, int64
         make_uint4(h[0], h[1], h[2], h[3]);
 }
 
-// Rows of src [M][n] into panels.  One workgroup a row; the row is read twice
-// (its largest value, then the values), the second time from the cache.
-// scale: FP8's scales of the reduction's rows, or null.
-template <typename V, int PK>
-__global__ __launch_bounds__(256) void rows_kernel(const V *__restrict__ src, int64_t n, int64_t Mp, uint8_t *__restrict__ A,
-                                                   int *__restrict__ e_out, const float *__restrict__ scale)
+// The passes over rows below take one workgroup a row of up to HELD groups of
+// eight a thread (16384 values with 512 threads), read once and held in
+// registers between the row's largest value and its stores; longer rows are
+// read twice, the second time from the cache.  One value at a time and twice,
+// 2048 rows of 14336 took 83 us for the gradients and 400 us for the gated
+// pair's.
+constexpr int HELD = 4, HELD_LONG = 0, ROW_THREADS = 512;
+
+// Rows of src [M][n] into panels.  scale: FP8's scales of the reduction's
+// rows, or null.
+template <typename V, int PK, int H, bool VEC>
+__global__ __launch_bounds__(ROW_THREADS) void rows_kernel(const V *__restrict__ src, int64_t n, int64_t Mp,
+                                                           uint8_t *__restrict__ A, int *__restrict__ e_out,
+                                                           const float *__restrict__ scale)
 {
-    __shared__ float red[4];
+    __shared__ float red[ROW_THREADS / 64];
     const int64_t m = blockIdx.x;
     const V *row = src + m * n;
+    const int64_t full = (n + 7) / 8, chunks = (n + PK - 1) / PK * (PK / 8);  // of eight: with values, with the zeros behind
+    auto value = [&](int64_t c, float v[8]) {
+        load8<VEC>(row, 8 * c, n, v);
+        if (scale)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (8 * c + j < n)
+                    v[j] *= scale[8 * c + j];
+    };
+    float held[H > 0 ? H : 1][8];
     float big = 0.0f;
-    bool odd = false;
-    for (int64_t i = threadIdx.x; i < n; i += 256) {
-        const float v = fabsf(scale ? load_value(row + i) * scale[i] : load_value(row + i));
-        odd |= !(v <= 3.4e38f);
-        big = fmaxf(big, v);
+    if constexpr (H > 0) {
+#pragma unroll
+        for (int i = 0; i < H; i++) {
+            const int64_t c = threadIdx.x + i * ROW_THREADS;
+            if (c < full)
+                value(c, held[i]);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    held[i][j] = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < H; i++)
+            big = size8(held[i], big);
+    } else {
+        for (int64_t c = threadIdx.x; c < full; c += ROW_THREADS) {
+            value(c, held[0]);
+            big = size8(held[0], big);
+        }
     }
-    big = block_max(odd ? INFINITY : big, red);
+    big = block_max(big, red);
     const int e = row_exponent(big);
     if (threadIdx.x == 0)
         e_out[m] = e;
-    const int64_t chunks = (n + PK - 1) / PK * (PK / 8);
-    for (int64_t c = threadIdx.x; c < chunks; c += 256) {
-        float v[8];
+    if constexpr (H > 0) {
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int64_t i = 8 * c + j;
-            v[j] = i < n ? (scale ? load_value(row + i) * scale[i] : load_value(row + i)) : 0.0f;
+        for (int i = 0; i < H; i++) {
+            const int64_t c = threadIdx.x + i * ROW_THREADS;
+            if (c < chunks)
+                store_a<PK>(A, Mp, m, c, held[i], e);
         }
-        store_a<PK>(A, Mp, m, c, v, e);
+    } else {
+        for (int64_t c = threadIdx.x; c < chunks; c += ROW_THREADS) {
+            float v[8] = {};
+            if (c < full)
+                value(c, v);
+            store_a<PK>(A, Mp, m, c, v, e);
+        }
     }
 }
 
@@ -154,62 +242,105 @@ __device__ __forceinline__ void glu_grad(int act, float g, float u, float dh, fl
 
 // One workgroup a row: g and u from the splits' sums, the two gradients (bf16
 // where wanted), and both as rows of A under one power of two.
-template <typename V>
-__global__ __launch_bounds__(1024) void glu_rows_kernel(const float *__restrict__ part, int splits, int64_t M, int64_t F,
-                                                        const int *__restrict__ ex, const float *__restrict__ sg,
-                                                        const float *__restrict__ su, const V *__restrict__ dH, int act,
-                                                        int64_t Mp, uint8_t *__restrict__ A, int *__restrict__ e_out,
-                                                        uint16_t *__restrict__ dG, uint16_t *__restrict__ dU)
+struct GluRows {
+    const float *part;   // [splits][M][2][F]
+    int splits, act;
+    int64_t M, F, Mp;
+    const int *ex;       // exponents of X's rows
+    const float *sg, *su;  // FP8's scales of the rows, or null
+    const void *dH;
+    uint8_t *A;
+    int *e_out;
+    uint16_t *dG, *dU;   // or null
+};
+template <typename V, int H, bool VEC>
+__global__ __launch_bounds__(ROW_THREADS) void glu_rows_kernel(GluRows a)
 {
-    __shared__ float red[16];
-    const int64_t m = blockIdx.x;
-    const int x = -ex[m];
-    const int nt = blockDim.x;
-    auto value = [&](int64_t f, float &dg, float &du) {
-        float g = 0.0f, u = 0.0f;
-        for (int s = 0; s < splits; s++) {
-            const float *y = part + ((int64_t)s * M + m) * 2 * F;
-            g += y[f], u += y[F + f];
+    __shared__ float red[ROW_THREADS / 64];
+    const int64_t m = blockIdx.x, F = a.F;
+    const int x = -a.ex[m];
+    const V *dh = static_cast<const V *>(a.dH) + m * F;
+    const int64_t panels = (F + 63) / 64, chunks = panels * 8, full = (F + 7) / 8;
+    // dg and du of eight values; the bf16 results with them
+    auto value = [&](int64_t c, float dg[8], float du[8], bool keep) {
+        float g[8] = {}, u[8] = {}, h[8], t[8];
+        for (int s = 0; s < a.splits; s++) {
+            const float *y = a.part + ((int64_t)s * a.M + m) * 2 * F;
+            load8<VEC>(y, 8 * c, F, t);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                g[j] += t[j];
+            load8<VEC>(y + F, 8 * c, F, t);
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                u[j] += t[j];
         }
-        g = __builtin_ldexpf(g, x), u = __builtin_ldexpf(u, x);
-        if (sg)  // FP8: the rows' scales
-            g *= sg[f], u *= su[f];
-        glu_grad(act, g, u, load_value(dH + m * F + f), dg, du);
-    };
-    float big = 0.0f;
-    bool odd = false;
-    for (int64_t f = threadIdx.x; f < F; f += nt) {
-        float dg, du;
-        value(f, dg, du);
-        if (dG)
-            dG[m * F + f] = bf16_bits(dg);
-        if (dU)
-            dU[m * F + f] = bf16_bits(du);
-        if (sg)
-            dg *= sg[f], du *= su[f];
-        const float v = fmaxf(fabsf(dg), fabsf(du));
-        odd |= !(fabsf(dg) <= 3.4e38f) || !(fabsf(du) <= 3.4e38f);
-        big = fmaxf(big, v);
-    }
-    big = block_max(odd ? INFINITY : big, red);
-    const int e = row_exponent(big);
-    if (threadIdx.x == 0)
-        e_out[m] = e;
-    const int64_t panels = (F + 63) / 64;
-    for (int64_t c = threadIdx.x; c < panels * 8; c += nt) {
-        float a[8], b[8];
+        load8<VEC>(dh, 8 * c, F, h);
 #pragma unroll
         for (int j = 0; j < 8; j++) {
-            const int64_t f = 8 * c + j;
-            a[j] = b[j] = 0.0f;
-            if (f < F) {
-                value(f, a[j], b[j]);
-                if (sg)
-                    a[j] *= sg[f], b[j] *= su[f];
+            float p = __builtin_ldexpf(g[j], x), q = __builtin_ldexpf(u[j], x);
+            const int64_t f = min(8 * c + j, F - 1);
+            if (a.sg)
+                p *= a.sg[f], q *= a.su[f];
+            glu_grad(a.act, p, q, h[j], dg[j], du[j]);
+            if (8 * c + j >= F)  // (the sigmoid's du is dh's share of 1 / 2 at g = 0)
+                dg[j] = du[j] = 0.0f;
+        }
+        if (keep) {
+            if (a.dG)
+                store8<VEC>(a.dG + m * F, 8 * c, F, dg);
+            if (a.dU)
+                store8<VEC>(a.dU + m * F, 8 * c, F, du);
+        }
+        if (a.sg)
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const int64_t f = min(8 * c + j, F - 1);
+                dg[j] *= a.sg[f], du[j] *= a.su[f];
+            }
+    };
+    float hg[H > 0 ? H : 1][8], hu[H > 0 ? H : 1][8];
+    float big = 0.0f;
+    if constexpr (H > 0) {
+#pragma unroll
+        for (int i = 0; i < H; i++) {
+            const int64_t c = threadIdx.x + i * ROW_THREADS;
+            if (c < full)
+                value(c, hg[i], hu[i], true);
+            else
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    hg[i][j] = hu[i][j] = 0.0f;
+            big = size8(hu[i], size8(hg[i], big));
+        }
+    } else {
+        for (int64_t c = threadIdx.x; c < full; c += ROW_THREADS) {
+            value(c, hg[0], hu[0], true);
+            big = size8(hu[0], size8(hg[0], big));
+        }
+    }
+    big = block_max(big, red);
+    const int e = row_exponent(big);
+    if (threadIdx.x == 0)
+        a.e_out[m] = e;
+    uint8_t *const A1 = a.A + panels * a.Mp * 128;
+    if constexpr (H > 0) {
+#pragma unroll
+        for (int i = 0; i < H; i++) {
+            const int64_t c = threadIdx.x + i * ROW_THREADS;
+            if (c < chunks) {
+                store_a<64>(a.A, a.Mp, m, c, hg[i], e);
+                store_a<64>(A1, a.Mp, m, c, hu[i], e);
             }
         }
-        store_a<64>(A, Mp, m, c, a, e);
-        store_a<64>(A + panels * Mp * 128, Mp, m, c, b, e);
+    } else {
+        for (int64_t c = threadIdx.x; c < chunks; c += ROW_THREADS) {
+            float dg[8] = {}, du[8] = {};
+            if (c < full)
+                value(c, dg, du, false);
+            store_a<64>(a.A, a.Mp, m, c, dg, e);
+            store_a<64>(A1, a.Mp, m, c, du, e);
+        }
     }
 }
 
@@ -230,102 +361,141 @@ __device__ __forceinline__ Stat join(Stat a, Stat b)
     return Stat{m, a.l * expf(a.m - m) + b.l * expf(b.m - m), fmaxf(a.s, b.s)};
 }
 
-__device__ __forceinline__ float logit(const float *part, int splits, int64_t stride, int64_t n, int x, const float *sw)
+struct XentRows {
+    const float *part;       // [splits][M][N]
+    int splits, runs;
+    int64_t M, N, run, Mp;   // runs of `run` logits (a multiple of 64), one a workgroup
+    const int *ex;           // exponents of X's rows
+    const float *sw;         // FP8's scales of the rows, or null
+    const int32_t *targets;
+    const float *weights;    // or null
+    Stat *stats;             // [M][runs]
+    uint8_t *A;              // or null
+    int *e_out;
+    float *w_out, *loss, *lse;  // lse: or null
+};
+
+__device__ __forceinline__ float logit(const XentRows &a, int64_t m, int64_t n, int x)
 {
     float z = 0.0f;
-    for (int s = 0; s < splits; s++)
-        z += part[s * stride + n];
+    for (int s = 0; s < a.splits; s++)
+        z += a.part[((int64_t)s * a.M + m) * a.N + n];
     z = __builtin_ldexpf(z, x);
-    return sw ? z * sw[n] : z;
+    return a.sw ? z * a.sw[n] : z;
+}
+// logits 8 c .. 8 c + 7 of row m, -inf behind the row's end
+template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, int64_t m, int64_t c, int x, float z[8])
+{
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        z[j] = 0.0f;
+    for (int s = 0; s < a.splits; s++) {
+        float t[8];
+        load8<VEC>(a.part + ((int64_t)s * a.M + m) * a.N, 8 * c, a.N, t);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            z[j] += t[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        z[j] = __builtin_ldexpf(z[j], x);
+        if (a.sw)
+            z[j] *= a.sw[min(8 * c + j, a.N - 1)];
+        if (!VEC && 8 * c + j >= a.N)
+            z[j] = -INFINITY;
+    }
 }
 
-// part of row m (blockIdx.y), run blockIdx.x of it: its Stat.  The given token
-// is left out: 1 - p of it is the others' share, with all of its digits.
-__global__ __launch_bounds__(256) void stat_kernel(const float *__restrict__ part, int splits, int64_t M, int64_t N, int64_t run,
-                                                   const int *__restrict__ ex, const float *__restrict__ sw,
-                                                   const int32_t *__restrict__ targets, Stat *__restrict__ out)
+// Run blockIdx.x of row blockIdx.y: its Stat, in one pass with the running
+// maximum and sum of each thread.  The given token is left out: 1 - p of it is
+// the others' share, with all of its digits.
+template <bool VEC> __global__ __launch_bounds__(256) void stat_kernel(XentRows a)
 {
     __shared__ float red[4];
-    const int64_t m = blockIdx.y, n0 = blockIdx.x * run, n1 = min(N, n0 + run);
-    const int64_t t = targets[m];
-    const float *row = part + m * N;
-    const int x = -ex[m];
-    float big = -INFINITY;
-    for (int64_t n = n0 + threadIdx.x; n < n1; n += 256)
-        if (n != t)
-            big = fmaxf(big, logit(row, splits, M * N, n, x, sw));
-    big = block_max(big, red);
-    float l = 0.0f;
-    for (int64_t n = n0 + threadIdx.x; n < n1; n += 256)
-        if (n != t)
-            l += expf(logit(row, splits, M * N, n, x, sw) - big);
-    l = block_sum(l, red);
+    const int64_t m = blockIdx.y, t = a.targets[m];
+    const int64_t c0 = blockIdx.x * a.run / 8, c1 = min((a.N + 7) / 8, c0 + a.run / 8);
+    const int x = -a.ex[m];
+    float big = -INFINITY, l = 0.0f;
+    bool odd = false;
+    for (int64_t c = c0 + threadIdx.x; c < c1; c += 256) {
+        float z[8];
+        logits8<VEC>(a, m, c, x, z);
+        float top = big;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            odd |= z[j] != z[j];
+            z[j] = 8 * c + j == t ? -INFINITY : z[j];
+            top = fmaxf(top, z[j]);
+        }
+        if (top == -INFINITY)
+            continue;
+        l *= expf(big - top);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            l += expf(z[j] - top);
+        big = top;
+    }
+    const float top = block_max(big, red);
+    l = block_sum(big == -INFINITY ? 0.0f : l * expf(big - top), red);
+    odd = __syncthreads_or(odd);
     float sc = 0.0f;
-    if (sw) {
-        for (int64_t n = n0 + threadIdx.x; n < n1; n += 256)
-            sc = fmaxf(sc, sw[n]);
+    if (a.sw) {
+        for (int64_t n = 8 * c0 + threadIdx.x; n < min(a.N, 8 * c1); n += 256)
+            sc = fmaxf(sc, a.sw[n]);
         sc = block_max(sc, red);
     }
     if (threadIdx.x == 0)
-        out[m * gridDim.x + blockIdx.x] = Stat{big, l, sc};
+        a.stats[m * a.runs + blockIdx.x] = Stat{top, odd ? NAN : l, sc};
 }
 
 // Row m: loss and lse, and its gradient with respect to the logits as a row of
 // A (a token that is not scored gives zeros).  p_n - [n = t] is at most
 // max(largest p of the others, 1 - p_t) in size, which fixes the power of two;
 // the row's weight enters as a factor of its own afterwards (w_out).
-__global__ __launch_bounds__(256) void xent_rows_kernel(const float *__restrict__ part, int splits, int64_t M, int64_t N,
-                                                        const int *__restrict__ ex, const float *__restrict__ sw,
-                                                        const int32_t *__restrict__ targets, const float *__restrict__ weights,
-                                                        const Stat *__restrict__ stats, int runs, int64_t run, int64_t Mp,
-                                                        uint8_t *__restrict__ A, int *__restrict__ e_out, float *__restrict__ w_out,
-                                                        float *__restrict__ loss, float *__restrict__ lse)
+template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(XentRows a)
 {
     const int64_t m = blockIdx.y;
-    const int64_t t = targets[m];
-    const bool given = t >= 0 && t < N;
-    const float *row = part + m * N;
-    const int x = -ex[m];
-    Stat rest = stats[m * runs];
-    for (int i = 1; i < runs; i++)
-        rest = join(rest, stats[m * runs + i]);
+    const int64_t t = a.targets[m];
+    const bool given = t >= 0 && t < a.N;
+    const int x = -a.ex[m];
+    Stat rest = a.stats[m * a.runs];
+    for (int i = 1; i < a.runs; i++)
+        rest = join(rest, a.stats[m * a.runs + i]);
     // the whole: the others and the given token
-    const float zt = given ? logit(row, splits, M * N, t, x, sw) : -INFINITY;
+    const float zt = given ? logit(a, m, t, x) : -INFINITY;
     const float top = fmaxf(rest.m, zt);
     const float lr = rest.l * expf(rest.m - top), lt = given ? expf(zt - top) : 0.0f;
     const float l = lr + lt;
     const bool first = blockIdx.x == 0 && threadIdx.x == 0;
     if (first) {
         // ln(l / lt) = log1p(lr / lt) where the token is the likelier side
-        loss[m] = !given ? 0.0f : lt > lr ? log1pf(lr / lt) : logf(l) + (top - zt);
-        if (lse)
-            lse[m] = logf(l) + top;
+        a.loss[m] = !given ? 0.0f : lt > lr ? log1pf(lr / lt) : logf(l) + (top - zt);
+        if (a.lse)
+            a.lse[m] = logf(l) + top;
     }
-    if (!A)
+    if (!a.A)
         return;
-    const float big = fmaxf(expf(rest.m - top) / l, lr / l) * (sw ? rest.s : 1.0f);
+    const float big = fmaxf(expf(rest.m - top) / l, lr / l) * (a.sw ? rest.s : 1.0f);
     const float rl = 1.0f / l;
     const float gt = -lr * rl;
-    const float w = given ? (weights ? weights[m] : 1.0f) : 0.0f;
     const int e = row_exponent(big);
     if (first) {
-        e_out[m] = e;
-        w_out[m] = w;
+        a.e_out[m] = e;
+        a.w_out[m] = given ? (a.weights ? a.weights[m] : 1.0f) : 0.0f;
     }
-    const int64_t c1 = min((N + 63) / 64 * 8, ((int64_t)blockIdx.x + 1) * run / 8);
-    for (int64_t c = blockIdx.x * run / 8 + threadIdx.x; c < c1; c += 256) {
-        float v[8];
+    const int64_t full = (a.N + 7) / 8, c1 = min((a.N + 63) / 64 * 8, ((int64_t)blockIdx.x + 1) * a.run / 8);
+    for (int64_t c = blockIdx.x * a.run / 8 + threadIdx.x; c < c1; c += 256) {
+        float v[8] = {};
+        if (given && c < full) {
+            logits8<VEC>(a, m, c, x, v);
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const int64_t n = 8 * c + j;
-            v[j] = 0.0f;
-            if (n < N && given) {
-                v[j] = n == t ? gt : expf(logit(row, splits, M * N, n, x, sw) - top) * rl;
-                if (sw)
-                    v[j] *= sw[n];
+            for (int j = 0; j < 8; j++) {
+                v[j] = 8 * c + j == t ? gt : expf(v[j] - top) * rl;
+                if (a.sw)
+                    v[j] *= a.sw[min(8 * c + j, a.N - 1)];
             }
         }
-        store_a<64>(A, Mp, m, c, v, e);
+        store_a<64>(a.A, a.Mp, m, c, v, e);
     }
 }
 
@@ -342,8 +512,8 @@ int tile_of(int64_t M) { return M <= 32 ? TILE_32 : M <= 64 ? TILE_64 : M <= 128
 int64_t split_to(int tile) { return tile == TILE_32 ? 512 : 256; }
 
 struct Plan {
-    int tile, splits;
-    int64_t Mp, tiles, steps, per;
+    int tile, splits, steps, per;
+    int64_t Mp, tiles;
 };
 Plan plan_of(int64_t M, int64_t col_tiles, int64_t steps)
 {
@@ -351,11 +521,11 @@ Plan plan_of(int64_t M, int64_t col_tiles, int64_t steps)
     p.tile = tile_of(M);
     p.Mp = up_to(M, tile_rows(p.tile));
     p.tiles = p.Mp / tile_rows(p.tile) * col_tiles;
-    p.steps = steps;
+    p.steps = (int)steps;
     int64_t n = split_to(p.tile) / p.tiles;
     n = n < 1 ? 1 : n > steps ? steps : n;
-    p.per = (steps + n - 1) / n;
-    p.splits = (int)((steps + p.per - 1) / p.per);
+    p.per = (int)((steps + n - 1) / n);
+    p.splits = (p.steps + p.per - 1) / p.per;
     return p;
 }
 // The most rows that the splits' sums of a call of up to M rows take (splits
@@ -403,6 +573,17 @@ hipError_t launch_product(int fmt, int mode, const Plan &p, const ProductArgs &a
 const float *row_scales(int fmt, const uint8_t *W, const Planes &p)
 {
     return fmt == FMT_FP8 ? reinterpret_cast<const float *>(W + p.scales) : nullptr;
+}
+
+// rows of src (M of n) into panels of PK
+template <int PK, typename V>
+hipError_t run_rows(const V *src, int64_t M, int64_t n, int64_t Mp, uint8_t *A, int *e, const float *scale, hipStream_t s)
+{
+    const bool held = n <= 8 * HELD * ROW_THREADS, vec = n % 8 == 0;
+    const auto run = [&](auto kernel) { kernel<<<(unsigned)M, ROW_THREADS, 0, s>>>(src, n, Mp, A, e, scale); };
+    held ? vec ? run(rows_kernel<V, PK, HELD, true>) : run(rows_kernel<V, PK, HELD, false>)
+         : vec ? run(rows_kernel<V, PK, HELD_LONG, true>) : run(rows_kernel<V, PK, HELD_LONG, false>);
+    return hipGetLastError();
 }
 
 // a workspace handed out piece by piece, each 256-byte aligned (from a base
@@ -464,11 +645,8 @@ hipError_t launch_grad(const GradArgs &a, hipStream_t s)
     const float *sw = row_scales(a.fmt, a.W, p);
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
-        if (a.dy_bf16)
-            rows_kernel<uint16_t, 64><<<(unsigned)n, 256, 0, s>>>(static_cast<const uint16_t *>(a.dY) + m * a.N, a.N, padded(n), A, e, sw);
-        else
-            rows_kernel<float, 64><<<(unsigned)n, 256, 0, s>>>(static_cast<const float *>(a.dY) + m * a.N, a.N, padded(n), A, e, sw);
-        hipError_t err = hipGetLastError();
+        hipError_t err = a.dy_bf16 ? run_rows<64>(static_cast<const uint16_t *>(a.dY) + m * a.N, n, a.N, padded(n), A, e, sw, s)
+                                   : run_rows<64>(static_cast<const float *>(a.dY) + m * a.N, n, a.N, padded(n), A, e, sw, s);
         if (err == hipSuccess)
             err = run_back(a.fmt, a.W, nullptr, p, A, e, nullptr, n, a.N, a.K, part, a.dX + m * a.K, s);
         if (err != hipSuccess)
@@ -517,8 +695,7 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
         const Plan p = plan_of(n, (a.F + 127) / 128, (a.K + 63) / 64);
-        rows_kernel<uint16_t, 64><<<(unsigned)n, 256, 0, s>>>(a.X + m * a.K, a.K, p.Mp, AX, ex, nullptr);
-        hipError_t err = hipGetLastError();
+        hipError_t err = run_rows<64>(a.X + m * a.K, n, a.K, p.Mp, AX, ex, nullptr, s);
         if (err != hipSuccess)
             return err;
         ProductArgs g{};
@@ -527,16 +704,19 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
         err = launch_product(a.fmt, FORE_GLU, p, g, s);
         if (err != hipSuccess)
             return err;
-        uint16_t *dG = a.dG ? a.dG + m * a.F : nullptr, *dU = a.dU ? a.dU + m * a.F : nullptr;
-        const int nt = n <= 64 ? 1024 : 256;
+        GluRows r{};
+        r.part = gu, r.splits = p.splits, r.act = a.act, r.M = n, r.F = a.F, r.Mp = p.Mp, r.ex = ex, r.sg = sg, r.su = su;
+        r.dH = a.dh_bf16 ? (const void *)(static_cast<const uint16_t *>(a.dH) + m * a.F)
+                         : (const void *)(static_cast<const float *>(a.dH) + m * a.F);
+        r.A = AD, r.e_out = ed, r.dG = a.dG ? a.dG + m * a.F : nullptr, r.dU = a.dU ? a.dU + m * a.F : nullptr;
+        const bool held = a.F <= 8 * HELD * ROW_THREADS, vec = a.F % 8 == 0;
+        const auto run = [&](auto kernel) { kernel<<<(unsigned)n, ROW_THREADS, 0, s>>>(r); };
         if (a.dh_bf16)
-            glu_rows_kernel<uint16_t><<<(unsigned)n, nt, 0, s>>>(gu, p.splits, n, a.F, ex, sg, su,
-                                                                 static_cast<const uint16_t *>(a.dH) + m * a.F, a.act, p.Mp, AD, ed,
-                                                                 dG, dU);
+            held ? vec ? run(glu_rows_kernel<uint16_t, HELD, true>) : run(glu_rows_kernel<uint16_t, HELD, false>)
+                 : vec ? run(glu_rows_kernel<uint16_t, HELD_LONG, true>) : run(glu_rows_kernel<uint16_t, HELD_LONG, false>);
         else
-            glu_rows_kernel<float><<<(unsigned)n, nt, 0, s>>>(gu, p.splits, n, a.F, ex, sg, su,
-                                                              static_cast<const float *>(a.dH) + m * a.F, a.act, p.Mp, AD, ed, dG,
-                                                              dU);
+            held ? vec ? run(glu_rows_kernel<float, HELD, true>) : run(glu_rows_kernel<float, HELD, false>)
+                 : vec ? run(glu_rows_kernel<float, HELD_LONG, true>) : run(glu_rows_kernel<float, HELD_LONG, false>);
         err = hipGetLastError();
         if (err == hipSuccess)
             err = run_back(a.fmt, a.gate, a.up, pl, AD, ed, nullptr, n, a.F, a.K, part, a.dX + m * a.K, s);
@@ -604,8 +784,7 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
         const Plan p = plan_of(n, (a.N + 255) / 256, (a.K + 31) / 32);
-        rows_kernel<uint16_t, 32><<<(unsigned)n, 256, 0, s>>>(a.X + m * a.K, a.K, p.Mp, AX, ex, nullptr);
-        hipError_t err = hipGetLastError();
+        hipError_t err = run_rows<32>(a.X + m * a.K, n, a.K, p.Mp, AX, ex, nullptr, s);
         if (err != hipSuccess)
             return err;
         ProductArgs g{};
@@ -614,15 +793,19 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
         err = launch_product(a.fmt, FORE_PAIR, p, g, s);
         if (err != hipSuccess)
             return err;
-        const int64_t run = xent_run(n, a.N), runs = (a.N + run - 1) / run;
-        const dim3 grid((unsigned)runs, (unsigned)n);
-        stat_kernel<<<grid, 256, 0, s>>>(z, p.splits, n, a.N, run, ex, sw, a.targets + m, stats);
-        err = hipGetLastError();
-        if (err != hipSuccess)
-            return err;
-        xent_rows_kernel<<<a.dX ? grid : dim3(1, (unsigned)n), 256, 0, s>>>(
-            z, p.splits, n, a.N, ex, sw, a.targets + m, a.weights ? a.weights + m : nullptr, stats, (int)runs, run, p.Mp, AD, ed, wd,
-            a.loss + m, a.lse ? a.lse + m : nullptr);
+        XentRows r{};
+        r.run = xent_run(n, a.N), r.runs = (int)((a.N + r.run - 1) / r.run);
+        r.part = z, r.splits = p.splits, r.M = n, r.N = a.N, r.Mp = p.Mp, r.ex = ex, r.sw = sw, r.targets = a.targets + m;
+        r.weights = a.weights ? a.weights + m : nullptr, r.stats = stats, r.A = AD, r.e_out = ed, r.w_out = wd;
+        r.loss = a.loss + m, r.lse = a.lse ? a.lse + m : nullptr;
+        const dim3 grid((unsigned)r.runs, (unsigned)n), rows = a.dX ? grid : dim3(1, (unsigned)n);
+        if (a.N % 8 == 0) {
+            stat_kernel<true><<<grid, 256, 0, s>>>(r);
+            xent_rows_kernel<true><<<rows, 256, 0, s>>>(r);
+        } else {
+            stat_kernel<false><<<grid, 256, 0, s>>>(r);
+            xent_rows_kernel<false><<<rows, 256, 0, s>>>(r);
+        }
         err = hipGetLastError();
         if (err == hipSuccess && a.dX)
             err = run_back(a.fmt, a.W, nullptr, pl, AD, ed, wd, n, a.N, a.K, part, a.dX + m * a.K, s);

@@ -8,6 +8,12 @@
 // gives its elements 8 t .. 8 t + 7 with the values of dequant8 (decode.h):
 // exact in fp32, the affine formats rounded once.  FP8 gives the codes'
 // values without the row's scale (the kernels apply it elsewhere).
+// halves(t, h) gives the same elements as four pairs of fp16, rounded once.
+// The tuned formats' codes reach it two at a time, as the 16-bit patterns of
+// fp16's smallest numbers: a code u in the low bits is u * 2^-24, which a mixed
+// multiply-add (fp32 scale times 2^24, fp16 code, fp32 offset, fp16 result)
+// takes as it is, without a conversion of its own (Q4K: 13 instructions for 8
+// weights, 23 through fp32).
 #pragma once
 
 #include "decode.h"
@@ -30,6 +36,27 @@ __device__ __forceinline__ void header_scales(uint4 h, int j, float &S, float &T
 // every unit ends in w = S u + T, one fused multiply-add per weight.
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t word(const uint2 &v, int i) { return i == 0 ? v.x : v.y; }
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ uint32_t pack_f16(float a, float b)
+{
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b});  // v_cvt_pk_f16_f32, to nearest even
+}
+// fp16(s u + t) of two codes in 16 bits each, s the scale times 2^24
+__device__ __forceinline__ uint32_t scale_codes(uint32_t codes, float s, float t)
+{
+    const f16x2 u = __builtin_bit_cast(f16x2, codes);
+    return __builtin_bit_cast(uint32_t, f16x2{(_Float16)fmaf(s, (float)u.x, t), (_Float16)fmaf(s, (float)u.y, t)});
+}
+template <typename U> __device__ __forceinline__ void halves_of(const U &u, int t, uint32_t h[4])
+{
+    float v[8];
+    u.decode(t, v);
+#pragma unroll
+    for (int j = 0; j < 4; j++)
+        h[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+}
 
 template <int FMT> struct Unit;
 
@@ -56,6 +83,16 @@ template <> struct Unit<FMT_Q8_0> {
             w[i + 4] = fmaf(S, byte_f32(y, i), T);
         }
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    {
+        const uint32_t x = word(t < 2 ? c0 : c1, 2 * (t & 1)) ^ 0x80808080u;
+        const uint32_t y = word(t < 2 ? c0 : c1, 2 * (t & 1) + 1) ^ 0x80808080u;
+        const float s = S * 0x1p24f;
+        h[0] = scale_codes(__builtin_amdgcn_perm(0u, x, 0x0c010c00u), s, T);
+        h[1] = scale_codes(__builtin_amdgcn_perm(0u, x, 0x0c030c02u), s, T);
+        h[2] = scale_codes(__builtin_amdgcn_perm(0u, y, 0x0c010c00u), s, T);
+        h[3] = scale_codes(__builtin_amdgcn_perm(0u, y, 0x0c030c02u), s, T);
+    }
 };
 
 template <> struct Unit<FMT_Q4K> {
@@ -79,6 +116,17 @@ template <> struct Unit<FMT_Q4K> {
             w[at[i]] = fmaf(S, byte_f32(e, i), T);
             w[at[i] + 2] = fmaf(S, byte_f32(o, i), T);
         }
+    }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    {
+        // elements 2 p and 2 p + 1 at nibbles p and p + 4; every second pair
+        // keeps its nibbles four bits up
+        const uint32_t d = word(c, t), d8 = d >> 8;
+        const float s = S * 0x1p24f, s16 = S * 0x1p20f;
+        h[0] = scale_codes(d & 0x000f000fu, s, T);
+        h[1] = scale_codes(d & 0x00f000f0u, s16, T);
+        h[2] = scale_codes(d8 & 0x000f000fu, s, T);
+        h[3] = scale_codes(d8 & 0x00f000f0u, s16, T);
     }
 };
 
@@ -119,6 +167,17 @@ template <> struct Unit<FMT_Q6K> {
             w[at[i] + 2] = fmaf(s, byte_f32(y, i), z);
         }
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    {
+        // elements 2 p and 2 p + 1: nibbles p and p + 4, high bits 2 p of the
+        // octet and of the one 16 bits up
+        const uint32_t d = word(lo, t), a = word(hi, t >> 1) >> (8 * (t & 1));
+        const float f = t < 2 ? S : S1, z = -32.0f * f, s = f * 0x1p24f, s16 = f * 0x1p20f;
+        h[0] = scale_codes((d & 0x000f000fu) | ((a << 4) & 0x00300030u), s, z);
+        h[1] = scale_codes((d & 0x00f000f0u) | ((a << 6) & 0x03000300u), s16, z);
+        h[2] = scale_codes(((d >> 8) & 0x000f000fu) | (a & 0x00300030u), s, z);
+        h[3] = scale_codes(((d >> 8) & 0x00f000f0u) | ((a << 2) & 0x03000300u), s16, z);
+    }
 };
 
 // Natural order (all formats below): element k of a task at field k of its
@@ -143,6 +202,7 @@ template <> struct Unit<FMT_Q5K> {
         for (int k = 0; k < 8; k++)
             w[k] = fmaf(S, (float)(((lo >> (4 * k)) & 15u) | ((hb >> k) & 1u) << 4), T);
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 template <> struct Unit<FMT_Q3K> {
@@ -177,6 +237,7 @@ template <> struct Unit<FMT_Q3K> {
         for (int k = 0; k < 8; k++)
             w[k] = s * (float)((int)(((lo >> (2 * k)) & 3u) | ((hb >> k) & 1u) << 2) - 4);
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 template <> struct Unit<FMT_Q2K> {
@@ -203,6 +264,7 @@ template <> struct Unit<FMT_Q2K> {
         for (int k = 0; k < 8; k++)
             w[k] = fmaf(s, (float)((lo >> (2 * k)) & 3u), z);
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 // E4M3 codes as their values
@@ -222,6 +284,7 @@ template <> struct Unit<FMT_FP8> {
         w[4] = __builtin_amdgcn_cvt_f32_fp8(y, 0), w[5] = __builtin_amdgcn_cvt_f32_fp8(y, 1);
         w[6] = __builtin_amdgcn_cvt_f32_fp8(y, 2), w[7] = __builtin_amdgcn_cvt_f32_fp8(y, 3);
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 // the 32-element blocks: Q4_0, Q5_0 (symmetric), Q4_1, Q5_1 (with a minimum)
@@ -253,6 +316,7 @@ template <int FMT> struct Unit {
         for (int k = 0; k < 8; k++)
             w[k] = fmaf(S, (float)(((lo >> (4 * k)) & 15u) | ((hb >> k) & 1u) << 4), T);
     }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 }  // namespace ql
