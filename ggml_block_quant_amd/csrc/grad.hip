@@ -130,17 +130,17 @@ __device__ __forceinline__ void store_a(uint8_t *A, int64_t Mp, int64_t m, int64
 // pair's.
 constexpr int HELD = 4, HELD_LONG = 0, ROW_THREADS = 512;
 
-// Rows of src [M][n] into panels.  scale: FP8's scales of the reduction's
+// Rows of src [M][n] into panels, with zeros up to column `wide`.  scale: FP8's scales of the reduction's
 // rows, or null.
 template <typename V, int PK, int H, bool VEC>
-__global__ __launch_bounds__(ROW_THREADS) void rows_kernel(const V *__restrict__ src, int64_t n, int64_t Mp,
+__global__ __launch_bounds__(ROW_THREADS) void rows_kernel(const V *__restrict__ src, int64_t n, int64_t wide, int64_t Mp,
                                                            uint8_t *__restrict__ A, int *__restrict__ e_out,
                                                            const float *__restrict__ scale)
 {
     __shared__ float red[ROW_THREADS / 64];
     const int64_t m = blockIdx.x;
     const V *row = src + m * n;
-    const int64_t full = (n + 7) / 8, chunks = (n + PK - 1) / PK * (PK / 8);  // of eight: with values, with the zeros behind
+    const int64_t full = (n + 7) / 8, chunks = wide / 8;  // of eight: with values, with the zeros behind
     auto value = [&](int64_t c, float v[8]) {
         load8<VEC>(row, 8 * c, n, v);
         if (scale)
@@ -192,10 +192,46 @@ __global__ __launch_bounds__(ROW_THREADS) void rows_kernel(const V *__restrict__
     }
 }
 
-// dX = the splits' sums, scaled back (K is a multiple of 32)
+// dX = the splits' sums, scaled back by the row's power of two (e) and factor
+// (w), each or null.  A workgroup takes 64 columns: 16 lanes of four, and 16
+// runs of splits beside each other, whose sums meet in LDS.  (One thread a
+// column over 32 splits took 11 us for one row, of which there are no more.)
 __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ part, const int *__restrict__ e,
                                                    const float *__restrict__ w, int splits, int64_t M, int64_t K,
                                                    uint16_t *__restrict__ out)
+{
+    __shared__ float4 sum[16][16];
+    const int c = threadIdx.x & 15, run = threadIdx.x >> 4;
+    const int64_t m = blockIdx.y, k = 64 * (int64_t)blockIdx.x + 4 * c;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (k < K) {
+        const int per = (splits + 15) / 16, s1 = min(splits, (run + 1) * per);
+#pragma unroll 4
+        for (int s = run * per; s < s1; s++) {
+            const float4 t = *reinterpret_cast<const float4 *>(part + ((int64_t)s * M + m) * K + k);
+            v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+        }
+    }
+    sum[run][c] = v;
+    __syncthreads();
+    if (run || k >= K)
+        return;
+    v = sum[0][c];
+#pragma unroll
+    for (int i = 1; i < 16; i++) {
+        const float4 t = sum[i][c];
+        v.x += t.x, v.y += t.y, v.z += t.z, v.w += t.w;
+    }
+    const int x = e ? -e[m] : 0;
+    const float f = w ? w[m] : 1.0f;
+    const uint32_t lo = bf16_bits(__builtin_ldexpf(v.x, x) * f) | (uint32_t)bf16_bits(__builtin_ldexpf(v.y, x) * f) << 16;
+    const uint32_t hi = bf16_bits(__builtin_ldexpf(v.z, x) * f) | (uint32_t)bf16_bits(__builtin_ldexpf(v.w, x) * f) << 16;
+    *reinterpret_cast<uint2 *>(out + m * K + k) = make_uint2(lo, hi);
+}
+// The same for few splits of many rows: eight columns a thread.
+__global__ __launch_bounds__(256) void join_few_kernel(const float *__restrict__ part, const int *__restrict__ e,
+                                                       const float *__restrict__ w, int splits, int64_t M, int64_t K,
+                                                       uint16_t *__restrict__ out)
 {
     const int64_t m = blockIdx.y, k = 8 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
     if (k >= K)
@@ -207,13 +243,12 @@ __global__ __launch_bounds__(256) void join_kernel(const float *__restrict__ par
         v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
         v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
     }
-    const int x = -e[m];
+    const int x = e ? -e[m] : 0;
     const float f = w ? w[m] : 1.0f;
-    uint32_t h[4];
 #pragma unroll
-    for (int j = 0; j < 4; j++)
-        h[j] = bf16_bits(__builtin_ldexpf(v[2 * j], x) * f) | (uint32_t)bf16_bits(__builtin_ldexpf(v[2 * j + 1], x) * f) << 16;
-    *reinterpret_cast<uint4 *>(out + m * K + k) = make_uint4(h[0], h[1], h[2], h[3]);
+    for (int j = 0; j < 8; j++)
+        v[j] = __builtin_ldexpf(v[j], x) * f;
+    store8<true>(out + m * K, k, K, v);
 }
 
 // ---------------------------------------------------------------------------
@@ -240,65 +275,85 @@ __device__ __forceinline__ void glu_grad(int act, float g, float u, float dh, fl
     }
 }
 
-// One workgroup a row: g and u from the splits' sums, the two gradients (bf16
-// where wanted), and both as rows of A under one power of two.
 struct GluRows {
-    const float *part;   // [splits][M][2][F]
+    const float *g, *u;  // sums of the rows: split s and row m at (s M + m) ld
     int splits, act;
-    int64_t M, F, Mp;
-    const int *ex;       // exponents of X's rows
+    int64_t M, F, Mp, ld;
+    const int *ex;       // exponents of X's rows, or null
     const float *sg, *su;  // FP8's scales of the rows, or null
+    bool raw;            // whether g and u still lack them
     const void *dH;
     uint8_t *A;
     int *e_out;
     uint16_t *dG, *dU;   // or null
 };
+// dg and du of row m's values 8 c .. 8 c + 7, with FP8's scales taken; keep: the
+// bf16 results (without them) with them
+template <typename V, bool VEC>
+__device__ __forceinline__ void glu_values(const GluRows &a, int64_t m, int64_t c, float dg[8], float du[8], bool keep)
+{
+    const int64_t F = a.F;
+    const int x = a.ex ? -a.ex[m] : 0;
+    float g[8] = {}, u[8] = {}, h[8], t[8];
+    for (int s = 0; s < a.splits; s++) {
+        const int64_t at = ((int64_t)s * a.M + m) * a.ld;
+        load8<VEC>(a.g + at, 8 * c, F, t);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            g[j] += t[j];
+        load8<VEC>(a.u + at, 8 * c, F, t);
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            u[j] += t[j];
+    }
+    load8<VEC>(static_cast<const V *>(a.dH) + m * F, 8 * c, F, h);
+#pragma unroll
+    for (int j = 0; j < 8; j++) {
+        float p = __builtin_ldexpf(g[j], x), q = __builtin_ldexpf(u[j], x);
+        const int64_t f = min(8 * c + j, F - 1);
+        if (a.raw && a.sg)
+            p *= a.sg[f], q *= a.su[f];
+        glu_grad(a.act, p, q, h[j], dg[j], du[j]);
+        if (8 * c + j >= F)
+            dg[j] = du[j] = 0.0f;
+    }
+    if (keep) {
+        if (a.dG)
+            store8<VEC>(a.dG + m * F, 8 * c, F, dg);
+        if (a.dU)
+            store8<VEC>(a.dU + m * F, 8 * c, F, du);
+    }
+    if (a.sg)
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const int64_t f = min(8 * c + j, F - 1);
+            dg[j] *= a.sg[f], du[j] *= a.su[f];
+        }
+}
+
+// One row, for one_kernel: both gradients in fp32, one behind the other
+template <typename V, bool VEC> __global__ __launch_bounds__(64) void glu_one_kernel(GluRows a, float *__restrict__ D)
+{
+    const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+    if (8 * c >= a.F)
+        return;
+    float dg[8], du[8];
+    glu_values<V, VEC>(a, 0, c, dg, du, true);
+#pragma unroll
+    for (int j = 0; j < 8; j++)
+        if (8 * c + j < a.F)
+            D[8 * c + j] = dg[j], D[a.F + 8 * c + j] = du[j];
+}
+
+// One workgroup a row: g and u from the splits' sums, the two gradients (bf16
+// where wanted), and both as rows of A under one power of two.
 template <typename V, int H, bool VEC>
 __global__ __launch_bounds__(ROW_THREADS) void glu_rows_kernel(GluRows a)
 {
     __shared__ float red[ROW_THREADS / 64];
     const int64_t m = blockIdx.x, F = a.F;
-    const int x = -a.ex[m];
-    const V *dh = static_cast<const V *>(a.dH) + m * F;
     const int64_t panels = (F + 63) / 64, chunks = panels * 8, full = (F + 7) / 8;
-    // dg and du of eight values; the bf16 results with them
-    auto value = [&](int64_t c, float dg[8], float du[8], bool keep) {
-        float g[8] = {}, u[8] = {}, h[8], t[8];
-        for (int s = 0; s < a.splits; s++) {
-            const float *y = a.part + ((int64_t)s * a.M + m) * 2 * F;
-            load8<VEC>(y, 8 * c, F, t);
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                g[j] += t[j];
-            load8<VEC>(y + F, 8 * c, F, t);
-#pragma unroll
-            for (int j = 0; j < 8; j++)
-                u[j] += t[j];
-        }
-        load8<VEC>(dh, 8 * c, F, h);
-#pragma unroll
-        for (int j = 0; j < 8; j++) {
-            float p = __builtin_ldexpf(g[j], x), q = __builtin_ldexpf(u[j], x);
-            const int64_t f = min(8 * c + j, F - 1);
-            if (a.sg)
-                p *= a.sg[f], q *= a.su[f];
-            glu_grad(a.act, p, q, h[j], dg[j], du[j]);
-            if (8 * c + j >= F)  // (the sigmoid's du is dh's share of 1 / 2 at g = 0)
-                dg[j] = du[j] = 0.0f;
-        }
-        if (keep) {
-            if (a.dG)
-                store8<VEC>(a.dG + m * F, 8 * c, F, dg);
-            if (a.dU)
-                store8<VEC>(a.dU + m * F, 8 * c, F, du);
-        }
-        if (a.sg)
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const int64_t f = min(8 * c + j, F - 1);
-                dg[j] *= a.sg[f], du[j] *= a.su[f];
-            }
-    };
+    auto value = [&](int64_t c, float dg[8], float du[8], bool keep) { glu_values<V, VEC>(a, m, c, dg, du, keep); };
     float hg[H > 0 ? H : 1][8], hu[H > 0 ? H : 1][8];
     float big = 0.0f;
     if constexpr (H > 0) {
@@ -365,12 +420,14 @@ struct XentRows {
     const float *part;       // [splits][M][N]
     int splits, runs;
     int64_t M, N, run, Mp;   // runs of `run` logits (a multiple of 64), one a workgroup
-    const int *ex;           // exponents of X's rows
+    const int *ex;           // exponents of X's rows, or null
     const float *sw;         // FP8's scales of the rows, or null
+    bool raw;                // whether the sums still lack them
     const int32_t *targets;
     const float *weights;    // or null
     Stat *stats;             // [M][runs]
-    uint8_t *A;              // or null
+    uint8_t *A;              // panels for the gradient, or null
+    float *D;                // the gradient of one row in fp32, or null
     int *e_out;
     float *w_out, *loss, *lse;  // lse: or null
 };
@@ -381,7 +438,7 @@ __device__ __forceinline__ float logit(const XentRows &a, int64_t m, int64_t n, 
     for (int s = 0; s < a.splits; s++)
         z += a.part[((int64_t)s * a.M + m) * a.N + n];
     z = __builtin_ldexpf(z, x);
-    return a.sw ? z * a.sw[n] : z;
+    return a.raw && a.sw ? z * a.sw[n] : z;
 }
 // logits 8 c .. 8 c + 7 of row m, -inf behind the row's end
 template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, int64_t m, int64_t c, int x, float z[8])
@@ -399,7 +456,7 @@ template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, i
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         z[j] = __builtin_ldexpf(z[j], x);
-        if (a.sw)
+        if (a.raw && a.sw)
             z[j] *= a.sw[min(8 * c + j, a.N - 1)];
         if (!VEC && 8 * c + j >= a.N)
             z[j] = -INFINITY;
@@ -414,7 +471,7 @@ template <bool VEC> __global__ __launch_bounds__(256) void stat_kernel(XentRows 
     __shared__ float red[4];
     const int64_t m = blockIdx.y, t = a.targets[m];
     const int64_t c0 = blockIdx.x * a.run / 8, c1 = min((a.N + 7) / 8, c0 + a.run / 8);
-    const int x = -a.ex[m];
+    const int x = a.ex ? -a.ex[m] : 0;
     float big = -INFINITY, l = 0.0f;
     bool odd = false;
     for (int64_t c = c0 + threadIdx.x; c < c1; c += 256) {
@@ -457,10 +514,20 @@ template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(Xent
     const int64_t m = blockIdx.y;
     const int64_t t = a.targets[m];
     const bool given = t >= 0 && t < a.N;
-    const int x = -a.ex[m];
-    Stat rest = a.stats[m * a.runs];
-    for (int i = 1; i < a.runs; i++)
+    const int x = a.ex ? -a.ex[m] : 0;
+    // the runs' Stats, as the threads' own first (in an order that does not change)
+    __shared__ float red[4];
+    Stat rest{-INFINITY, 0.0f, 0.0f};
+    for (int i = threadIdx.x; i < a.runs; i += 256)
         rest = join(rest, a.stats[m * a.runs + i]);
+    if (a.runs > 1) {
+        const float big = block_max(rest.m, red);
+        rest.l = block_sum(rest.m == -INFINITY ? rest.l : rest.l * expf(rest.m - big), red);
+        rest.s = block_max(rest.s, red);
+        rest.m = big;
+    } else {
+        rest = a.stats[m];
+    }
     // the whole: the others and the given token
     const float zt = given ? logit(a, m, t, x) : -INFINITY;
     const float top = fmaxf(rest.m, zt);
@@ -473,15 +540,16 @@ template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(Xent
         if (a.lse)
             a.lse[m] = logf(l) + top;
     }
-    if (!a.A)
+    if (!a.A && !a.D)
         return;
     const float big = fmaxf(expf(rest.m - top) / l, lr / l) * (a.sw ? rest.s : 1.0f);
     const float rl = 1.0f / l;
     const float gt = -lr * rl;
     const int e = row_exponent(big);
-    if (first) {
+    const float weight = given ? (a.weights ? a.weights[m] : 1.0f) : 0.0f;
+    if (first && a.A) {
         a.e_out[m] = e;
-        a.w_out[m] = given ? (a.weights ? a.weights[m] : 1.0f) : 0.0f;
+        a.w_out[m] = weight;
     }
     const int64_t full = (a.N + 7) / 8, c1 = min((a.N + 63) / 64 * 8, ((int64_t)blockIdx.x + 1) * a.run / 8);
     for (int64_t c = blockIdx.x * a.run / 8 + threadIdx.x; c < c1; c += 256) {
@@ -495,7 +563,14 @@ template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(Xent
                     v[j] *= a.sw[min(8 * c + j, a.N - 1)];
             }
         }
-        store_a<64>(a.A, a.Mp, m, c, v, e);
+        if (a.A) {
+            store_a<64>(a.A, a.Mp, m, c, v, e);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                if (8 * c + j < a.N)
+                    a.D[8 * c + j] = v[j] * weight;
+        }
     }
 }
 
@@ -507,35 +582,50 @@ int tile_rows(int tile) { return 32 << tile; }
 // rows of one call -> the tile
 int tile_of(int64_t M) { return M <= 32 ? TILE_32 : M <= 64 ? TILE_64 : M <= 128 ? TILE_128 : TILE_256; }
 
-// Workgroups that a launch may split its reduction into; also the bound of
-// what the splits' sums take (splits * tiles <= this where splits > 1).
-int64_t split_to(int tile) { return tile == TILE_32 ? 512 : 256; }
+// A form of the product by its mode and tile: columns of C and of the
+// reduction that a workgroup takes at a time, columns of a panel of A, and how
+// many workgroups its reduction is split for.
+struct Form {
+    int cols, step, panel, split_to;
+};
+Form form_of(int mode, int tile)
+{
+    if (mode == BACK)
+        return Form{256, 64, 64, tile <= TILE_64 ? 512 : 256};
+    if (tile <= TILE_64)
+        return Form{mode == FORE_GLU ? 32 : 64, 128, 64, 512};
+    return mode == FORE_GLU ? Form{128, 64, 64, 256} : Form{256, 32, 32, 256};
+}
 
 struct Plan {
     int tile, splits, steps, per;
     int64_t Mp, tiles;
+    Form f;
 };
-Plan plan_of(int64_t M, int64_t col_tiles, int64_t steps)
+// M rows, `cols` columns of C, a reduction over `parts` times `depth`
+Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
 {
     Plan p;
     p.tile = tile_of(M);
+    p.f = form_of(mode, p.tile);
     p.Mp = up_to(M, tile_rows(p.tile));
-    p.tiles = p.Mp / tile_rows(p.tile) * col_tiles;
-    p.steps = (int)steps;
-    int64_t n = split_to(p.tile) / p.tiles;
-    n = n < 1 ? 1 : n > steps ? steps : n;
-    p.per = (int)((steps + n - 1) / n);
+    p.tiles = p.Mp / tile_rows(p.tile) * ((cols + p.f.cols - 1) / p.f.cols);
+    p.steps = (int)((depth + p.f.step - 1) / p.f.step) * parts;
+    int64_t n = p.f.split_to / p.tiles;
+    n = n < 1 ? 1 : n > p.steps ? p.steps : n;
+    p.per = (int)((p.steps + n - 1) / n);
     p.splits = (p.steps + p.per - 1) / p.per;
     return p;
 }
 // The most rows that the splits' sums of a call of up to M rows take (splits
-// times rows; 0 or the call's own rows where nothing is split).  It grows with
-// M, so that a workspace for M rows serves fewer.
-int64_t split_rows(int64_t M, int64_t col_tiles)
+// times rows; 0 where nothing is split).  It grows with M, so that a workspace
+// for M rows serves fewer.
+int64_t split_rows(int mode, int64_t M, int64_t cols)
 {
     int64_t most = 0;
     for (int t = 0; t <= tile_of(M); t++) {
-        const int64_t n = split_to(t) / col_tiles;
+        const Form f = form_of(mode, t);
+        const int64_t n = f.split_to / ((cols + f.cols - 1) / f.cols);
         if (n > 1 && n * tile_rows(t) > most)
             most = n * tile_rows(t);
     }
@@ -553,11 +643,13 @@ int64_t chunk_rows(int64_t M, int64_t width, int e)
 }
 int64_t padded(int64_t M) { return up_to(M, tile_rows(tile_of(M))); }
 
-int64_t panels_bytes(int64_t Mp, int64_t n, int pk) { return up_to(n, pk) * Mp * 2; }
+// panels of n columns (a multiple of 128: the widest step)
+int64_t panels_bytes(int64_t Mp, int64_t n) { return up_to(n, 128) * Mp * 2; }
 
-hipError_t launch_product(int fmt, int mode, const Plan &p, const ProductArgs &a, hipStream_t s)
+hipError_t launch_product(int fmt, int mode, const Plan &p, ProductArgs a, hipStream_t s)
 {
-    const dim3 grid((unsigned)p.tiles, (unsigned)p.splits);
+    a.Mp = p.Mp, a.steps = p.steps, a.per = p.per, a.tiles = (uint32_t)p.tiles;
+    const unsigned grid = (unsigned)(p.tiles * p.splits);
     switch (fmt) {
     case FMT_Q8_0: return launch_product_q8_0(mode, p.tile, a, grid, s);
     case FMT_Q4K: return launch_product_q4k(mode, p.tile, a, grid, s);
@@ -575,12 +667,13 @@ const float *row_scales(int fmt, const uint8_t *W, const Planes &p)
     return fmt == FMT_FP8 ? reinterpret_cast<const float *>(W + p.scales) : nullptr;
 }
 
-// rows of src (M of n) into panels of PK
+// rows of src (M of n) into panels of PK columns, zeros up to `wide`
 template <int PK, typename V>
-hipError_t run_rows(const V *src, int64_t M, int64_t n, int64_t Mp, uint8_t *A, int *e, const float *scale, hipStream_t s)
+hipError_t run_rows(const V *src, int64_t M, int64_t n, int64_t wide, int64_t Mp, uint8_t *A, int *e, const float *scale,
+                    hipStream_t s)
 {
-    const bool held = n <= 8 * HELD * ROW_THREADS, vec = n % 8 == 0;
-    const auto run = [&](auto kernel) { kernel<<<(unsigned)M, ROW_THREADS, 0, s>>>(src, n, Mp, A, e, scale); };
+    const bool held = wide <= 8 * HELD * ROW_THREADS, vec = n % 8 == 0;
+    const auto run = [&](auto kernel) { kernel<<<(unsigned)M, ROW_THREADS, 0, s>>>(src, n, wide, Mp, A, e, scale); };
     held ? vec ? run(rows_kernel<V, PK, HELD, true>) : run(rows_kernel<V, PK, HELD, false>)
          : vec ? run(rows_kernel<V, PK, HELD_LONG, true>) : run(rows_kernel<V, PK, HELD_LONG, false>);
     return hipGetLastError();
@@ -599,24 +692,77 @@ struct Pieces {
     }
 };
 
+hipError_t run_join(const float *part, const int *e, const float *w, int splits, int64_t M, int64_t K, uint16_t *dX, hipStream_t s)
+{
+    // (48 splits of one row: 4 us against 11; 2 of 2048 rows: 13 against 19)
+    if (splits >= 16)
+        join_kernel<<<dim3((unsigned)((K + 63) / 64), (unsigned)M), 256, 0, s>>>(part, e, w, splits, M, K, dX);
+    else
+        join_few_kernel<<<dim3((unsigned)((K + 2047) / 2048), (unsigned)M), 256, 0, s>>>(part, e, w, splits, M, K, dX);
+    return hipGetLastError();
+}
+
 // dX = the backward product of A's rows over one weight or two, split or not
-int64_t back_steps(int64_t rows, int weights) { return (rows + 63) / 64 * weights; }
 hipError_t run_back(int fmt, const uint8_t *W0, const uint8_t *W1, const Planes &pl, const uint8_t *A, const int *e,
                     const float *w, int64_t M, int64_t rows, int64_t K, float *part, uint16_t *dX, hipStream_t s)
 {
-    const Plan p = plan_of(M, (K + 255) / 256, back_steps(rows, W1 ? 2 : 1));
+    const Plan p = plan_of(BACK, M, K, rows, W1 ? 2 : 1);
     ProductArgs a{};
     a.W0 = W0, a.W1 = W1, a.p = pl, a.A = A, a.e = e, a.w = w;
     a.part = p.splits > 1 ? part : nullptr;
     a.out = p.splits > 1 ? nullptr : dX;
-    a.M = M, a.Mp = p.Mp, a.ld = K, a.rows = rows, a.K = K, a.steps = p.steps, a.per = p.per;
-    hipError_t err = launch_product(fmt, BACK, p, a, s);
+    a.M = M, a.ld = K, a.rows = rows, a.K = K;
+    const hipError_t err = launch_product(fmt, BACK, p, a, s);
     if (err != hipSuccess || p.splits == 1)
         return err;
-    join_kernel<<<dim3((unsigned)((K + 2047) / 2048), (unsigned)M), 256, 0, s>>>(part, e, w, p.splits, M, K, dX);
-    return hipGetLastError();
+    return run_join(part, e, w, p.splits, M, K, dX, s);
 }
-int64_t back_part_bytes(int64_t M, int64_t K) { return split_rows(M, (K + 255) / 256) * K * 4; }
+// the same of one row in fp32 or bf16 (of two weights, one behind the other)
+constexpr int kOneSplitTo = 1024;
+hipError_t run_one(int fmt, const uint8_t *W0, const uint8_t *W1, const Planes &pl, const void *D, bool bf16, const float *scale,
+                   int64_t rows, int64_t K, float *part, uint16_t *dX, hipStream_t s)
+{
+    const int64_t groups = (K + 255) / 256, all = (W1 ? 2 * rows : rows), runs = (all + 31) / 32;
+    int64_t n = kOneSplitTo / groups;
+    // (at least eight runs of 32 rows: a split ends in 32 KiB of LDS summed)
+    n = n > runs / 8 ? runs / 8 : n;
+    n = n < 1 ? 1 : n;
+    OneArgs a{};
+    a.W0 = W0, a.W1 = W1, a.p = pl, a.D = D, a.scale = scale, a.part = part, a.rows = rows, a.K = K;
+    a.per = (int)((runs + n - 1) / n);
+    const int splits = (int)((runs + a.per - 1) / a.per);
+    const unsigned grid = (unsigned)(groups * splits);
+    hipError_t err;
+    switch (fmt) {
+    case FMT_Q8_0: err = launch_one_q8_0(bf16, a, grid, s); break;
+    case FMT_Q4K: err = launch_one_q4k(bf16, a, grid, s); break;
+    case FMT_Q6K: err = launch_one_q6k(bf16, a, grid, s); break;
+    case FMT_Q5K:
+    case FMT_Q3K:
+    case FMT_Q2K:
+    case FMT_FP8: err = launch_one_kquants(fmt, bf16, a, grid, s); break;
+    default: err = launch_one_legacy(fmt, bf16, a, grid, s); break;
+    }
+    return err != hipSuccess ? err : run_join(part, nullptr, nullptr, splits, 1, K, dX, s);
+}
+// the splits' sums of either
+int64_t back_part_bytes(int64_t M, int64_t K)
+{
+    const int64_t one = kOneSplitTo / ((K + 255) / 256), tiles = split_rows(BACK, M, K);
+    return 4 * K * (tiles > one ? tiles : one > 1 ? one : 1);
+}
+// sums of a forward product: rows of `width` values, split or not (and room to
+// start the second half on a 256-byte boundary)
+int64_t fore_part_bytes(int mode, int64_t M, int64_t cols, int64_t width)
+{
+    const int64_t r = split_rows(mode, M, cols);
+    return (r > M ? r : M) * width * 4 + 256;
+}
+
+// Up to two rows the forward products are matrix-vector products: the GEMV
+// takes the weights exactly and sums in fp32 (131072 x 5120 Q6K, one and two
+// rows: 99 and 148 us; tiles of 32 rows 270; three rows 336).
+constexpr int64_t kGemvRows = 2;
 
 }  // namespace
 
@@ -628,7 +774,7 @@ int64_t grad_workspace(int fmt, int64_t M, int64_t N, int64_t K)
 {
     const int64_t R = chunk_rows(M, up_to(N, 64), kGradChunk);
     Pieces w{nullptr};
-    w.take(panels_bytes(padded(R), N, 64));
+    w.take(panels_bytes(padded(R), N));
     w.take(4 * R);
     w.take(back_part_bytes(R, K));
     return w.used;
@@ -639,14 +785,16 @@ hipError_t launch_grad(const GradArgs &a, hipStream_t s)
     const Planes p = planes_of(a.fmt, a.N, a.K);
     const int64_t R = chunk_rows(a.M, up_to(a.N, 64), kGradChunk);
     Pieces w{a.ws};
-    uint8_t *A = w.take(panels_bytes(padded(R), a.N, 64));
+    uint8_t *A = w.take(panels_bytes(padded(R), a.N));
     int *e = reinterpret_cast<int *>(w.take(4 * R));
     float *part = reinterpret_cast<float *>(w.take(back_part_bytes(R, a.K)));
     const float *sw = row_scales(a.fmt, a.W, p);
+    if (a.M == 1)
+        return run_one(a.fmt, a.W, nullptr, p, a.dY, a.dy_bf16, sw, a.N, a.K, part, a.dX, s);
     for (int64_t m = 0; m < a.M; m += R) {
-        const int64_t n = a.M - m < R ? a.M - m : R;
-        hipError_t err = a.dy_bf16 ? run_rows<64>(static_cast<const uint16_t *>(a.dY) + m * a.N, n, a.N, padded(n), A, e, sw, s)
-                                   : run_rows<64>(static_cast<const float *>(a.dY) + m * a.N, n, a.N, padded(n), A, e, sw, s);
+        const int64_t n = a.M - m < R ? a.M - m : R, wide = up_to(a.N, 64);
+        hipError_t err = a.dy_bf16 ? run_rows<64>(static_cast<const uint16_t *>(a.dY) + m * a.N, n, a.N, wide, padded(n), A, e, sw, s)
+                                   : run_rows<64>(static_cast<const float *>(a.dY) + m * a.N, n, a.N, wide, padded(n), A, e, sw, s);
         if (err == hipSuccess)
             err = run_back(a.fmt, a.W, nullptr, p, A, e, nullptr, n, a.N, a.K, part, a.dX + m * a.K, s);
         if (err != hipSuccess)
@@ -659,24 +807,15 @@ hipError_t launch_grad(const GradArgs &a, hipStream_t s)
 
 constexpr int kGluChunk = 26;  // log2 of the values of G (and of U) at once
 
-namespace {
-// sums of a forward product: rows of `width` values, split or not
-int64_t fore_part_bytes(int64_t M, int64_t col_tiles, int64_t width)
-{
-    const int64_t r = split_rows(M, col_tiles);
-    return (r > M ? r : M) * width * 4;
-}
-}  // namespace
-
 int64_t glu_grad_workspace(int fmt, int64_t M, int64_t F, int64_t K)
 {
     const int64_t R = chunk_rows(M, up_to(F, 64), kGluChunk);
     Pieces w{nullptr};
-    w.take(panels_bytes(padded(R), K, 64));
-    w.take(2 * panels_bytes(padded(R), F, 64));
+    w.take(panels_bytes(padded(R), K));
+    w.take(2 * panels_bytes(padded(R), F));
     w.take(4 * R);
     w.take(4 * R);
-    w.take(fore_part_bytes(R, (F + 127) / 128, 2 * F));
+    w.take(fore_part_bytes(FORE_GLU, R, F, 2 * F));
     w.take(back_part_bytes(R, K));
     return w.used;
 }
@@ -686,40 +825,63 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
     const Planes pl = planes_of(a.fmt, a.F, a.K);
     const int64_t R = chunk_rows(a.M, up_to(a.F, 64), kGluChunk);
     Pieces w{a.ws};
-    uint8_t *AX = w.take(panels_bytes(padded(R), a.K, 64));
-    uint8_t *AD = w.take(2 * panels_bytes(padded(R), a.F, 64));
+    uint8_t *AX = w.take(panels_bytes(padded(R), a.K));
+    uint8_t *AD = w.take(2 * panels_bytes(padded(R), a.F));
     int *ex = reinterpret_cast<int *>(w.take(4 * R)), *ed = reinterpret_cast<int *>(w.take(4 * R));
-    float *gu = reinterpret_cast<float *>(w.take(fore_part_bytes(R, (a.F + 127) / 128, 2 * a.F)));
+    float *gu = reinterpret_cast<float *>(w.take(fore_part_bytes(FORE_GLU, R, a.F, 2 * a.F)));
     float *part = reinterpret_cast<float *>(w.take(back_part_bytes(R, a.K)));
-    const float *sg = row_scales(a.fmt, a.gate, pl), *su = row_scales(a.fmt, a.up, pl);
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
-        const Plan p = plan_of(n, (a.F + 127) / 128, (a.K + 63) / 64);
-        hipError_t err = run_rows<64>(a.X + m * a.K, n, a.K, p.Mp, AX, ex, nullptr, s);
-        if (err != hipSuccess)
-            return err;
-        ProductArgs g{};
-        g.W0 = a.gate, g.W1 = a.up, g.p = pl, g.A = AX, g.e = ex, g.part = gu;
-        g.M = n, g.Mp = p.Mp, g.ld = 2 * a.F, g.rows = a.F, g.K = a.K, g.steps = p.steps, g.per = p.per;
-        err = launch_product(a.fmt, FORE_GLU, p, g, s);
-        if (err != hipSuccess)
-            return err;
         GluRows r{};
-        r.part = gu, r.splits = p.splits, r.act = a.act, r.M = n, r.F = a.F, r.Mp = p.Mp, r.ex = ex, r.sg = sg, r.su = su;
+        r.splits = 1, r.act = a.act, r.M = n, r.F = a.F, r.Mp = padded(n);
+        r.sg = row_scales(a.fmt, a.gate, pl), r.su = row_scales(a.fmt, a.up, pl);
         r.dH = a.dh_bf16 ? (const void *)(static_cast<const uint16_t *>(a.dH) + m * a.F)
                          : (const void *)(static_cast<const float *>(a.dH) + m * a.F);
         r.A = AD, r.e_out = ed, r.dG = a.dG ? a.dG + m * a.F : nullptr, r.dU = a.dU ? a.dU + m * a.F : nullptr;
+        hipError_t err = hipErrorNotSupported;
+        if (n <= kGemvRows) {
+            float *u = gu + up_to(n * a.F, 64);
+            r.g = gu, r.u = u, r.ld = a.F;
+            err = launch_gemv(a.fmt, a.gate, a.X + m * a.K, gu, (int)n, a.F, a.K, s);
+            if (err == hipSuccess)
+                err = launch_gemv(a.fmt, a.up, a.X + m * a.K, u, (int)n, a.F, a.K, s);
+        }
+        if (err == hipErrorNotSupported) {
+            const Plan p = plan_of(FORE_GLU, n, a.F, a.K, 1);
+            err = run_rows<64>(a.X + m * a.K, n, a.K, up_to(a.K, p.f.step), p.Mp, AX, ex, nullptr, s);
+            if (err != hipSuccess)
+                return err;
+            ProductArgs g{};
+            g.W0 = a.gate, g.W1 = a.up, g.p = pl, g.A = AX, g.part = gu, g.M = n, g.ld = 2 * a.F, g.rows = a.F, g.K = a.K;
+            err = launch_product(a.fmt, FORE_GLU, p, g, s);
+            r.g = gu, r.u = gu + a.F, r.ld = 2 * a.F, r.splits = p.splits, r.ex = ex, r.raw = true;
+        }
+        if (err != hipSuccess)
+            return err;
         const bool held = a.F <= 8 * HELD * ROW_THREADS, vec = a.F % 8 == 0;
-        const auto run = [&](auto kernel) { kernel<<<(unsigned)n, ROW_THREADS, 0, s>>>(r); };
-        if (a.dh_bf16)
-            held ? vec ? run(glu_rows_kernel<uint16_t, HELD, true>) : run(glu_rows_kernel<uint16_t, HELD, false>)
-                 : vec ? run(glu_rows_kernel<uint16_t, HELD_LONG, true>) : run(glu_rows_kernel<uint16_t, HELD_LONG, false>);
-        else
-            held ? vec ? run(glu_rows_kernel<float, HELD, true>) : run(glu_rows_kernel<float, HELD, false>)
-                 : vec ? run(glu_rows_kernel<float, HELD_LONG, true>) : run(glu_rows_kernel<float, HELD_LONG, false>);
-        err = hipGetLastError();
-        if (err == hipSuccess)
-            err = run_back(a.fmt, a.gate, a.up, pl, AD, ed, nullptr, n, a.F, a.K, part, a.dX + m * a.K, s);
+        if (n == 1) {
+            float *D = reinterpret_cast<float *>(AD);
+            const unsigned grid = (unsigned)((a.F + 511) / 512);
+            const auto run = [&](auto kernel) { kernel<<<grid, 64, 0, s>>>(r, D); };
+            if (a.dh_bf16)
+                vec ? run(glu_one_kernel<uint16_t, true>) : run(glu_one_kernel<uint16_t, false>);
+            else
+                vec ? run(glu_one_kernel<float, true>) : run(glu_one_kernel<float, false>);
+            err = hipGetLastError();
+            if (err == hipSuccess)
+                err = run_one(a.fmt, a.gate, a.up, pl, D, false, nullptr, a.F, a.K, part, a.dX + m * a.K, s);
+        } else {
+            const auto run = [&](auto kernel) { kernel<<<(unsigned)n, ROW_THREADS, 0, s>>>(r); };
+            if (a.dh_bf16)
+                held ? vec ? run(glu_rows_kernel<uint16_t, HELD, true>) : run(glu_rows_kernel<uint16_t, HELD, false>)
+                     : vec ? run(glu_rows_kernel<uint16_t, HELD_LONG, true>) : run(glu_rows_kernel<uint16_t, HELD_LONG, false>);
+            else
+                held ? vec ? run(glu_rows_kernel<float, HELD, true>) : run(glu_rows_kernel<float, HELD, false>)
+                     : vec ? run(glu_rows_kernel<float, HELD_LONG, true>) : run(glu_rows_kernel<float, HELD_LONG, false>);
+            err = hipGetLastError();
+            if (err == hipSuccess)
+                err = run_back(a.fmt, a.gate, a.up, pl, AD, ed, nullptr, n, a.F, a.K, part, a.dX + m * a.K, s);
+        }
         if (err != hipSuccess)
             return err;
     }
@@ -739,21 +901,24 @@ int64_t xent_run(int64_t M, int64_t N)
     runs = runs > most ? most : runs;
     return up_to((N + runs - 1) / runs, 64);
 }
-int64_t xent_most_runs(int64_t N) { return (N + 2047) / 2048; }
+// runs * rows: at most 2048 + rows, and at most a run of 2048 logits each
+int64_t stats_bytes(int64_t R, int64_t N)
+{
+    const int64_t a = 2048 + R, b = R * ((N + 2047) / 2048);
+    return (a < b ? a : b) * (int64_t)sizeof(Stat);
+}
 }  // namespace
 
 int64_t xent_workspace(int fmt, int64_t M, int64_t N, int64_t K, bool grad)
 {
     const int64_t R = chunk_rows(M, up_to(N, 64), kXentChunk);
     Pieces w{nullptr};
-    w.take(panels_bytes(padded(R), K, 32));
+    w.take(panels_bytes(padded(R), K));
     w.take(4 * R);
-    w.take(fore_part_bytes(R, (N + 255) / 256, N));
-    // runs * rows: at most 2048 + rows, and at most a run of 2048 logits each
-    const int64_t a = 2048 + R, b = R * xent_most_runs(N);
-    w.take((a < b ? a : b) * (int64_t)sizeof(Stat));
+    w.take(fore_part_bytes(FORE_PAIR, R, N, N));
+    w.take(stats_bytes(R, N));
     if (grad) {
-        w.take(panels_bytes(padded(R), N, 64));
+        w.take(panels_bytes(padded(R), N));
         w.take(4 * R);
         w.take(4 * R);
         w.take(back_part_bytes(R, K));
@@ -766,38 +931,47 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
     const Planes pl = planes_of(a.fmt, a.N, a.K);
     const int64_t R = chunk_rows(a.M, up_to(a.N, 64), kXentChunk);
     Pieces w{a.ws};
-    uint8_t *AX = w.take(panels_bytes(padded(R), a.K, 32));
+    uint8_t *AX = w.take(panels_bytes(padded(R), a.K));
     int *ex = reinterpret_cast<int *>(w.take(4 * R));
-    float *z = reinterpret_cast<float *>(w.take(fore_part_bytes(R, (a.N + 255) / 256, a.N)));
-    const int64_t sa = 2048 + R, sb = R * xent_most_runs(a.N);
-    Stat *stats = reinterpret_cast<Stat *>(w.take((sa < sb ? sa : sb) * (int64_t)sizeof(Stat)));
+    float *z = reinterpret_cast<float *>(w.take(fore_part_bytes(FORE_PAIR, R, a.N, a.N)));
+    Stat *stats = reinterpret_cast<Stat *>(w.take(stats_bytes(R, a.N)));
     uint8_t *AD = nullptr;
     int *ed = nullptr;
     float *wd = nullptr, *part = nullptr;
     if (a.dX) {
-        AD = w.take(panels_bytes(padded(R), a.N, 64));
+        AD = w.take(panels_bytes(padded(R), a.N));
         ed = reinterpret_cast<int *>(w.take(4 * R));
         wd = reinterpret_cast<float *>(w.take(4 * R));
         part = reinterpret_cast<float *>(w.take(back_part_bytes(R, a.K)));
     }
-    const float *sw = row_scales(a.fmt, a.W, pl);
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
-        const Plan p = plan_of(n, (a.N + 255) / 256, (a.K + 31) / 32);
-        hipError_t err = run_rows<32>(a.X + m * a.K, n, a.K, p.Mp, AX, ex, nullptr, s);
-        if (err != hipSuccess)
-            return err;
-        ProductArgs g{};
-        g.W0 = a.W, g.p = pl, g.A = AX, g.e = ex, g.part = z;
-        g.M = n, g.Mp = p.Mp, g.ld = a.N, g.rows = a.N, g.K = a.K, g.steps = p.steps, g.per = p.per;
-        err = launch_product(a.fmt, FORE_PAIR, p, g, s);
-        if (err != hipSuccess)
-            return err;
+        const uint16_t *X = a.X + m * a.K;
         XentRows r{};
         r.run = xent_run(n, a.N), r.runs = (int)((a.N + r.run - 1) / r.run);
-        r.part = z, r.splits = p.splits, r.M = n, r.N = a.N, r.Mp = p.Mp, r.ex = ex, r.sw = sw, r.targets = a.targets + m;
-        r.weights = a.weights ? a.weights + m : nullptr, r.stats = stats, r.A = AD, r.e_out = ed, r.w_out = wd;
+        r.part = z, r.splits = 1, r.M = n, r.N = a.N, r.Mp = padded(n), r.sw = row_scales(a.fmt, a.W, pl), r.targets = a.targets + m;
+        r.weights = a.weights ? a.weights + m : nullptr, r.stats = stats, r.e_out = ed, r.w_out = wd;
+        if (n == 1)
+            r.D = reinterpret_cast<float *>(AD);
+        else
+            r.A = AD;
         r.loss = a.loss + m, r.lse = a.lse ? a.lse + m : nullptr;
+        hipError_t err = hipErrorNotSupported;
+        if (n <= kGemvRows)
+            err = launch_gemv(a.fmt, a.W, X, z, (int)n, a.N, a.K, s);
+        if (err == hipErrorNotSupported) {
+            const Plan p = plan_of(FORE_PAIR, n, a.N, a.K, 1);
+            err = p.f.panel == 64 ? run_rows<64>(X, n, a.K, up_to(a.K, p.f.step), p.Mp, AX, ex, nullptr, s)
+                                  : run_rows<32>(X, n, a.K, up_to(a.K, p.f.step), p.Mp, AX, ex, nullptr, s);
+            if (err != hipSuccess)
+                return err;
+            ProductArgs g{};
+            g.W0 = a.W, g.p = pl, g.A = AX, g.part = z, g.M = n, g.ld = a.N, g.rows = a.N, g.K = a.K;
+            err = launch_product(a.fmt, FORE_PAIR, p, g, s);
+            r.splits = p.splits, r.ex = ex, r.raw = true;
+        }
+        if (err != hipSuccess)
+            return err;
         const dim3 grid((unsigned)r.runs, (unsigned)n), rows = a.dX ? grid : dim3(1, (unsigned)n);
         if (a.N % 8 == 0) {
             stat_kernel<true><<<grid, 256, 0, s>>>(r);
@@ -808,7 +982,8 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
         }
         err = hipGetLastError();
         if (err == hipSuccess && a.dX)
-            err = run_back(a.fmt, a.W, nullptr, pl, AD, ed, wd, n, a.N, a.K, part, a.dX + m * a.K, s);
+            err = n == 1 ? run_one(a.fmt, a.W, nullptr, pl, r.D, false, nullptr, a.N, a.K, part, a.dX + m * a.K, s)
+                         : run_back(a.fmt, a.W, nullptr, pl, AD, ed, wd, n, a.N, a.K, part, a.dX + m * a.K, s);
         if (err != hipSuccess)
             return err;
     }

@@ -26,6 +26,7 @@ namespace ql {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
@@ -84,7 +85,30 @@ struct ProductArgs {
     int64_t rows;            // rows of one weight (N or F)
     int64_t K;
     int steps, per;          // steps along the reduction, steps per split
+    uint32_t tiles;          // row tiles times column tiles
 };
+
+// Consecutive workgroups go to the 8 XCDs in turn: each XCD gets a run of
+// places, row tiles first, column tiles next, splits last.  The row tiles share
+// their weights in its L2, the column tiles their rows of A and the lines that
+// hold a row's scales: a column tile uses 16 of a line's 128 bytes of Q4K's
+// headers and 2 or 3 values of Q6K's.  (Column tiles in turn over the XCDs made
+// each fetch those lines: one row backward, 14336 x 4096 Q4K, 16.4 -> 14.6 us.)
+__device__ __forceinline__ uint32_t xcd_run(uint32_t i, uint32_t n)
+{
+    const uint32_t xcd = i % 8;
+    return xcd * (n / 8) + min(xcd, n % 8) + i / 8;
+}
+struct Place {
+    uint32_t ct;
+    int split;
+    int64_t m0;
+};
+__device__ __forceinline__ Place place(const ProductArgs &a, int tm)
+{
+    const uint32_t mt = (uint32_t)(a.Mp / tm), t = xcd_run(blockIdx.x, gridDim.x), tile = t % a.tiles;
+    return Place{tile / mt, (int)(t / a.tiles), (int64_t)(tile % mt) * tm};
+}
 
 enum { BACK = 0, FORE_PAIR = 1, FORE_GLU = 2 };
 
@@ -108,6 +132,18 @@ struct Tile {
     static constexpr int BUF = ABYTES + WBYTES;
     static constexpr int UNITS = MODE == BACK ? 64 * 8 : 256 * BK / 32;
     static constexpr int UPT = (UNITS + NT - 1) / NT;
+    // Up to 32 rows of A a step's products are short against the memory's
+    // latency: what is on its way has to be several steps.  A then comes
+    // through registers as W does, and the compiler's own waits let every set
+    // but the one it needs stay on its way (a wait for direct loads to LDS is
+    // one for everything asked for before it).  131072 x 5120 Q6K: 170 -> 149
+    // us; with 37 rows of 4096 x 14336 the direct loads win, 26.5 against 33.
+    static constexpr bool AREG = TM <= 32;
+    static constexpr int DEPTH = AREG ? 4 : 2;
+    // 16-byte pieces of A a thread (where there are fewer than threads, two
+    // threads bring the same one)
+    static constexpr int PIECES = ABYTES / 16, APT = AREG ? (PIECES + NT - 1) / NT : 1;
+    static_assert(!AREG || PIECES % NT == 0 || NT % PIECES == 0, "every piece has a thread");
     static_assert(WN * NI * 32 == TN && UNITS % NT == 0, "256 columns, whole units");
 };
 
@@ -122,15 +158,10 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
     const int wm = wave % WM, wn = wave / WM;
     const int r32 = lane & 31, half = lane >> 5;
 
-    // consecutive workgroups go to the 8 XCDs in turn: each XCD gets a run of
-    // tiles that walks the row tiles of one column tile, whose weights then
-    // stay in its L2
-    const uint32_t mt = (uint32_t)(a.Mp / T::TM), ntiles = gridDim.x;
-    const uint32_t xcd = blockIdx.x % 8, q = ntiles / 8, rem = ntiles % 8;
-    const uint32_t tile = xcd * q + min(xcd, rem) + blockIdx.x / 8;
-    const uint32_t ct = tile / mt;
-    const int64_t m0 = (int64_t)(tile % mt) * T::TM;
-    const int s0 = blockIdx.y * a.per, s1 = min(a.steps, s0 + a.per);
+    const Place at = place(a, T::TM);
+    const uint32_t ct = at.ct;
+    const int64_t m0 = at.m0;
+    const int s0 = at.split * a.per, s1 = min(a.steps, s0 + a.per);
 
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8 *)smem;
 
@@ -149,8 +180,12 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
     // (rows are below 2^24, units of a row below 2^15: 32 x 32 -> 64 bits)
     const uint32_t upr = (uint32_t)(a.K / 32);  // units in a row of W
     const int rows = (int)a.rows, halfsteps = (rows + 63) / 64;
-    // (two sets: a step's bytes are asked for while the step two before it runs)
-    Unit<FMT> un[2][T::UPT];
+    // (a set holds a step's bytes on their way, DEPTH sets DEPTH steps')
+    struct Set {
+        Unit<FMT> u[T::UPT];
+        u32x4 a[T::APT];
+    };
+    Set set[T::DEPTH];
     auto load_w = [&](int s, Unit<FMT>(&u)[T::UPT]) {
 #pragma unroll
         for (int i = 0; i < T::UPT; i++) {
@@ -180,15 +215,11 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
         const int x = tid + i * T::NT;
         uint8_t *const w = smem + buf * T::BUF + T::ABYTES;
         uint32_t h[4];
-        [[maybe_unused]] float v[8];
-        if constexpr (MODE == FORE_PAIR) {
-            u[i].decode(t, v);
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                h[j] = pack_f16(v[2 * j], v[2 * j + 1]);
-        } else {
+        [[maybe_unused]] uint32_t l[4];
+        if constexpr (MODE == FORE_PAIR)
+            u[i].pairs(t, h, l);
+        else
             u[i].halves(t, h);
-        }
         if constexpr (MODE == BACK) {
             *reinterpret_cast<uint4 *>(w + (x >> 3) * T::WPITCH + 16 * w_chunk(x >> 3, x & 7, t)) = make_uint4(h[0], h[1], h[2], h[3]);
         } else {
@@ -196,16 +227,23 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
             const int r = x / UR, c = (x % UR) * 4 + t;
             uint8_t *const at = w + r * T::WPITCH + 16 * a_chunk<BK>(r, c);
             *reinterpret_cast<uint4 *>(at) = make_uint4(h[0], h[1], h[2], h[3]);
-            if constexpr (MODE == FORE_PAIR) {
-                uint32_t l[4];
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const f16x2 p = __builtin_bit_cast(f16x2, h[j]);
-                    l[j] = pack_f16(v[2 * j] - (float)p.x, v[2 * j + 1] - (float)p.y);
-                }
+            if constexpr (MODE == FORE_PAIR)
                 *reinterpret_cast<uint4 *>(at + T::WBYTES / 2) = make_uint4(l[0], l[1], l[2], l[3]);
-            }
         }
+    };
+
+    auto load_set = [&](int s, Set &t) {
+        if constexpr (T::AREG)
+#pragma unroll
+            for (int i = 0; i < T::APT; i++)
+                t.a[i] = *reinterpret_cast<const u32x4 *>(Abase + s * Astep + 16 * ((tid + i * T::NT) % T::PIECES));
+        load_w(s, t.u);
+    };
+    auto store_a_regs = [&](const Set &t, int buf) {
+        if constexpr (T::AREG)
+#pragma unroll
+            for (int i = 0; i < T::APT; i++)
+                *reinterpret_cast<u32x4 *>(smem + buf * T::BUF + 16 * ((tid + i * T::NT) % T::PIECES)) = t.a[i];
     };
 
     f32x16 acc[MI][NI];
@@ -277,15 +315,16 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
     };
     int buf = 0;
     const int last = s1 - 1;
-    // step s with the next one's weights in `u`, which it refills for s + 3
-    auto step = [&](int s, Unit<FMT>(&u)[T::UPT]) {
+    // step s with the next one's bytes in `t`, which it refills for DEPTH later
+    auto step = [&](int s, Set &t) {
         constexpr int tasks = 4 * T::UPT;
+        store_a_regs(t, buf ^ 1);
 #pragma unroll
         for (int x = 0; x + 1 < NP; x++) {
             product(x, buf, true);
 #pragma unroll
-            for (int t = x * tasks / (NP - 1); t < (x + 1) * tasks / (NP - 1); t++)
-                store_w(u, t / 4, t % 4, buf ^ 1);
+            for (int k = x * tasks / (NP - 1); k < (x + 1) * tasks / (NP - 1); k++)
+                store_w(t.u, k / 4, k % 4, buf ^ 1);
             // a product of the matrix cores, then decode beside it
 #pragma unroll
             for (int g = 0; g < MI * NI; g++) {
@@ -293,47 +332,59 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
                 __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
             }
         }
-        wait_loads();
+        if constexpr (!T::AREG)
+            wait_loads();
         lds_barrier();
-        load_w(min(s + 3, last), u);
-        issue_a(min(s + 2, last), buf);
+        load_set(min(s + 1 + T::DEPTH, last), t);
+        if constexpr (!T::AREG)
+            issue_a(min(s + 2, last), buf);
         product(NP - 1, buf ^ 1, true);
         buf ^= 1;
     };
     if (s0 < s1) {
-        load_w(s0, un[1]);
-        issue_a(s0, 0);
-        load_w(min(s0 + 1, last), un[0]);
+        Set head;
+        load_set(s0, head);
+        if constexpr (!T::AREG) {
+            issue_a(s0, 0);
+            issue_a(min(s0 + 1, last), 1);
+        }
 #pragma unroll
-        for (int i = 0; i < T::UPT; i++)
+        for (int i = 0; i < T::DEPTH; i++) {
+            __builtin_amdgcn_sched_barrier(0);  // in this order, which the loop's waits count on
+            load_set(min(s0 + 1 + i, last), set[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        store_a_regs(head, 0);
 #pragma unroll
-            for (int t = 0; t < 4; t++)
-                store_w(un[1], i, t, 0);
-        load_w(min(s0 + 2, last), un[1]);
-        issue_a(min(s0 + 1, last), 1);
-        wait_loads();
+        for (int k = 0; k < 4 * T::UPT; k++)
+            store_w(head.u, k / 4, k % 4, 0);
+        if constexpr (!T::AREG)
+            wait_loads();
         lds_barrier();
         read_ws(0, 0);
 #pragma unroll
         for (int i = 0; i < MI; i++)
             af[i] = read_a(i, 0, 0);
-        // Two steps a turn, each with registers of its own for the weights on
-        // their way, and no branch in it: loads are asked for whatever step
-        // they are for (behind the last, the last again) and waited for a step
-        // later, so no wait stands before their use.  (With the loads under
-        // conditions, or handed from one set of registers to the other, the
-        // compiler waits for them where they are asked for.)
+        // DEPTH steps a turn, each with registers of its own for the bytes on
+        // their way, and no condition on a load: they are asked for whatever
+        // step they are for (behind the last, the last again), so no wait
+        // stands before their use.  (With the loads under conditions, or handed
+        // from one set of registers to the other, the compiler waits for them
+        // where they are asked for.)
         int s = s0;
-        for (; s + 1 < last; s += 2) {
-            step(s, un[0]);
-            step(s + 1, un[1]);
-        }
-        if (s < last)
-            step(s, un[0]);
+        for (; s + T::DEPTH <= last; s += T::DEPTH)
+#pragma unroll
+            for (int i = 0; i < T::DEPTH; i++)
+                step(s + i, set[i]);
+#pragma unroll
+        for (int i = 0; i + 1 < T::DEPTH; i++)
+            if (s + i < last)
+                step(s + i, set[i]);
 #pragma unroll
         for (int x = 0; x < NP; x++)
             product(x, buf, x + 1 < NP);
-        wait_loads();  // none may land in LDS after the workgroup's end
+        if constexpr (!T::AREG)
+            wait_loads();  // none may land in LDS after the workgroup's end
     }
 
     // register r of a lane: row 8 (r / 4) + 4 half + r % 4, column r32 of its tile
@@ -359,7 +410,7 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
                     continue;
                 }
             }
-            float *const y = a.part + ((int64_t)blockIdx.y * a.M + m) * a.ld;
+            float *const y = a.part + ((int64_t)at.split * a.M + m) * a.ld;
 #pragma unroll
             for (int j = 0; j < NI; j++) {
                 if constexpr (MODE == FORE_GLU) {
@@ -386,11 +437,12 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
 // every lane reads another row, 32 or 64 elements at a time: at one row of A
 // that fetched each line of the head several times, 1090 us).  Four waves: two
 // column tiles times the two halves of a step's K, whose sums meet in LDS at
-// the end.  The steps run as in product_kernel.
+// the end.  The bytes on their way stand in registers as in product_kernel.
 template <int MODE, int MI> struct Thin {
     static constexpr int TM = 32 * MI, BK = 128, NT = 256;
     static constexpr int P = MODE == FORE_PAIR ? 2 : 1;
     static constexpr int ABYTES = TM * BK * 2, WPLANE = 64 * BK * 2, BUF = ABYTES + P * WPLANE;
+    static constexpr int DEPTH = 4, APT = ABYTES / 16 / NT;
 };
 
 template <int FMT, int MODE, int MI>
@@ -403,32 +455,39 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = wave & 1, kh = wave >> 1;
     const int r32 = lane & 31, half = lane >> 5;
-    const uint32_t mt = (uint32_t)(a.Mp / T::TM), ntiles = gridDim.x;
-    const uint32_t xcd = blockIdx.x % 8, q = ntiles / 8, rem = ntiles % 8;
-    const uint32_t tile = xcd * q + min(xcd, rem) + blockIdx.x / 8;
-    const uint32_t ct = tile / mt;
-    const int64_t m0 = (int64_t)(tile % mt) * T::TM;
-    const int s0 = blockIdx.y * a.per, s1 = min(a.steps, s0 + a.per);
-    const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8 *)smem;
+    const Place at = place(a, T::TM);
+    const uint32_t ct = at.ct;
+    const int64_t m0 = at.m0;
+    const int s0 = at.split * a.per, s1 = min(a.steps, s0 + a.per);
 
-    // A: two panels of 64 columns a step
-    auto issue_a = [&](int s, int buf) {
-#pragma unroll
-        for (int i = 0; i < T::ABYTES / 1024; i += 4) {
-            const int at = (i + wave) * 1024;  // of the step's bytes
-            const int panel = at / (T::TM * 128);
-            load_to_lds(a.A + (((int64_t)2 * s + panel) * a.Mp + m0) * 128, (uint32_t)(at % (T::TM * 128) + 16 * lane),
-                        lds0 + buf * T::BUF + at);
-        }
-    };
     // W: unit tid % 4 of the step, row tid / 4 of the tile
     const uint32_t upr = (uint32_t)(a.K / 32);
     const int rows = (int)a.rows, wr = tid >> 2, wc = tid & 3;
     const int first = MODE == FORE_GLU ? (int)ct * 32 + (wr & 31) : (int)ct * 64 + wr;
     const uint64_t row0 = (uint64_t)(uint32_t)min(first, rows - 1) * upr;
     const uint8_t *const W = MODE == FORE_GLU && wr >= 32 ? a.W1 : a.W0;
-    Unit<FMT> un[2];
-    auto load_w = [&](int s, Unit<FMT> &u) { u.load(W, a.p, (int64_t)(row0 + min((uint32_t)(s * 4 + wc), upr - 1))); };
+    // a step's bytes on their way: the unit, and this thread's pieces of A's two
+    // panels of 64 columns
+    struct Set {
+        Unit<FMT> u;
+        u32x4 a[T::APT];
+    };
+    Set set[T::DEPTH];
+    const int64_t panel = a.Mp * 128;
+    const uint8_t *const Abase = a.A + m0 * 128;
+    auto load_set = [&](int s, Set &t) {
+#pragma unroll
+        for (int i = 0; i < T::APT; i++) {
+            const int at = 16 * (tid + i * T::NT);
+            t.a[i] = *reinterpret_cast<const u32x4 *>(Abase + (2 * s + at / (T::TM * 128)) * panel + at % (T::TM * 128));
+        }
+        t.u.load(W, a.p, (int64_t)(row0 + min((uint32_t)(s * 4 + wc), upr - 1)));
+    };
+    auto store_a_regs = [&](const Set &t, int buf) {
+#pragma unroll
+        for (int i = 0; i < T::APT; i++)
+            *reinterpret_cast<u32x4 *>(smem + buf * T::BUF + 16 * (tid + i * T::NT)) = t.a[i];
+    };
     // chunk c of row r of a tile of W: 16 rows' same chunk on all banks, and a
     // row's units' same task on banks of their own
     auto w_at = [&](int r, int c) { return r * 256 + 16 * ((4 * (c >> 2) + ((c & 3) ^ (c >> 2))) ^ (r & 15)); };
@@ -438,15 +497,8 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
         uint8_t *const at = smem + buf * T::BUF + T::ABYTES + w_at(wr, 4 * wc + t);
         uint32_t h[4];
         if constexpr (MODE == FORE_PAIR) {
-            float v[8];
             uint32_t l[4];
-            u.decode(t, v);
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                h[j] = pack_f16(v[2 * j], v[2 * j + 1]);
-                const f16x2 p = __builtin_bit_cast(f16x2, h[j]);
-                l[j] = pack_f16(v[2 * j] - (float)p.x, v[2 * j + 1] - (float)p.y);
-            }
+            u.pairs(t, h, l);
             *reinterpret_cast<uint4 *>(at + T::WPLANE) = make_uint4(l[0], l[1], l[2], l[3]);
         } else {
             u.halves(t, h);
@@ -460,56 +512,72 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
 #pragma unroll
         for (int r = 0; r < 16; r++)
             acc[i][r] = 0.0f;
-    // product x of buffer `from`: columns 16 (x / P) of the wave's half
-    auto product = [&](int x, int from) {
-        const int kk = x / P % 4;
+    // all fragments of a step (columns 16 kk of the wave's half), read before
+    // anything else of it: the decode of the next step hides their way
+    f16x8 af[4][MI], wf[NP];
+    auto read_all = [&](int from) {
         const uint8_t *const b = smem + from * T::BUF;
-        const f16x8 w = *reinterpret_cast<const f16x8 *>(b + T::ABYTES + (x % P) * T::WPLANE +
-                                                         w_at(col * 32 + r32, 8 * kh + 2 * kk + half));
 #pragma unroll
-        for (int i = 0; i < MI; i++) {
-            const int row = 32 * i + r32;
-            const f16x8 x8 = *reinterpret_cast<const f16x8 *>(b + kh * (T::TM * 128) + row * 128 + 16 * a_chunk<64>(row, 2 * kk + half));
-            acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(x8, w, acc[i], 0, 0, 0);
+        for (int x = 0; x < NP; x++) {
+            const int kk = x / P;
+            wf[x] = *reinterpret_cast<const f16x8 *>(b + T::ABYTES + (x % P) * T::WPLANE +
+                                                     w_at(col * 32 + r32, 8 * kh + 2 * kk + half));
+            if (x % P == 0)
+#pragma unroll
+                for (int i = 0; i < MI; i++) {
+                    const int row = 32 * i + r32;
+                    af[kk][i] = *reinterpret_cast<const f16x8 *>(b + kh * (T::TM * 128) + row * 128 +
+                                                                 16 * a_chunk<64>(row, 2 * kk + half));
+                }
         }
+        if constexpr (P == 1 && MI == 1)  // (one token of 2 x 14336 x 4096 Q4K 37.8 -> 29.3 us; with more to read it costs)
+            __builtin_amdgcn_sched_barrier(0);
+    };
+    auto products = [&]() {
+#pragma unroll
+        for (int x = 0; x < NP; x++)
+#pragma unroll
+            for (int i = 0; i < MI; i++)
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[x / P][i], wf[x], acc[i], 0, 0, 0);
     };
     int buf = 0;
     const int last = s1 - 1;
-    auto step = [&](int s, Unit<FMT> &u) {
+    auto step = [&](int s, Set &t) {
+        read_all(buf);
+        store_a_regs(t, buf ^ 1);
 #pragma unroll
-        for (int x = 0; x < NP; x++) {
-            product(x, buf);
-            if (x < 4)
-                store_w(u, x, buf ^ 1);
-        }
-        wait_loads();
+        for (int x = 0; x < 4; x++)
+            store_w(t.u, x, buf ^ 1);
+        load_set(min(s + 1 + T::DEPTH, last), t);
+        products();
         lds_barrier();
-        load_w(min(s + 3, last), u);
-        issue_a(min(s + 2, last), buf);
         buf ^= 1;
     };
     if (s0 < s1) {
-        load_w(s0, un[1]);
-        issue_a(s0, 0);
-        load_w(min(s0 + 1, last), un[0]);
+        Set head;
+        load_set(s0, head);
+#pragma unroll
+        for (int i = 0; i < T::DEPTH; i++) {
+            __builtin_amdgcn_sched_barrier(0);  // in this order, which the loop's waits count on
+            load_set(min(s0 + 1 + i, last), set[i]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        store_a_regs(head, 0);
 #pragma unroll
         for (int t = 0; t < 4; t++)
-            store_w(un[1], t, 0);
-        load_w(min(s0 + 2, last), un[1]);
-        issue_a(min(s0 + 1, last), 1);
-        wait_loads();
+            store_w(head.u, t, 0);
         lds_barrier();
         int s = s0;
-        for (; s + 1 < last; s += 2) {
-            step(s, un[0]);
-            step(s + 1, un[1]);
-        }
-        if (s < last)
-            step(s, un[0]);
+        for (; s + T::DEPTH <= last; s += T::DEPTH)
 #pragma unroll
-        for (int x = 0; x < NP; x++)
-            product(x, buf);
-        wait_loads();  // none may land in LDS after this
+            for (int i = 0; i < T::DEPTH; i++)
+                step(s + i, set[i]);
+#pragma unroll
+        for (int i = 0; i + 1 < T::DEPTH; i++)
+            if (s + i < last)
+                step(s + i, set[i]);
+        read_all(buf);
+        products();
     }
     // the halves of K meet: 64 lanes' values of a register stand together
     __syncthreads();
@@ -533,33 +601,141 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
         for (int r = 0; r < 16; r++) {
             const int64_t m = m0 + 32 * i + 8 * (r / 4) + 4 * half + r % 4;
             if (m < a.M)
-                a.part[((int64_t)blockIdx.y * a.M + m) * a.ld + (MODE == FORE_GLU ? col * a.rows : 0) + c] =
+                a.part[((int64_t)at.split * a.M + m) * a.ld + (MODE == FORE_GLU ? col * a.rows : 0) + c] =
                     acc[i][r] + sum[(i * 16 + r) * 64];
         }
+}
+
+// ---------------------------------------------------------------------------
+// The backward product of one row
+// ---------------------------------------------------------------------------
+
+struct OneArgs {
+    const uint8_t *W0, *W1;  // W1: the second weight, or null
+    Planes p;
+    const void *D;           // [rows] (of two weights: the second's behind the first's), fp32 or bf16
+    const float *scale;      // FP8: the rows' scales still to be taken, or null
+    float *part;             // [splits][K]
+    int64_t rows, K;
+    int per;                 // rows of 32 a split
+};
+
+// One row needs no matrix cores: a thread decodes units of its own 32 columns,
+// row after row, and multiplies them by the rows' gradients in fp32 (nothing is
+// rounded but the weights' own fp32 values and the sums); 8 lanes read a group
+// of 256 weights, a wave 8 rows, nothing meets before the end.  Against the
+// tiles of 32 rows, which also need the gradients as fp16 panels first (3.5
+// us): 14336 x 4096 Q4K 13.4 against 14.6 us, Q8_0 17.1 against 18.1, 131072 x
+// 5120 Q6K 136 against 141; two rows in this way 20 us, so they take the tiles.
+// Bound by the decode's instructions and the loads' latency together (2.5 to
+// 4 TB/s of weights).
+template <int FMT, typename V>
+__global__ __launch_bounds__(256) void one_kernel(OneArgs a)
+{
+    constexpr int DEPTH = 4;
+    __shared__ float sum[32][256 + 4];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int slot = wave * 8 + (lane >> 3), c = lane & 7;
+    const uint32_t upr = (uint32_t)(a.K / 32);
+    const uint32_t groups = (uint32_t)((a.K + 255) / 256), at = xcd_run(blockIdx.x, gridDim.x);
+    const int col = (int)(at % groups), split = (int)(at / groups);
+    const uint32_t unit = min((uint32_t)(col * 8 + c), upr - 1);  // behind the row's end: not stored
+    const int rows = (int)a.rows, all = a.W1 ? 2 * rows : rows;
+    const int n0 = split * a.per * 32 + slot;
+    const int n1 = min(all, (split + 1) * a.per * 32);
+    const V *const D = static_cast<const V *>(a.D);
+    struct Set {
+        Unit<FMT> u;
+        float d;
+    };
+    Set set[DEPTH];
+    auto load = [&](int n, Set &t) {
+        const int r = min(n, all - 1);
+        const bool second = r >= rows;
+        t.u.load(second ? a.W1 : a.W0, a.p, (int64_t)((uint64_t)(uint32_t)(second ? r - rows : r) * upr + unit));
+        if constexpr (sizeof(V) == 2)
+            t.d = __builtin_bit_cast(float, (uint32_t)D[r] << 16);
+        else
+            t.d = D[r];
+        if (FMT == FMT_FP8 && a.scale)
+            t.d *= a.scale[r];
+        t.d = n < n1 ? t.d : 0.0f;
+    };
+    float acc[32];
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        acc[i] = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DEPTH; i++)
+        load(n0 + 32 * i, set[i]);
+    for (int n = n0; n < n1; n += 32 * DEPTH) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; i++) {
+            Set &t = set[i];
+            t.u.begin();
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                float w[8];
+                t.u.values(k, w);
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    acc[8 * k + j] = fmaf(t.d, w[j], acc[8 * k + j]);
+            }
+            load(n + 32 * (DEPTH + i), t);
+        }
+    }
+    // the 32 rows' sums of a column meet in LDS, in this order
+#pragma unroll
+    for (int i = 0; i < 32; i += 4)
+        *reinterpret_cast<float4 *>(&sum[slot][32 * c + i]) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    __syncthreads();
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 32; i++)
+        v += sum[i][tid];
+    const int64_t k = (int64_t)col * 256 + tid;
+    if (k < a.K)
+        a.part[(int64_t)split * a.K + k] = v;
 }
 
 // The shapes of a product's workgroups, by the rows of A they take.
 enum { TILE_32 = 0, TILE_64 = 1, TILE_128 = 2, TILE_256 = 3 };
 
 template <int FMT, int MODE>
-hipError_t launch_mode(int tile, const ProductArgs &a, dim3 grid, hipStream_t s)
+hipError_t launch_mode(int tile, const ProductArgs &a, unsigned grid, hipStream_t s)
 {
-    switch (tile) {
-    case TILE_32: product_kernel<FMT, MODE, 1, 4, 1, 2><<<grid, 256, 0, s>>>(a); break;
-    case TILE_64: product_kernel<FMT, MODE, 1, 4, 2, 2><<<grid, 256, 0, s>>>(a); break;
-    case TILE_128: product_kernel<FMT, MODE, 2, 2, 2, 4><<<grid, 256, 0, s>>>(a); break;
-    default:
-        // (a pair's step is 256 units: four waves)
-        if constexpr (MODE == FORE_PAIR)
-            product_kernel<FMT, MODE, 2, 2, 4, 4><<<grid, 256, 0, s>>>(a);
-        else
-            product_kernel<FMT, MODE, 2, 4, 4, 2><<<grid, 512, 0, s>>>(a);
-        break;
+    if constexpr (MODE == BACK) {
+        // (one token of 14336 x 4096 Q4K: eight waves 16.4 us, four 18.0)
+        if (tile == TILE_32)
+            product_kernel<FMT, MODE, 1, 8, 1, 1><<<grid, 512, 0, s>>>(a);
+        else if (tile == TILE_64)
+            product_kernel<FMT, MODE, 1, 4, 2, 2><<<grid, 256, 0, s>>>(a);
+    } else {
+        if (tile == TILE_32)
+            thin_kernel<FMT, MODE, 1><<<grid, 256, 0, s>>>(a);
+        else if (tile == TILE_64)
+            thin_kernel<FMT, MODE, 2><<<grid, 256, 0, s>>>(a);
+    }
+    if (tile >= TILE_128) {
+        // eight waves of 128 x 64 against four of 128 x 128: 2048 x 14336 x 4096
+        // Q8_0 backward 222 against 238 us, gate and up Q4K 507 against 610.  A
+        // pair's step is 256 units: four waves
+        if constexpr (MODE == FORE_PAIR) {
+            if (tile == TILE_128)
+                product_kernel<FMT, MODE, 2, 2, 2, 4><<<grid, 256, 0, s>>>(a);
+            else
+                product_kernel<FMT, MODE, 2, 2, 4, 4><<<grid, 256, 0, s>>>(a);
+        } else {
+            if (tile == TILE_128)
+                product_kernel<FMT, MODE, 2, 4, 2, 2><<<grid, 512, 0, s>>>(a);
+            else
+                product_kernel<FMT, MODE, 2, 4, 4, 2><<<grid, 512, 0, s>>>(a);
+        }
     }
     return hipGetLastError();
 }
 template <int FMT>
-hipError_t launch_fmt(int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s)
+hipError_t launch_fmt(int mode, int tile, const ProductArgs &a, unsigned grid, hipStream_t s)
 {
     switch (mode) {
     case BACK: return launch_mode<FMT, BACK>(tile, a, grid, s);
@@ -567,12 +743,25 @@ hipError_t launch_fmt(int mode, int tile, const ProductArgs &a, dim3 grid, hipSt
     default: return launch_mode<FMT, FORE_PAIR>(tile, a, grid, s);
     }
 }
+template <int FMT> hipError_t launch_one_fmt(bool bf16, const OneArgs &a, unsigned grid, hipStream_t s)
+{
+    if (bf16)
+        one_kernel<FMT, uint16_t><<<grid, 256, 0, s>>>(a);
+    else
+        one_kernel<FMT, float><<<grid, 256, 0, s>>>(a);
+    return hipGetLastError();
+}
 
 // one instance a source file (product_*.hip)
-hipError_t launch_product_q8_0(int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s);
-hipError_t launch_product_q4k(int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s);
-hipError_t launch_product_q6k(int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s);
-hipError_t launch_product_kquants(int fmt, int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s);
-hipError_t launch_product_legacy(int fmt, int mode, int tile, const ProductArgs &a, dim3 grid, hipStream_t s);
+hipError_t launch_product_q8_0(int mode, int tile, const ProductArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_one_q8_0(bool bf16, const OneArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_product_q4k(int mode, int tile, const ProductArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_one_q4k(bool bf16, const OneArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_product_q6k(int mode, int tile, const ProductArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_one_q6k(bool bf16, const OneArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_product_kquants(int fmt, int mode, int tile, const ProductArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_one_kquants(int fmt, bool bf16, const OneArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_product_legacy(int fmt, int mode, int tile, const ProductArgs &a, unsigned grid, hipStream_t s);
+hipError_t launch_one_legacy(int fmt, bool bf16, const OneArgs &a, unsigned grid, hipStream_t s);
 
 }  // namespace ql

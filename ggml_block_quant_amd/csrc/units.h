@@ -4,12 +4,12 @@
 // the tile before.
 //
 // Unit b is elements 32 b .. 32 b + 31 of the flattened [N][K] tensor; K is a
-// multiple of 32, so a unit never crosses a row or a block.  decode(t, w)
-// gives its elements 8 t .. 8 t + 7 with the values of dequant8 (decode.h):
-// exact in fp32, the affine formats rounded once.  FP8 gives the codes'
-// values without the row's scale (the kernels apply it elsewhere).
-// halves(t, h) gives the same elements as four pairs of fp16, rounded once.
-// The tuned formats' codes reach it two at a time, as the 16-bit patterns of
+// multiple of 32, so a unit never crosses a row or a block.  Its elements 8 t ..
+// 8 t + 7 have the values of dequant8 (decode.h), exact in fp32 or, in the
+// affine formats, rounded once; FP8 gives the codes' values without the row's
+// scale (the kernels apply it elsewhere): values(t, w).  halves(t, h) gives
+// them as four pairs of fp16, rounded once more; pairs(t, h, l) with what that rounding
+// leaves as a second fp16 each.  The tuned formats' codes reach it two at a time, as the 16-bit patterns of
 // fp16's smallest numbers: a code u in the low bits is u * 2^-24, which a mixed
 // multiply-add (fp32 scale times 2^24, fp16 code, fp32 offset, fp16 result)
 // takes as it is, without a conversion of its own (Q4K: 13 instructions for 8
@@ -20,9 +20,6 @@
 
 namespace ql {
 
-// the four bytes of a dword as fp32 (v_cvt_f32_ubyte0 .. 3)
-__device__ __forceinline__ float byte_f32(uint32_t d, int i) { return (float)((d >> (8 * i)) & 255u); }
-
 // 6-bit scale and min j (of 8) of a Q4K / Q5K header, times d and dmin
 __device__ __forceinline__ void header_scales(uint4 h, int j, float &S, float &T)
 {
@@ -32,8 +29,6 @@ __device__ __forceinline__ void header_scales(uint4 h, int j, float &S, float &T
     T = -(f16_bits_to_f32(h.x >> 16) * (float)mq);
 }
 
-// Codes in bytes u of two dwords, element 2 i of the task in byte i of `a`...:
-// every unit ends in w = S u + T, one fused multiply-add per weight.
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 __device__ __forceinline__ uint32_t word(const uint2 &v, int i) { return i == 0 ? v.x : v.y; }
 
@@ -49,20 +44,76 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t codes, float s, float t
     const f16x2 u = __builtin_bit_cast(f16x2, codes);
     return __builtin_bit_cast(uint32_t, f16x2{(_Float16)fmaf(s, (float)u.x, t), (_Float16)fmaf(s, (float)u.y, t)});
 }
-template <typename U> __device__ __forceinline__ void halves_of(const U &u, int t, uint32_t h[4])
+// hi = fp16(v), lo = fp16(v - hi) of two values
+__device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo)
 {
-    float v[8];
-    u.decode(t, v);
-#pragma unroll
-    for (int j = 0; j < 4; j++)
-        h[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+    hi = pack_f16(a, b);
+    const f16x2 p = __builtin_bit_cast(f16x2, hi);
+    lo = __builtin_bit_cast(uint32_t, f16x2{(_Float16)fmaf((float)p.x, -1.0f, a), (_Float16)fmaf((float)p.y, -1.0f, b)});
 }
+
+// Through fp32: units that give values (decode)
+template <typename U> struct ByValue {
+    __device__ __forceinline__ void values(int t, float w[8]) const { static_cast<const U *>(this)->decode(t, w); }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    {
+        float v[8];
+        static_cast<const U *>(this)->decode(t, v);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            h[j] = pack_f16(v[2 * j], v[2 * j + 1]);
+    }
+    __device__ __forceinline__ void pairs(int t, uint32_t h[4], uint32_t l[4]) const
+    {
+        float v[8];
+        static_cast<const U *>(this)->decode(t, v);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            split_f16(v[2 * j], v[2 * j + 1], h[j], l[j]);
+    }
+};
+// From 16-bit codes: units that give codes(t, c, s, z), four pairs of codes,
+// each pair's scale times 2^24 (or 2^20 where the codes stand four bits up),
+// and the offset of the task's weights
+template <typename U> struct ByCode {
+    __device__ __forceinline__ void values(int t, float w[8]) const
+    {
+        uint32_t c[4];
+        float s[4], z;
+        static_cast<const U *>(this)->codes(t, c, s, z);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const f16x2 u = __builtin_bit_cast(f16x2, c[j]);
+            w[2 * j] = fmaf(s[j], (float)u.x, z), w[2 * j + 1] = fmaf(s[j], (float)u.y, z);
+        }
+    }
+    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    {
+        uint32_t c[4];
+        float s[4], z;
+        static_cast<const U *>(this)->codes(t, c, s, z);
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            h[j] = scale_codes(c[j], s[j], z);
+    }
+    __device__ __forceinline__ void pairs(int t, uint32_t h[4], uint32_t l[4]) const
+    {
+        uint32_t c[4];
+        float s[4], z;
+        static_cast<const U *>(this)->codes(t, c, s, z);
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const f16x2 u = __builtin_bit_cast(f16x2, c[j]);
+            split_f16(fmaf(s[j], (float)u.x, z), fmaf(s[j], (float)u.y, z), h[j], l[j]);
+        }
+    }
+};
 
 template <int FMT> struct Unit;
 
 // S (u - 128) with the signed code's sign bit flipped: S u - 128 S is exact
 // before its one rounding, which S times the code needs none of
-template <> struct Unit<FMT_Q8_0> {
+template <> struct Unit<FMT_Q8_0> : ByCode<Unit<FMT_Q8_0>> {
     uint4 c0, c1;
     uint32_t d;
     float S, T;
@@ -73,29 +124,18 @@ template <> struct Unit<FMT_Q8_0> {
         d = reinterpret_cast<const uint16_t *>(B + p.scales)[b];
     }
     __device__ __forceinline__ void begin() { S = f16_bits_to_f32(d), T = -128.0f * S; }
-    __device__ __forceinline__ void decode(int t, float w[8]) const
+    __device__ __forceinline__ void codes(int t, uint32_t c[4], float s[4], float &z) const
     {
         const uint32_t x = word(t < 2 ? c0 : c1, 2 * (t & 1)) ^ 0x80808080u;
         const uint32_t y = word(t < 2 ? c0 : c1, 2 * (t & 1) + 1) ^ 0x80808080u;
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            w[i] = fmaf(S, byte_f32(x, i), T);
-            w[i + 4] = fmaf(S, byte_f32(y, i), T);
-        }
-    }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
-    {
-        const uint32_t x = word(t < 2 ? c0 : c1, 2 * (t & 1)) ^ 0x80808080u;
-        const uint32_t y = word(t < 2 ? c0 : c1, 2 * (t & 1) + 1) ^ 0x80808080u;
-        const float s = S * 0x1p24f;
-        h[0] = scale_codes(__builtin_amdgcn_perm(0u, x, 0x0c010c00u), s, T);
-        h[1] = scale_codes(__builtin_amdgcn_perm(0u, x, 0x0c030c02u), s, T);
-        h[2] = scale_codes(__builtin_amdgcn_perm(0u, y, 0x0c010c00u), s, T);
-        h[3] = scale_codes(__builtin_amdgcn_perm(0u, y, 0x0c030c02u), s, T);
+        c[0] = __builtin_amdgcn_perm(0u, x, 0x0c010c00u), c[1] = __builtin_amdgcn_perm(0u, x, 0x0c030c02u);
+        c[2] = __builtin_amdgcn_perm(0u, y, 0x0c010c00u), c[3] = __builtin_amdgcn_perm(0u, y, 0x0c030c02u);
+        s[0] = s[1] = s[2] = s[3] = S * 0x1p24f;
+        z = T;
     }
 };
 
-template <> struct Unit<FMT_Q4K> {
+template <> struct Unit<FMT_Q4K> : ByCode<Unit<FMT_Q4K>> {
     uint4 c, h;
     int j;
     float S, T;
@@ -106,31 +146,18 @@ template <> struct Unit<FMT_Q4K> {
         j = (int)(b & 7);
     }
     __device__ __forceinline__ void begin() { header_scales(h, j, S, T); }
-    __device__ __forceinline__ void decode(int t, float w[8]) const
-    {
-        // even nibbles n0 n2 n4 n6 are elements 0 4 1 5, odd ones 2 6 3 7
-        const uint32_t e = word(c, t) & 0x0f0f0f0fu, o = (word(c, t) >> 4) & 0x0f0f0f0fu;
-        constexpr int at[4] = {0, 4, 1, 5};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            w[at[i]] = fmaf(S, byte_f32(e, i), T);
-            w[at[i] + 2] = fmaf(S, byte_f32(o, i), T);
-        }
-    }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    __device__ __forceinline__ void codes(int t, uint32_t x[4], float s[4], float &z) const
     {
         // elements 2 p and 2 p + 1 at nibbles p and p + 4; every second pair
         // keeps its nibbles four bits up
         const uint32_t d = word(c, t), d8 = d >> 8;
-        const float s = S * 0x1p24f, s16 = S * 0x1p20f;
-        h[0] = scale_codes(d & 0x000f000fu, s, T);
-        h[1] = scale_codes(d & 0x00f000f0u, s16, T);
-        h[2] = scale_codes(d8 & 0x000f000fu, s, T);
-        h[3] = scale_codes(d8 & 0x00f000f0u, s16, T);
+        x[0] = d & 0x000f000fu, x[1] = d & 0x00f000f0u, x[2] = d8 & 0x000f000fu, x[3] = d8 & 0x00f000f0u;
+        s[0] = s[2] = S * 0x1p24f, s[1] = s[3] = S * 0x1p20f;
+        z = T;
     }
 };
 
-template <> struct Unit<FMT_Q6K> {
+template <> struct Unit<FMT_Q6K> : ByCode<Unit<FMT_Q6K>> {
     uint4 lo;
     uint2 hi;
     uint32_t sc, d;
@@ -149,40 +176,24 @@ template <> struct Unit<FMT_Q6K> {
         const float f = f16_bits_to_f32(d);
         S = f * (float)(int8_t)sc, S1 = f * (float)(int8_t)(sc >> 8);
     }
-    __device__ __forceinline__ void decode(int t, float w[8]) const
-    {
-        const uint32_t e = word(lo, t) & 0x0f0f0f0fu, o = (word(lo, t) >> 4) & 0x0f0f0f0fu;
-        // byte a of `h` holds the high bits of elements 0 2 4 6, byte a + 2 of
-        // 1 3 5 7: laid under the nibbles' order 0 4 1 5 | 2 6 3 7
-        const uint32_t h = word(hi, t >> 1) >> (8 * (t & 1));
-        const uint32_t a = h & 0x00ff00ffu;                      // x0: bits of 0 2 4 6, x2: of 1 3 5 7
-        const uint32_t eh = ((a << 4) & 0x00300030u) | ((a << 8) & 0x30003000u);   // 0 4 1 5
-        const uint32_t oh = ((a << 2) & 0x00300030u) | ((a << 6) & 0x30003000u);   // 2 6 3 7
-        const uint32_t x = e | eh, y = o | oh;
-        const float s = t < 2 ? S : S1, z = -32.0f * s;
-        constexpr int at[4] = {0, 4, 1, 5};
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            w[at[i]] = fmaf(s, byte_f32(x, i), z);
-            w[at[i] + 2] = fmaf(s, byte_f32(y, i), z);
-        }
-    }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const
+    __device__ __forceinline__ void codes(int t, uint32_t x[4], float s[4], float &z) const
     {
         // elements 2 p and 2 p + 1: nibbles p and p + 4, high bits 2 p of the
         // octet and of the one 16 bits up
-        const uint32_t d = word(lo, t), a = word(hi, t >> 1) >> (8 * (t & 1));
-        const float f = t < 2 ? S : S1, z = -32.0f * f, s = f * 0x1p24f, s16 = f * 0x1p20f;
-        h[0] = scale_codes((d & 0x000f000fu) | ((a << 4) & 0x00300030u), s, z);
-        h[1] = scale_codes((d & 0x00f000f0u) | ((a << 6) & 0x03000300u), s16, z);
-        h[2] = scale_codes(((d >> 8) & 0x000f000fu) | (a & 0x00300030u), s, z);
-        h[3] = scale_codes(((d >> 8) & 0x00f000f0u) | ((a << 2) & 0x03000300u), s16, z);
+        const uint32_t l = word(lo, t), a = word(hi, t >> 1) >> (8 * (t & 1));
+        x[0] = (l & 0x000f000fu) | ((a << 4) & 0x00300030u);
+        x[1] = (l & 0x00f000f0u) | ((a << 6) & 0x03000300u);
+        x[2] = ((l >> 8) & 0x000f000fu) | (a & 0x00300030u);
+        x[3] = ((l >> 8) & 0x00f000f0u) | ((a << 2) & 0x03000300u);
+        const float f = t < 2 ? S : S1;
+        s[0] = s[2] = f * 0x1p24f, s[1] = s[3] = f * 0x1p20f;
+        z = -32.0f * f;
     }
 };
 
 // Natural order (all formats below): element k of a task at field k of its
 // word, the top bit (where there is one) at bit k of its byte.
-template <> struct Unit<FMT_Q5K> {
+template <> struct Unit<FMT_Q5K> : ByValue<Unit<FMT_Q5K>> {
     uint4 c, h;
     uint32_t hi;
     int j;
@@ -202,10 +213,9 @@ template <> struct Unit<FMT_Q5K> {
         for (int k = 0; k < 8; k++)
             w[k] = fmaf(S, (float)(((lo >> (4 * k)) & 15u) | ((hb >> k) & 1u) << 4), T);
     }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
-template <> struct Unit<FMT_Q3K> {
+template <> struct Unit<FMT_Q3K> : ByValue<Unit<FMT_Q3K>> {
     uint2 c;
     uint32_t hi, s0, s2, d;
     int j;
@@ -237,10 +247,9 @@ template <> struct Unit<FMT_Q3K> {
         for (int k = 0; k < 8; k++)
             w[k] = s * (float)((int)(((lo >> (2 * k)) & 3u) | ((hb >> k) & 1u) << 2) - 4);
     }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
-template <> struct Unit<FMT_Q2K> {
+template <> struct Unit<FMT_Q2K> : ByValue<Unit<FMT_Q2K>> {
     uint2 c;
     uint32_t sm, dd;
     float S, T, S1, T1;
@@ -264,11 +273,10 @@ template <> struct Unit<FMT_Q2K> {
         for (int k = 0; k < 8; k++)
             w[k] = fmaf(s, (float)((lo >> (2 * k)) & 3u), z);
     }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 // E4M3 codes as their values
-template <> struct Unit<FMT_FP8> {
+template <> struct Unit<FMT_FP8> : ByValue<Unit<FMT_FP8>> {
     uint4 c0, c1;
     __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &, int64_t b)
     {
@@ -284,11 +292,10 @@ template <> struct Unit<FMT_FP8> {
         w[4] = __builtin_amdgcn_cvt_f32_fp8(y, 0), w[5] = __builtin_amdgcn_cvt_f32_fp8(y, 1);
         w[6] = __builtin_amdgcn_cvt_f32_fp8(y, 2), w[7] = __builtin_amdgcn_cvt_f32_fp8(y, 3);
     }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 // the 32-element blocks: Q4_0, Q5_0 (symmetric), Q4_1, Q5_1 (with a minimum)
-template <int FMT> struct Unit {
+template <int FMT> struct Unit : ByValue<Unit<FMT>> {
     static constexpr bool five = FMT == FMT_Q5_0 || FMT == FMT_Q5_1;
     static constexpr bool affine = FMT == FMT_Q4_1 || FMT == FMT_Q5_1;
     static_assert(FMT == FMT_Q4_0 || five || affine, "a 32-element block format");
@@ -316,7 +323,6 @@ template <int FMT> struct Unit {
         for (int k = 0; k < 8; k++)
             w[k] = fmaf(S, (float)(((lo >> (4 * k)) & 15u) | ((hb >> k) & 1u) << 4), T);
     }
-    __device__ __forceinline__ void halves(int t, uint32_t h[4]) const { halves_of(*this, t, h); }
 };
 
 }  // namespace ql
