@@ -578,23 +578,20 @@ template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(Xent
 // Plans and launches
 // ---------------------------------------------------------------------------
 
-int tile_rows(int tile) { return 32 << tile; }
-// rows of one call -> the tile
-int tile_of(int64_t M) { return M <= 32 ? TILE_32 : M <= 64 ? TILE_64 : M <= 128 ? TILE_128 : TILE_256; }
+int tile_rows(int tile) { return tile == TILE_192 ? 192 : tile == TILE_256 ? 256 : 32 << tile; }
 
 // A form of the product by its mode and tile: columns of C and of the
-// reduction that a workgroup takes at a time, columns of a panel of A, and how
-// many workgroups its reduction is split for.
+// reduction that a workgroup takes at a time, columns of a panel of A.
 struct Form {
-    int cols, step, panel, split_to;
+    int cols, step, panel;
 };
 Form form_of(int mode, int tile)
 {
     if (mode == BACK)
-        return Form{256, 64, 64, tile <= TILE_64 ? 512 : 256};
+        return Form{256, 64, 64};
     if (tile <= TILE_64)
-        return Form{mode == FORE_GLU ? 32 : 64, 128, 64, 512};
-    return mode == FORE_GLU ? Form{128, 64, 64, 256} : Form{256, 32, 32, 256};
+        return Form{mode == FORE_GLU ? 32 : 64, 128, 64};
+    return mode == FORE_GLU ? Form{128, 64, 64} : Form{256, 32, 32};
 }
 
 struct Plan {
@@ -602,20 +599,62 @@ struct Plan {
     int64_t Mp, tiles;
     Form f;
 };
-// M rows, `cols` columns of C, a reduction over `parts` times `depth`
-Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
+// Up to 64 rows a launch is split until it fills the card twice; from 65 on a
+// workgroup has a CU to itself, and splits are chosen by time.
+constexpr int kSplitTo = 512, kTimedSplits = 64, kTimedTo = 1024;
+
+Plan plan_with(int mode, int tile, int64_t M, int64_t cols, int64_t depth, int parts, int64_t n)
 {
     Plan p;
-    p.tile = tile_of(M);
-    p.f = form_of(mode, p.tile);
-    p.Mp = up_to(M, tile_rows(p.tile));
-    p.tiles = p.Mp / tile_rows(p.tile) * ((cols + p.f.cols - 1) / p.f.cols);
+    p.tile = tile;
+    p.f = form_of(mode, tile);
+    p.Mp = up_to(M, tile_rows(tile));
+    p.tiles = p.Mp / tile_rows(tile) * ((cols + p.f.cols - 1) / p.f.cols);
     p.steps = (int)((depth + p.f.step - 1) / p.f.step) * parts;
-    int64_t n = p.f.split_to / p.tiles;
     n = n < 1 ? 1 : n > p.steps ? p.steps : n;
     p.per = (int)((p.steps + n - 1) / n);
     p.splits = (p.steps + p.per - 1) / p.per;
     return p;
+}
+// Estimated time of a plan in us, from what its kernels reach: a workgroup's
+// products in TFLOP/s (256 rows: 1.0 to 1.1 PFLOP/s of the card in the backward
+// form, half for pairs), whole rounds of 256 workgroups, 4 us to start, and the
+// splits' sums written and read (backward: none where there is one split; the
+// cross entropy reads them twice) at 4.5 TB/s.
+double plan_us(const Plan &p, int mode, int64_t M, int64_t cols)
+{
+    const double rate = (p.tile == TILE_256 ? 4.1 : p.tile == TILE_192 ? 3.6 : 2.6) * (mode == FORE_PAIR ? 0.5 : 1.0);
+    const int64_t rounds = (p.tiles * p.splits + 255) / 256;
+    const double flops = 2.0 * tile_rows(p.tile) * 256 * p.f.step * p.per;
+    const double bytes = 4.0 * M * cols * (mode == FORE_GLU ? 2 : 1);
+    const double moved = mode == BACK ? (p.splits > 1 ? 2 * p.splits : 0) : mode == FORE_GLU ? 2 * p.splits : 3 * p.splits;
+    return rounds * (flops / rate * 1e-6 + 4.0) + moved * bytes / 4.5e6;
+}
+// M rows, `cols` columns of C, a reduction over `parts` times `depth`.  Between
+// one tile of 192 and of 256 rows, and between splits, the least time decides:
+// 515 rows are 3 tiles of either (6144 x 4096 Q4K backward 49.7 and 41.0 us);
+// 375 tiles in one round and a half leave half of the card idle in the second.
+Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
+{
+    if (M <= 64) {
+        const int tile = M <= 32 ? TILE_32 : TILE_64;
+        const Form f = form_of(mode, tile);
+        return plan_with(mode, tile, M, cols, depth, parts, kSplitTo / ((cols + f.cols - 1) / f.cols));
+    }
+    Plan best{};
+    double least = 0.0;
+    // (192 only where it pads to no more than 256 does: padded() counts on it)
+    const int first = M <= 128 ? TILE_128 : up_to(M, 192) < up_to(M, 256) ? TILE_192 : TILE_256;
+    for (int tile = first; tile <= (M <= 128 ? TILE_128 : TILE_256); tile++)
+        for (int n = 1; n <= kTimedSplits; n++) {
+            const Plan p = plan_with(mode, tile, M, cols, depth, parts, n);
+            if (n > 1 && p.tiles * p.splits > kTimedTo)
+                break;
+            const double us = plan_us(p, mode, M, cols);
+            if (best.steps == 0 || us < least)
+                best = p, least = us;
+        }
+    return best;
 }
 // The most rows that the splits' sums of a call of up to M rows take (splits
 // times rows; 0 where nothing is split).  It grows with M, so that a workspace
@@ -623,11 +662,13 @@ Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
 int64_t split_rows(int mode, int64_t M, int64_t cols)
 {
     int64_t most = 0;
-    for (int t = 0; t <= tile_of(M); t++) {
-        const Form f = form_of(mode, t);
-        const int64_t n = f.split_to / ((cols + f.cols - 1) / f.cols);
-        if (n > 1 && n * tile_rows(t) > most)
-            most = n * tile_rows(t);
+    for (int t = 0; t <= (M <= 32 ? TILE_32 : M <= 64 ? TILE_64 : M <= 128 ? TILE_128 : TILE_256); t++) {
+        const int64_t ct = (cols + form_of(mode, t).cols - 1) / form_of(mode, t).cols;
+        // splits * row tiles * ct is at most this where there is more than one
+        const int64_t n = (t <= TILE_64 ? kSplitTo : kTimedTo) / ct;
+        int64_t rows = n > 1 ? n * tile_rows(t) : 0;
+        rows = t > TILE_64 && rows > kTimedSplits * M ? kTimedSplits * M : rows;
+        most = rows > most ? rows : most;
     }
     return most;
 }
@@ -641,7 +682,8 @@ int64_t chunk_rows(int64_t M, int64_t width, int e)
     r = r > 32768 ? 32768 : r;
     return r < M ? r : M;
 }
-int64_t padded(int64_t M) { return up_to(M, tile_rows(tile_of(M))); }
+// the most rows that a tile of some plan of M rows pads them to
+int64_t padded(int64_t M) { return up_to(M, M <= 32 ? 32 : M <= 64 ? 64 : M <= 128 ? 128 : 256); }
 
 // panels of n columns (a multiple of 128: the widest step)
 int64_t panels_bytes(int64_t Mp, int64_t n) { return up_to(n, 128) * Mp * 2; }
@@ -703,10 +745,10 @@ hipError_t run_join(const float *part, const int *e, const float *w, int splits,
 }
 
 // dX = the backward product of A's rows over one weight or two, split or not
-hipError_t run_back(int fmt, const uint8_t *W0, const uint8_t *W1, const Planes &pl, const uint8_t *A, const int *e,
+Plan back_plan(int64_t M, int64_t rows, int64_t K, int weights) { return plan_of(BACK, M, K, rows, weights); }
+hipError_t run_back(int fmt, const Plan &p, const uint8_t *W0, const uint8_t *W1, const Planes &pl, const uint8_t *A, const int *e,
                     const float *w, int64_t M, int64_t rows, int64_t K, float *part, uint16_t *dX, hipStream_t s)
 {
-    const Plan p = plan_of(BACK, M, K, rows, W1 ? 2 : 1);
     ProductArgs a{};
     a.W0 = W0, a.W1 = W1, a.p = pl, a.A = A, a.e = e, a.w = w;
     a.part = p.splits > 1 ? part : nullptr;
@@ -793,10 +835,11 @@ hipError_t launch_grad(const GradArgs &a, hipStream_t s)
         return run_one(a.fmt, a.W, nullptr, p, a.dY, a.dy_bf16, sw, a.N, a.K, part, a.dX, s);
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R, wide = up_to(a.N, 64);
-        hipError_t err = a.dy_bf16 ? run_rows<64>(static_cast<const uint16_t *>(a.dY) + m * a.N, n, a.N, wide, padded(n), A, e, sw, s)
-                                   : run_rows<64>(static_cast<const float *>(a.dY) + m * a.N, n, a.N, wide, padded(n), A, e, sw, s);
+        const Plan b = back_plan(n, a.N, a.K, 1);
+        hipError_t err = a.dy_bf16 ? run_rows<64>(static_cast<const uint16_t *>(a.dY) + m * a.N, n, a.N, wide, b.Mp, A, e, sw, s)
+                                   : run_rows<64>(static_cast<const float *>(a.dY) + m * a.N, n, a.N, wide, b.Mp, A, e, sw, s);
         if (err == hipSuccess)
-            err = run_back(a.fmt, a.W, nullptr, p, A, e, nullptr, n, a.N, a.K, part, a.dX + m * a.K, s);
+            err = run_back(a.fmt, b, a.W, nullptr, p, A, e, nullptr, n, a.N, a.K, part, a.dX + m * a.K, s);
         if (err != hipSuccess)
             return err;
     }
@@ -832,8 +875,9 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
     float *part = reinterpret_cast<float *>(w.take(back_part_bytes(R, a.K)));
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
+        const Plan b = back_plan(n, a.F, a.K, 2);
         GluRows r{};
-        r.splits = 1, r.act = a.act, r.M = n, r.F = a.F, r.Mp = padded(n);
+        r.splits = 1, r.act = a.act, r.M = n, r.F = a.F, r.Mp = b.Mp;
         r.sg = row_scales(a.fmt, a.gate, pl), r.su = row_scales(a.fmt, a.up, pl);
         r.dH = a.dh_bf16 ? (const void *)(static_cast<const uint16_t *>(a.dH) + m * a.F)
                          : (const void *)(static_cast<const float *>(a.dH) + m * a.F);
@@ -880,7 +924,7 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
                      : vec ? run(glu_rows_kernel<float, HELD_LONG, true>) : run(glu_rows_kernel<float, HELD_LONG, false>);
             err = hipGetLastError();
             if (err == hipSuccess)
-                err = run_back(a.fmt, a.gate, a.up, pl, AD, ed, nullptr, n, a.F, a.K, part, a.dX + m * a.K, s);
+                err = run_back(a.fmt, b, a.gate, a.up, pl, AD, ed, nullptr, n, a.F, a.K, part, a.dX + m * a.K, s);
         }
         if (err != hipSuccess)
             return err;
@@ -947,9 +991,10 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
         const uint16_t *X = a.X + m * a.K;
+        const Plan b = back_plan(n, a.N, a.K, 1);
         XentRows r{};
         r.run = xent_run(n, a.N), r.runs = (int)((a.N + r.run - 1) / r.run);
-        r.part = z, r.splits = 1, r.M = n, r.N = a.N, r.Mp = padded(n), r.sw = row_scales(a.fmt, a.W, pl), r.targets = a.targets + m;
+        r.part = z, r.splits = 1, r.M = n, r.N = a.N, r.Mp = b.Mp, r.sw = row_scales(a.fmt, a.W, pl), r.targets = a.targets + m;
         r.weights = a.weights ? a.weights + m : nullptr, r.stats = stats, r.e_out = ed, r.w_out = wd;
         if (n == 1)
             r.D = reinterpret_cast<float *>(AD);
@@ -983,7 +1028,7 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
         err = hipGetLastError();
         if (err == hipSuccess && a.dX)
             err = n == 1 ? run_one(a.fmt, a.W, nullptr, pl, r.D, false, nullptr, a.N, a.K, part, a.dX + m * a.K, s)
-                         : run_back(a.fmt, a.W, nullptr, pl, AD, ed, wd, n, a.N, a.K, part, a.dX + m * a.K, s);
+                         : run_back(a.fmt, b, a.W, nullptr, pl, AD, ed, wd, n, a.N, a.K, part, a.dX + m * a.K, s);
         if (err != hipSuccess)
             return err;
     }

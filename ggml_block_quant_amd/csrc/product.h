@@ -131,7 +131,7 @@ struct Tile {
     static constexpr int ABYTES = TM * BK * 2;
     static constexpr int BUF = ABYTES + WBYTES;
     static constexpr int UNITS = MODE == BACK ? 64 * 8 : 256 * BK / 32;
-    static constexpr int UPT = (UNITS + NT - 1) / NT;
+    static constexpr int UPT = UNITS / NT, TASKS = 4 * UPT;  // units a thread, tasks of eight weights
     // Up to 32 rows of A a step's products are short against the memory's
     // latency: what is on its way has to be several steps.  A then comes
     // through registers as W does, and the compiler's own waits let every set
@@ -208,8 +208,9 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
             }
         }
     };
-    // task t (8 elements) of unit i into LDS
-    auto store_w = [&](Unit<FMT>(&u)[T::UPT], int i, int t, int buf) {
+    // task k of this thread (8 weights: task t of unit i) into LDS
+    auto store_w = [&](Unit<FMT>(&u)[T::UPT], int k, int buf) {
+        const int i = k / 4, t = k % 4;
         if (t == 0)
             u[i].begin();
         const int x = tid + i * T::NT;
@@ -317,14 +318,14 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
     const int last = s1 - 1;
     // step s with the next one's bytes in `t`, which it refills for DEPTH later
     auto step = [&](int s, Set &t) {
-        constexpr int tasks = 4 * T::UPT;
+        constexpr int tasks = T::TASKS;
         store_a_regs(t, buf ^ 1);
 #pragma unroll
         for (int x = 0; x + 1 < NP; x++) {
             product(x, buf, true);
 #pragma unroll
             for (int k = x * tasks / (NP - 1); k < (x + 1) * tasks / (NP - 1); k++)
-                store_w(t.u, k / 4, k % 4, buf ^ 1);
+                store_w(t.u, k, buf ^ 1);
             // a product of the matrix cores, then decode beside it
 #pragma unroll
             for (int g = 0; g < MI * NI; g++) {
@@ -356,8 +357,8 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
         __builtin_amdgcn_sched_barrier(0);
         store_a_regs(head, 0);
 #pragma unroll
-        for (int k = 0; k < 4 * T::UPT; k++)
-            store_w(head.u, k / 4, k % 4, 0);
+        for (int k = 0; k < T::TASKS; k++)
+            store_w(head.u, k, 0);
         if constexpr (!T::AREG)
             wait_loads();
         lds_barrier();
@@ -699,7 +700,7 @@ __global__ __launch_bounds__(256) void one_kernel(OneArgs a)
 }
 
 // The shapes of a product's workgroups, by the rows of A they take.
-enum { TILE_32 = 0, TILE_64 = 1, TILE_128 = 2, TILE_256 = 3 };
+enum { TILE_32 = 0, TILE_64 = 1, TILE_128 = 2, TILE_192 = 3, TILE_256 = 4 };
 
 template <int FMT, int MODE>
 hipError_t launch_mode(int tile, const ProductArgs &a, unsigned grid, hipStream_t s)
@@ -719,15 +720,20 @@ hipError_t launch_mode(int tile, const ProductArgs &a, unsigned grid, hipStream_
     if (tile >= TILE_128) {
         // eight waves of 128 x 64 against four of 128 x 128: 2048 x 14336 x 4096
         // Q8_0 backward 222 against 238 us, gate and up Q4K 507 against 610.  A
-        // pair's step is 256 units: four waves
+        // pair's step is 256 units: four waves (eight that share units 1914
+        // against 1461 us at 512 x 131072 x 5120 Q6K)
         if constexpr (MODE == FORE_PAIR) {
             if (tile == TILE_128)
                 product_kernel<FMT, MODE, 2, 2, 2, 4><<<grid, 256, 0, s>>>(a);
+            else if (tile == TILE_192)
+                product_kernel<FMT, MODE, 2, 2, 3, 4><<<grid, 256, 0, s>>>(a);
             else
                 product_kernel<FMT, MODE, 2, 2, 4, 4><<<grid, 256, 0, s>>>(a);
         } else {
             if (tile == TILE_128)
                 product_kernel<FMT, MODE, 2, 4, 2, 2><<<grid, 512, 0, s>>>(a);
+            else if (tile == TILE_192)
+                product_kernel<FMT, MODE, 2, 4, 3, 2><<<grid, 512, 0, s>>>(a);
             else
                 product_kernel<FMT, MODE, 2, 4, 4, 2><<<grid, 512, 0, s>>>(a);
         }
