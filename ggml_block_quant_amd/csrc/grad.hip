@@ -6,6 +6,8 @@
 #include "grad.h"
 #include "product.h"
 
+#include <initializer_list>
+
 namespace ql {
 
 namespace {
@@ -276,8 +278,10 @@ __device__ __forceinline__ void glu_grad(int act, float g, float u, float dh, fl
 }
 
 struct GluRows {
-    const float *g, *u;  // sums of the rows: split s and row m at (s M + m) ld
+    const float *g, *u;  // sums of the rows, the first split: row m at m ld
+    const float *mg, *mu;  // the others, from column `from` on: row m of split s at ((s - 1) M + m) more_ld - from
     int splits, act;
+    int64_t more_ld, from;
     int64_t M, F, Mp, ld;
     const int *ex;       // exponents of X's rows, or null
     const float *sg, *su;  // FP8's scales of the rows, or null
@@ -294,14 +298,17 @@ __device__ __forceinline__ void glu_values(const GluRows &a, int64_t m, int64_t 
 {
     const int64_t F = a.F;
     const int x = a.ex ? -a.ex[m] : 0;
-    float g[8] = {}, u[8] = {}, h[8], t[8];
-    for (int s = 0; s < a.splits; s++) {
-        const int64_t at = ((int64_t)s * a.M + m) * a.ld;
-        load8<VEC>(a.g + at, 8 * c, F, t);
+    float g[8], u[8], h[8], t[8];
+    load8<VEC>(a.g + m * a.ld, 8 * c, F, g);
+    load8<VEC>(a.u + m * a.ld, 8 * c, F, u);
+    const int splits = 8 * c < a.from ? 1 : a.splits;
+    for (int s = 1; s < splits; s++) {
+        const int64_t at = ((int64_t)(s - 1) * a.M + m) * a.more_ld - a.from;
+        load8<VEC>(a.mg + at, 8 * c, F, t);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             g[j] += t[j];
-        load8<VEC>(a.u + at, 8 * c, F, t);
+        load8<VEC>(a.mu + at, 8 * c, F, t);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             u[j] += t[j];
@@ -417,8 +424,10 @@ __device__ __forceinline__ Stat join(Stat a, Stat b)
 }
 
 struct XentRows {
-    const float *part;       // [splits][M][N]
+    const float *part;       // sums, the first split: [M][ld]
+    const float *more;       // the others, from column `from` on: [splits - 1][M][more_ld]
     int splits, runs;
+    int64_t ld, more_ld, from;
     int64_t M, N, run, Mp;   // runs of `run` logits (a multiple of 64), one a workgroup
     const int *ex;           // exponents of X's rows, or null
     const float *sw;         // FP8's scales of the rows, or null
@@ -434,21 +443,20 @@ struct XentRows {
 
 __device__ __forceinline__ float logit(const XentRows &a, int64_t m, int64_t n, int x)
 {
-    float z = 0.0f;
-    for (int s = 0; s < a.splits; s++)
-        z += a.part[((int64_t)s * a.M + m) * a.N + n];
+    float z = a.part[m * a.ld + n];
+    for (int s = 1; s < (n < a.from ? 1 : a.splits); s++)
+        z += a.more[((int64_t)(s - 1) * a.M + m) * a.more_ld + n - a.from];
     z = __builtin_ldexpf(z, x);
     return a.raw && a.sw ? z * a.sw[n] : z;
 }
-// logits 8 c .. 8 c + 7 of row m, -inf behind the row's end
+// logits 8 c .. 8 c + 7 of row m, -inf behind the row's end.  VEC: rows 16-byte
+// aligned, with room for whole groups of eight
 template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, int64_t m, int64_t c, int x, float z[8])
 {
-#pragma unroll
-    for (int j = 0; j < 8; j++)
-        z[j] = 0.0f;
-    for (int s = 0; s < a.splits; s++) {
+    load8<VEC>(a.part + m * a.ld, 8 * c, a.N, z);
+    for (int s = 1; s < (8 * c < a.from ? 1 : a.splits); s++) {
         float t[8];
-        load8<VEC>(a.part + ((int64_t)s * a.M + m) * a.N, 8 * c, a.N, t);
+        load8<VEC>(a.more + ((int64_t)(s - 1) * a.M + m) * a.more_ld - a.from, 8 * c, a.N, t);
 #pragma unroll
         for (int j = 0; j < 8; j++)
             z[j] += t[j];
@@ -458,7 +466,7 @@ template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, i
         z[j] = __builtin_ldexpf(z[j], x);
         if (a.raw && a.sw)
             z[j] *= a.sw[min(8 * c + j, a.N - 1)];
-        if (!VEC && 8 * c + j >= a.N)
+        if (8 * c + j >= a.N)
             z[j] = -INFINITY;
     }
 }
@@ -594,10 +602,14 @@ Form form_of(int mode, int tile)
     return mode == FORE_GLU ? Form{128, 64, 64} : Form{256, 32, 32};
 }
 
+// tiles of which the first `whole` are not split, the others `splits` ways
 struct Plan {
     int tile, splits, steps, per;
-    int64_t Mp, tiles;
+    int64_t Mp, tiles, whole;
     Form f;
+    int64_t workgroups() const { return whole + (tiles - whole) * splits; }
+    int64_t split_from() const { return splits > 1 ? whole / (Mp / rows) * f.cols : 0; }  // the first column that is split
+    int64_t rows;  // of a tile
 };
 // Up to 64 rows a launch is split until it fills the card twice; from 65 on a
 // workgroup has a CU to itself, and splits are chosen by time.
@@ -606,7 +618,7 @@ constexpr int kSplitTo = 512, kTimedSplits = 64, kTimedTo = 1024;
 Plan plan_with(int mode, int tile, int64_t M, int64_t cols, int64_t depth, int parts, int64_t n)
 {
     Plan p;
-    p.tile = tile;
+    p.tile = tile, p.rows = tile_rows(tile), p.whole = 0;
     p.f = form_of(mode, tile);
     p.Mp = up_to(M, tile_rows(tile));
     p.tiles = p.Mp / tile_rows(tile) * ((cols + p.f.cols - 1) / p.f.cols);
@@ -614,6 +626,17 @@ Plan plan_with(int mode, int tile, int64_t M, int64_t cols, int64_t depth, int p
     n = n < 1 ? 1 : n > p.steps ? p.steps : n;
     p.per = (int)((p.steps + n - 1) / n);
     p.splits = (p.steps + p.per - 1) / p.per;
+    p.whole = p.splits == 1 ? p.tiles : 0;
+    return p;
+}
+// the same with whole columns of tiles unsplit in front, as many as fill whole
+// rounds of 256 workgroups
+Plan with_whole(Plan p)
+{
+    const int64_t mt = p.Mp / p.rows;
+    p.whole = p.tiles / 256 * 256 / mt * mt;
+    if (p.whole == p.tiles || p.splits == 1)
+        p.whole = p.tiles, p.splits = 1, p.per = p.steps;
     return p;
 }
 // Estimated time of a plan in us, from what its kernels reach: a workgroup's
@@ -624,16 +647,19 @@ Plan plan_with(int mode, int tile, int64_t M, int64_t cols, int64_t depth, int p
 double plan_us(const Plan &p, int mode, int64_t M, int64_t cols)
 {
     const double rate = (p.tile == TILE_256 ? 4.1 : p.tile == TILE_192 ? 3.6 : 2.6) * (mode == FORE_PAIR ? 0.5 : 1.0);
-    const int64_t rounds = (p.tiles * p.splits + 255) / 256;
-    const double flops = 2.0 * tile_rows(p.tile) * 256 * p.f.step * p.per;
-    const double bytes = 4.0 * M * cols * (mode == FORE_GLU ? 2 : 1);
-    const double moved = mode == BACK ? (p.splits > 1 ? 2 * p.splits : 0) : mode == FORE_GLU ? 2 * p.splits : 3 * p.splits;
-    return rounds * (flops / rate * 1e-6 + 4.0) + moved * bytes / 4.5e6;
+    const int64_t rounds = (p.whole + 255) / 256, parted = ((p.tiles - p.whole) * p.splits + 255) / 256;
+    const double flops = 2.0 * p.rows * 256 * p.f.step;  // of a step
+    const double bytes = 4.0 * M * cols * (mode == FORE_GLU ? 2 : 1), part = 1.0 - (double)p.whole / p.tiles;
+    const double times = (1.0 - part) + part * p.splits;  // that a value of C is written
+    const double moved = mode == BACK ? (p.splits > 1 ? 2 * times : 0) : mode == FORE_GLU ? 2 * times : 3 * times;
+    return rounds * (flops * p.steps / rate * 1e-6 + 4.0) + parted * (flops * p.per / rate * 1e-6 + 4.0) + moved * bytes / 4.5e6;
 }
 // M rows, `cols` columns of C, a reduction over `parts` times `depth`.  Between
 // one tile of 192 and of 256 rows, and between splits, the least time decides:
 // 515 rows are 3 tiles of either (6144 x 4096 Q4K backward 49.7 and 41.0 us);
-// 375 tiles in one round and a half leave half of the card idle in the second.
+// 375 tiles in one round and a half leave half of the card idle in the second,
+// so a forward product may split what its whole rounds leave (gate and up of
+// 2048 x 14336 x 4096: 896 tiles, the last 128 in halves).
 Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
 {
     if (M <= 64) {
@@ -647,12 +673,15 @@ Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
     const int first = M <= 128 ? TILE_128 : up_to(M, 192) < up_to(M, 256) ? TILE_192 : TILE_256;
     for (int tile = first; tile <= (M <= 128 ? TILE_128 : TILE_256); tile++)
         for (int n = 1; n <= kTimedSplits; n++) {
-            const Plan p = plan_with(mode, tile, M, cols, depth, parts, n);
-            if (n > 1 && p.tiles * p.splits > kTimedTo)
-                break;
-            const double us = plan_us(p, mode, M, cols);
-            if (best.steps == 0 || us < least)
-                best = p, least = us;
+            const Plan p = plan_with(mode, tile, M, cols, depth, parts, n), q = with_whole(p);
+            // (a backward product's sums are joined for all columns or none)
+            for (const Plan &t : {p, q}) {
+                if (t.splits > 1 && ((t.tiles - t.whole) * t.splits > kTimedTo || (mode == BACK && t.whole > 0)))
+                    continue;
+                const double us = plan_us(t, mode, M, cols);
+                if (best.steps == 0 || us < least)
+                    best = t, least = us;
+            }
         }
     return best;
 }
@@ -690,8 +719,8 @@ int64_t panels_bytes(int64_t Mp, int64_t n) { return up_to(n, 128) * Mp * 2; }
 
 hipError_t launch_product(int fmt, int mode, const Plan &p, ProductArgs a, hipStream_t s)
 {
-    a.Mp = p.Mp, a.steps = p.steps, a.per = p.per, a.tiles = (uint32_t)p.tiles;
-    const unsigned grid = (unsigned)(p.tiles * p.splits);
+    a.Mp = p.Mp, a.steps = p.steps, a.per = p.per, a.tiles = (uint32_t)p.tiles, a.whole = (uint32_t)p.whole;
+    const unsigned grid = (unsigned)p.workgroups();
     switch (fmt) {
     case FMT_Q8_0: return launch_product_q8_0(mode, p.tile, a, grid, s);
     case FMT_Q4K: return launch_product_q4k(mode, p.tile, a, grid, s);
@@ -753,7 +782,7 @@ hipError_t run_back(int fmt, const Plan &p, const uint8_t *W0, const uint8_t *W1
     a.W0 = W0, a.W1 = W1, a.p = pl, a.A = A, a.e = e, a.w = w;
     a.part = p.splits > 1 ? part : nullptr;
     a.out = p.splits > 1 ? nullptr : dX;
-    a.M = M, a.ld = K, a.rows = rows, a.K = K;
+    a.M = M, a.ld = a.more_ld = K, a.more = part + M * K, a.rows = rows, a.K = K;
     const hipError_t err = launch_product(fmt, BACK, p, a, s);
     if (err != hipSuccess || p.splits == 1)
         return err;
@@ -793,12 +822,16 @@ int64_t back_part_bytes(int64_t M, int64_t K)
     const int64_t one = kOneSplitTo / ((K + 255) / 256), tiles = split_rows(BACK, M, K);
     return 4 * K * (tiles > one ? tiles : one > 1 ? one : 1);
 }
-// sums of a forward product: rows of `width` values, split or not (and room to
-// start the second half on a 256-byte boundary)
-int64_t fore_part_bytes(int mode, int64_t M, int64_t cols, int64_t width)
+// Sums of a forward product: rows of `width` values, and what the other splits
+// of split columns take: at most the tiles they are split into (64 x 64 values
+// up to 64 rows, 256 x 256 from 65), and so many times the rows.  (256 bytes to
+// start a second half on a boundary.)
+int64_t fore_part_bytes(int64_t M, int64_t width)
 {
-    const int64_t r = split_rows(mode, M, cols);
-    return (r > M ? r : M) * width * 4 + 256;
+    const auto least = [](int64_t a, int64_t b) { return a < b ? a : b; };
+    const int64_t few = least((int64_t)kSplitTo * 64 * 64, kSplitTo * (M < 64 ? M : 64) * width);
+    const int64_t many = M > 64 ? least((int64_t)kTimedTo * 256 * 256, kTimedSplits * M * width) : 0;
+    return 4 * (M * width + (few > many ? few : many)) + 256;
 }
 
 // Up to two rows the forward products are matrix-vector products: the GEMV
@@ -858,7 +891,7 @@ int64_t glu_grad_workspace(int fmt, int64_t M, int64_t F, int64_t K)
     w.take(2 * panels_bytes(padded(R), F));
     w.take(4 * R);
     w.take(4 * R);
-    w.take(fore_part_bytes(FORE_GLU, R, F, 2 * F));
+    w.take(fore_part_bytes(R, 2 * F));
     w.take(back_part_bytes(R, K));
     return w.used;
 }
@@ -871,7 +904,7 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
     uint8_t *AX = w.take(panels_bytes(padded(R), a.K));
     uint8_t *AD = w.take(2 * panels_bytes(padded(R), a.F));
     int *ex = reinterpret_cast<int *>(w.take(4 * R)), *ed = reinterpret_cast<int *>(w.take(4 * R));
-    float *gu = reinterpret_cast<float *>(w.take(fore_part_bytes(FORE_GLU, R, a.F, 2 * a.F)));
+    float *gu = reinterpret_cast<float *>(w.take(fore_part_bytes(R, 2 * a.F)));
     float *part = reinterpret_cast<float *>(w.take(back_part_bytes(R, a.K)));
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
@@ -897,8 +930,10 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
                 return err;
             ProductArgs g{};
             g.W0 = a.gate, g.W1 = a.up, g.p = pl, g.A = AX, g.part = gu, g.M = n, g.ld = 2 * a.F, g.rows = a.F, g.K = a.K;
+            r.from = g.from = p.split_from(), r.more_ld = g.more_ld = 2 * (a.F - g.from), g.more = gu + n * g.ld;
             err = launch_product(a.fmt, FORE_GLU, p, g, s);
-            r.g = gu, r.u = gu + a.F, r.ld = 2 * a.F, r.splits = p.splits, r.ex = ex, r.raw = true;
+            r.g = gu, r.u = gu + a.F, r.ld = 2 * a.F, r.mg = g.more, r.mu = g.more + g.more_ld / 2;
+            r.splits = p.splits, r.ex = ex, r.raw = true;
         }
         if (err != hipSuccess)
             return err;
@@ -959,7 +994,7 @@ int64_t xent_workspace(int fmt, int64_t M, int64_t N, int64_t K, bool grad)
     Pieces w{nullptr};
     w.take(panels_bytes(padded(R), K));
     w.take(4 * R);
-    w.take(fore_part_bytes(FORE_PAIR, R, N, N));
+    w.take(fore_part_bytes(R, up_to(N, 8)));
     w.take(stats_bytes(R, N));
     if (grad) {
         w.take(panels_bytes(padded(R), N));
@@ -977,7 +1012,7 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
     Pieces w{a.ws};
     uint8_t *AX = w.take(panels_bytes(padded(R), a.K));
     int *ex = reinterpret_cast<int *>(w.take(4 * R));
-    float *z = reinterpret_cast<float *>(w.take(fore_part_bytes(FORE_PAIR, R, a.N, a.N)));
+    float *z = reinterpret_cast<float *>(w.take(fore_part_bytes(R, up_to(a.N, 8))));
     Stat *stats = reinterpret_cast<Stat *>(w.take(stats_bytes(R, a.N)));
     uint8_t *AD = nullptr;
     int *ed = nullptr;
@@ -994,7 +1029,7 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
         const Plan b = back_plan(n, a.N, a.K, 1);
         XentRows r{};
         r.run = xent_run(n, a.N), r.runs = (int)((a.N + r.run - 1) / r.run);
-        r.part = z, r.splits = 1, r.M = n, r.N = a.N, r.Mp = b.Mp, r.sw = row_scales(a.fmt, a.W, pl), r.targets = a.targets + m;
+        r.part = z, r.splits = 1, r.ld = a.N, r.M = n, r.N = a.N, r.Mp = b.Mp, r.sw = row_scales(a.fmt, a.W, pl), r.targets = a.targets + m;
         r.weights = a.weights ? a.weights + m : nullptr, r.stats = stats, r.e_out = ed, r.w_out = wd;
         if (n == 1)
             r.D = reinterpret_cast<float *>(AD);
@@ -1011,14 +1046,17 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
             if (err != hipSuccess)
                 return err;
             ProductArgs g{};
-            g.W0 = a.W, g.p = pl, g.A = AX, g.part = z, g.M = n, g.ld = a.N, g.rows = a.N, g.K = a.K;
+            // (rows of whole groups of eight, whatever N)
+            r.ld = up_to(a.N, 8);
+            g.W0 = a.W, g.p = pl, g.A = AX, g.part = z, g.M = n, g.ld = r.ld, g.rows = a.N, g.K = a.K;
+            r.from = g.from = p.split_from(), r.more_ld = g.more_ld = r.ld - g.from, r.more = g.more = z + n * r.ld;
             err = launch_product(a.fmt, FORE_PAIR, p, g, s);
             r.splits = p.splits, r.ex = ex, r.raw = true;
         }
         if (err != hipSuccess)
             return err;
         const dim3 grid((unsigned)r.runs, (unsigned)n), rows = a.dX ? grid : dim3(1, (unsigned)n);
-        if (a.N % 8 == 0) {
+        if (r.ld % 8 == 0) {
             stat_kernel<true><<<grid, 256, 0, s>>>(r);
             xent_rows_kernel<true><<<rows, 256, 0, s>>>(r);
         } else {

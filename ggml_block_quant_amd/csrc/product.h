@@ -79,13 +79,18 @@ struct ProductArgs {
     const uint8_t *A;        // panels (backward of two weights: the second's behind the first's)
     const int *e;            // [M] exponents: A holds values times 2^e
     const float *w;          // [M] factors of the rows of C, or null (backward, one split)
-    float *part;             // [splits][M][ld] unscaled sums, or null
+    // unscaled sums: of the first split [M][ld], of the others [splits - 1][M]
+    // [more_ld], columns from `from` on (what comes before is not split);
+    // FORE_GLU: the second weight's half a row on.  Or null
+    float *part, *more;
+    int64_t more_ld, from;
     uint16_t *out;           // bf16 [M][ld] (backward, one split)
     int64_t M, Mp, ld;
     int64_t rows;            // rows of one weight (N or F)
     int64_t K;
     int steps, per;          // steps along the reduction, steps per split
     uint32_t tiles;          // row tiles times column tiles
+    uint32_t whole;          // of them (the first, whole columns of tiles) those that are not split
 };
 
 // Consecutive workgroups go to the 8 XCDs in turn: each XCD gets a run of
@@ -101,13 +106,27 @@ __device__ __forceinline__ uint32_t xcd_run(uint32_t i, uint32_t n)
 }
 struct Place {
     uint32_t ct;
-    int split;
+    int split, s0, s1;
     int64_t m0;
 };
 __device__ __forceinline__ Place place(const ProductArgs &a, int tm)
 {
-    const uint32_t mt = (uint32_t)(a.Mp / tm), t = xcd_run(blockIdx.x, gridDim.x), tile = t % a.tiles;
-    return Place{tile / mt, (int)(t / a.tiles), (int64_t)(tile % mt) * tm};
+    const uint32_t mt = (uint32_t)(a.Mp / tm);
+    // (the whole tiles and the split ones each spread evenly over the XCDs)
+    uint32_t tile = xcd_run(blockIdx.x, a.whole), split = 0;
+    int s0 = 0, s1 = a.steps;
+    if (blockIdx.x >= a.whole) {
+        const uint32_t i = xcd_run(blockIdx.x - a.whole, gridDim.x - a.whole), n = a.tiles - a.whole;
+        tile = a.whole + i % n, split = i / n;
+        s0 = split * a.per, s1 = min(a.steps, s0 + a.per);
+    }
+    return Place{tile / mt, (int)split, s0, s1, (int64_t)(tile % mt) * tm};
+}
+
+// row m of the sums of a place's split, by column
+__device__ __forceinline__ float *sums_row(const ProductArgs &a, const Place &at, int64_t m)
+{
+    return at.split ? a.more + ((int64_t)(at.split - 1) * a.M + m) * a.more_ld - a.from : a.part + m * a.ld;
 }
 
 enum { BACK = 0, FORE_PAIR = 1, FORE_GLU = 2 };
@@ -161,7 +180,7 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
     const Place at = place(a, T::TM);
     const uint32_t ct = at.ct;
     const int64_t m0 = at.m0;
-    const int s0 = at.split * a.per, s1 = min(a.steps, s0 + a.per);
+    const int s0 = at.s0, s1 = at.s1;
 
     const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_u8 *)smem;
 
@@ -411,13 +430,13 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
                     continue;
                 }
             }
-            float *const y = a.part + ((int64_t)at.split * a.M + m) * a.ld;
+            float *const y = sums_row(a, at, m);
 #pragma unroll
             for (int j = 0; j < NI; j++) {
                 if constexpr (MODE == FORE_GLU) {
                     const int64_t c = (int64_t)ct * 128 + (wn * (NI / 2) + j % (NI / 2)) * 32 + r32;
                     if (c < ncol)
-                        y[(j / (NI / 2)) * ncol + c] = acc[i][j][r];
+                        y[(j / (NI / 2)) * ((at.split ? a.more_ld : a.ld) / 2) + c] = acc[i][j][r];
                 } else {
                     const int64_t c = (int64_t)ct * 256 + (wn * NI + j) * 32 + r32;
                     if (c < ncol)
@@ -459,7 +478,7 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
     const Place at = place(a, T::TM);
     const uint32_t ct = at.ct;
     const int64_t m0 = at.m0;
-    const int s0 = at.split * a.per, s1 = min(a.steps, s0 + a.per);
+    const int s0 = at.s0, s1 = at.s1;
 
     // W: unit tid % 4 of the step, row tid / 4 of the tile
     const uint32_t upr = (uint32_t)(a.K / 32);
@@ -602,7 +621,7 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
         for (int r = 0; r < 16; r++) {
             const int64_t m = m0 + 32 * i + 8 * (r / 4) + 4 * half + r % 4;
             if (m < a.M)
-                a.part[((int64_t)at.split * a.M + m) * a.ld + (MODE == FORE_GLU ? col * a.rows : 0) + c] =
+                sums_row(a, at, m)[(MODE == FORE_GLU ? col * ((at.split ? a.more_ld : a.ld) / 2) : 0) + c] =
                     acc[i][r] + sum[(i * 16 + r) * 64];
         }
 }
