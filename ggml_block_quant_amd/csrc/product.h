@@ -360,6 +360,7 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
             issue_a(min(s + 2, last), buf);
         product(NP - 1, buf ^ 1, true);
         buf ^= 1;
+        __builtin_amdgcn_sched_barrier(0);  // each step's products and decode are ordered by themselves
     };
     if (s0 < s1) {
         Set head;
@@ -645,14 +646,13 @@ struct OneArgs {
 // rounded but the weights' own fp32 values and the sums); 8 lanes read a group
 // of 256 weights, a wave 8 rows, nothing meets before the end.  Against the
 // tiles of 32 rows, which also need the gradients as fp16 panels first (3.5
-// us): 14336 x 4096 Q4K 13.4 against 14.6 us, Q8_0 17.1 against 18.1, 131072 x
-// 5120 Q6K 136 against 141; two rows in this way 20 us, so they take the tiles.
-// Bound by the decode's instructions and the loads' latency together (2.5 to
-// 4 TB/s of weights).
+// us): 14336 x 4096 Q4K 13.4 against 14.6 us, Q8_0 16.1 against 18.1, 131072 x
+// 5120 Q6K 122 against 141; two rows in this way 20 us, so they take the tiles.
+// Bound by the decode's instructions (2.4 to 4.5 TB/s of weights).
 template <int FMT, typename V>
 __global__ __launch_bounds__(256) void one_kernel(OneArgs a)
 {
-    constexpr int DEPTH = 4;
+    constexpr int DEPTH = 2;  // (131072 x 5120 Q6K: 122 us; 3, 4 and 6: 130, 131, 157)
     __shared__ float sum[32][256 + 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int slot = wave * 8 + (lane >> 3), c = lane & 7;

@@ -109,13 +109,19 @@ template <typename U> struct ByCode {
     }
 };
 
+// Holds back what is computed from a loaded register.  Without it the compiler
+// moves a unit's first conversions up behind its load and waits for the memory
+// there, steps too early (a field that is widened where it is loaded likewise:
+// 16-bit fields stay 16 bits wide in a unit).
+__device__ __forceinline__ void hold(uint16_t &x) { asm volatile("" : "+v"(x)); }
+
 template <int FMT> struct Unit;
 
 // S (u - 128) with the signed code's sign bit flipped: S u - 128 S is exact
 // before its one rounding, which S times the code needs none of
 template <> struct Unit<FMT_Q8_0> : ByCode<Unit<FMT_Q8_0>> {
     uint4 c0, c1;
-    uint32_t d;
+    uint16_t d;
     float S, T;
     __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
     {
@@ -123,7 +129,11 @@ template <> struct Unit<FMT_Q8_0> : ByCode<Unit<FMT_Q8_0>> {
         c1 = reinterpret_cast<const uint4 *>(B)[2 * b + 1];
         d = reinterpret_cast<const uint16_t *>(B + p.scales)[b];
     }
-    __device__ __forceinline__ void begin() { S = f16_bits_to_f32(d), T = -128.0f * S; }
+    __device__ __forceinline__ void begin()
+    {
+        hold(d);
+        S = f16_bits_to_f32(d), T = -128.0f * S;
+    }
     __device__ __forceinline__ void codes(int t, uint32_t c[4], float s[4], float &z) const
     {
         const uint32_t x = word(t < 2 ? c0 : c1, 2 * (t & 1)) ^ 0x80808080u;
@@ -160,7 +170,7 @@ template <> struct Unit<FMT_Q4K> : ByCode<Unit<FMT_Q4K>> {
 template <> struct Unit<FMT_Q6K> : ByCode<Unit<FMT_Q6K>> {
     uint4 lo;
     uint2 hi;
-    uint32_t sc, d;
+    uint16_t sc, d;
     float S, S1;
     __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
     {
@@ -173,6 +183,7 @@ template <> struct Unit<FMT_Q6K> : ByCode<Unit<FMT_Q6K>> {
     }
     __device__ __forceinline__ void begin()
     {
+        hold(sc), hold(d);
         const float f = f16_bits_to_f32(d);
         S = f * (float)(int8_t)sc, S1 = f * (float)(int8_t)(sc >> 8);
     }
@@ -217,7 +228,8 @@ template <> struct Unit<FMT_Q5K> : ByValue<Unit<FMT_Q5K>> {
 
 template <> struct Unit<FMT_Q3K> : ByValue<Unit<FMT_Q3K>> {
     uint2 c;
-    uint32_t hi, s0, s2, d;
+    uint32_t hi, s0, s2;
+    uint16_t d;
     int j;
     float S, S1;
     __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
@@ -251,7 +263,8 @@ template <> struct Unit<FMT_Q3K> : ByValue<Unit<FMT_Q3K>> {
 
 template <> struct Unit<FMT_Q2K> : ByValue<Unit<FMT_Q2K>> {
     uint2 c;
-    uint32_t sm, dd;
+    uint16_t sm;
+    uint32_t dd;
     float S, T, S1, T1;
     __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
     {
@@ -300,7 +313,8 @@ template <int FMT> struct Unit : ByValue<Unit<FMT>> {
     static constexpr bool affine = FMT == FMT_Q4_1 || FMT == FMT_Q5_1;
     static_assert(FMT == FMT_Q4_0 || five || affine, "a 32-element block format");
     uint4 c;
-    uint32_t hi, d, m;
+    uint32_t hi;
+    uint16_t d, m;
     float S, T;
     __device__ __forceinline__ void load(const uint8_t *__restrict__ B, const Planes &p, int64_t b)
     {
