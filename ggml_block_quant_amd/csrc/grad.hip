@@ -52,7 +52,7 @@ __device__ __forceinline__ float block_sum(float v, float *red)
 // leave their row as it is (it is not finite then, and no other is).
 __device__ __forceinline__ int row_exponent(float v)
 {
-    if (!(v > 0.0f) || v > 3.4e38f)
+    if (!(v > 0.0f) || v > __FLT_MAX__)
         return 0;
     return 15 - __builtin_amdgcn_frexp_expf(v);
 }
@@ -107,7 +107,7 @@ __device__ __forceinline__ float size8(const float v[8], float big)
 {
 #pragma unroll
     for (int j = 0; j < 8; j++)
-        big = !(fabsf(v[j]) <= 3.4e38f) ? INFINITY : fmaxf(big, fabsf(v[j]));
+        big = !(fabsf(v[j]) <= __FLT_MAX__) ? INFINITY : fmaxf(big, fabsf(v[j]));
     return big;
 }
 
@@ -260,8 +260,9 @@ __global__ __launch_bounds__(256) void join_few_kernel(const float *__restrict__
 __device__ __forceinline__ void glu_grad(int act, float g, float u, float dh, float &dg, float &du)
 {
     if (act == 1) {
-        dg = g > 0.0f ? dh * u : 0.0f;
-        du = g > 0.0f ? dh * g : 0.0f;
+        const bool on = !(g <= 0.0f);  // (a NaN stays one)
+        dg = on ? dh * u : 0.0f;
+        du = on ? dh * g : 0.0f;
         return;
     }
     // p = sigmoid(g) and q = 1 - p without the digits that the difference would
@@ -672,11 +673,14 @@ Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
     // (192 only where it pads to no more than 256 does: padded() counts on it)
     const int first = M <= 128 ? TILE_128 : up_to(M, 192) < up_to(M, 256) ? TILE_192 : TILE_256;
     for (int tile = first; tile <= (M <= 128 ? TILE_128 : TILE_256); tile++)
-        for (int n = 1; n <= kTimedSplits; n++) {
-            const Plan p = plan_with(mode, tile, M, cols, depth, parts, n), q = with_whole(p);
+        for (const int n : {1, 2, 3, 4, 5, 6, 7, 8, 10, 12, 16, 20, 24, 32, 48, kTimedSplits}) {
+            const Plan p = plan_with(mode, tile, M, cols, depth, parts, n);
             // (a backward product's sums are joined for all columns or none)
-            for (const Plan &t : {p, q}) {
-                if (t.splits > 1 && ((t.tiles - t.whole) * t.splits > kTimedTo || (mode == BACK && t.whole > 0)))
+            const bool tail = mode != BACK && p.tiles > 256;
+            if (p.tiles * n > kTimedTo && n > 1 && !tail)
+                break;
+            for (const Plan &t : {p, tail ? with_whole(p) : p}) {
+                if (t.splits > 1 && (t.tiles - t.whole) * t.splits > kTimedTo)
                     continue;
                 const double us = plan_us(t, mode, M, cols);
                 if (best.steps == 0 || us < least)

@@ -113,6 +113,25 @@ def test_grad_range_within_a_row():
     del blocks, W
 
 
+def test_grad_largest_and_smallest_values():
+    """Gradients up to fp32's largest and down to its smallest normal."""
+    N, K = 40, 256
+    w, W = weights("q8_0", 72750, N, K)
+    blocks = ql.isq("q8_0", to_dev_bf16(w))
+    for M in (1, 3, 100):
+        dY = gradients(4, M, N).sign() * torch.rand((M, N), device="cuda", generator=torch.Generator("cuda").manual_seed(M))
+        for size in (torch.finfo(torch.float32).max, 2.0 ** -110):
+            d = dY * size
+            d[:, 0] = size
+            y, tol = back(d.double(), W)
+            got = ql.qmatmul_grad("q8_0", blocks, d, K)
+            # (a result over bf16's range is infinite; one row's products lose
+            # their last digits below 2^-126)
+            fit = y.abs() < 3.3e38
+            small = N * 2.0 ** -149
+            within(torch.where(fit, got.double(), y), y, rounded(y, tol) + small, f"{M} rows of {size}")
+
+
 def test_grad_rows_that_are_not_finite_stay_alone():
     N, K = 100, 256
     w, W = weights("q4k", 72700, N, K)
@@ -137,7 +156,7 @@ def test_grad_same_bits_and_surroundings():
     blocks = ql.isq("q6k", to_dev_bf16(w))
     big = ql.grad_workspace_bytes("q6k", 600, N, K)
     ws = torch.full((big + 256,), 255, dtype=torch.uint8, device="cuda")
-    for M in (1, 20, 33, 64, 100, 128, 255, 256, 300, 512, 600):
+    for M in (1, 2, 20, 33, 64, 100, 128, 129, 192, 193, 255, 256, 257, 300, 384, 385, 512, 576, 577, 600):
         dY = gradients(M, M, N)
         hold = torch.full((M + 2, K), 7.0, dtype=torch.bfloat16, device="cuda")
         a = ql.qmatmul_grad("q6k", blocks, dY, K, out=hold[1:M + 1], workspace=ws[:big])
@@ -300,7 +319,7 @@ def test_glu_grad_same_bits_and_surroundings():
     bg, bu = (ql.isq("q4k", to_dev_bf16(synth.weights_bf16(76000 + i, F, K))) for i in range(2))
     big = ql.glu_grad_workspace_bytes("q4k", 400, F, K)
     ws = torch.full((big + 256,), 255, dtype=torch.uint8, device="cuda")
-    for M in (1, 33, 64, 65, 128, 200, 400):
+    for M in (1, 2, 3, 33, 64, 65, 128, 192, 193, 200, 256, 385, 400):
         X = to_dev_bf16(synth.activations_bf16(76010 + M, M, K))
         dH = gradients(M, M, F)
         hold = [torch.full((M + 16, n), 7.0, dtype=torch.bfloat16, device="cuda") for n in (K, F, F)]
@@ -315,19 +334,29 @@ def test_glu_grad_same_bits_and_surroundings():
             assert (h[:8] == 7).all() and (h[M + 8:] == 7).all()
 
 
-def test_glu_grad_rows_that_are_not_finite_stay_alone():
-    F, K, M = 100, 256, 40
-    bg, bu = (ql.isq("q8_0", to_dev_bf16(synth.weights_bf16(76100 + i, F, K))) for i in range(2))
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("M,x,h", ((40, 3, 9), (130, 128, 0), (2, 1, None), (2, None, 0), (1, 0, None), (1, None, 0)))
+def test_glu_grad_rows_that_are_not_finite_stay_alone(fmt, act, M, x, h):
+    """A NaN in row x of X, an infinity in row h of dH."""
+    F, K = 100, 256
+    bg, bu = (ql.isq(fmt, to_dev_bf16(synth.weights_bf16(76100 + i, F, K))) for i in range(2))
     X = to_dev_bf16(synth.activations_bf16(76110, M, K))
     dH = gradients(1, M, F)
-    clean = ql.qmatmul_glu_grad("q8_0", bg, bu, X, dH, parts=True)
+    clean = ql.qmatmul_glu_grad(fmt, bg, bu, X, dH, act=act, parts=True)
     Xb, db = X.clone(), dH.clone()
-    Xb[3, 7], db[9, 2] = float("nan"), float("inf")
-    got = ql.qmatmul_glu_grad("q8_0", bg, bu, Xb, db, parts=True)
-    keep = [m for m in range(M) if m not in (3, 9)]
+    if x is not None:
+        Xb[x, 7] = float("nan")
+    if h is not None:
+        db[h, 2] = float("inf")
+    got = ql.qmatmul_glu_grad(fmt, bg, bu, Xb, db, act=act, parts=True)
+    keep = [m for m in range(M) if m not in (x, h)]
     for a, b in zip(got, clean):
         assert torch.equal(a[keep], b[keep])
-    assert not torch.isfinite(got.dX[3]).any() and not torch.isfinite(got.dX[9]).any()
+    if x is not None:
+        assert not torch.isfinite(got.dX[x]).any()
+    if h is not None and act != "relu":  # (a gate that ReLU holds shut takes no gradient)
+        assert not torch.isfinite(got.dX[h]).any()
 
 
 # ---------------------------------------------------------------------------

@@ -153,18 +153,22 @@ def test_loss_alone_and_given_results():
     assert got is out and torch.equal(got.loss, full.loss) and torch.equal(got.dX, full.dX)
 
 
-def test_rows_that_are_not_finite_stay_alone():
-    M, N, K = 40, 300, 256
-    X, W, b, t = case("q4k", M, N, K)
-    clean = ql.qmatmul_xent("q4k", b, X, N, t)
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,rows", ((40, (2, 30)), (130, (2, 129)), (2, (1,)), (2, (0,)), (1, (0,))))
+def test_rows_that_are_not_finite_stay_alone(fmt, M, rows):
+    N, K = 300, 256
+    X, W, b, t = case(fmt, M, N, K)
+    clean = ql.qmatmul_xent(fmt, b, X, N, t)
     bad = X.clone()
-    bad[2, 5], bad[30, 0] = float("nan"), float("inf")
-    got = ql.qmatmul_xent("q4k", b, bad, N, t)
-    keep = [m for m in range(M) if m not in (2, 30)]
+    for i, m in enumerate(rows):
+        bad[m, 5 * i] = float("inf") if i else float("nan")
+    got = ql.qmatmul_xent(fmt, b, bad, N, t)
+    keep = [m for m in range(M) if m not in rows]
     for a, c in zip(got, clean):
         assert torch.equal(a[keep], c[keep])
-    assert not torch.isfinite(got.loss[[2, 30]]).any() and not torch.isfinite(got.lse[[2, 30]]).any()
-    assert not torch.isfinite(got.dX[[2, 30]]).any()
+    rows = list(rows)
+    assert not torch.isfinite(got.loss[rows]).any() and not torch.isfinite(got.lse[rows]).any()
+    assert not torch.isfinite(got.dX[rows]).any()
 
 
 def test_same_bits_and_surroundings():
@@ -173,7 +177,7 @@ def test_same_bits_and_surroundings():
     b = ql.isq("q4k", to_dev_bf16(w))
     big = ql.xent_workspace_bytes("q4k", 500, N, K)
     ws = torch.full((big + 256,), 255, dtype=torch.uint8, device="cuda")
-    for M in (1, 2, 31, 33, 64, 65, 128, 129, 300, 500):
+    for M in (1, 2, 3, 31, 33, 64, 65, 128, 129, 192, 193, 256, 257, 300, 384, 385, 500):
         X = to_dev_bf16(synth.activations_bf16(83100 + M, M, K))
         t = torch.arange(M, dtype=torch.int32, device="cuda")
         hold = [torch.full((M + 2,), 7.0, device="cuda"), torch.full((M + 2,), 7.0, device="cuda"),
