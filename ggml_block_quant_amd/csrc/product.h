@@ -151,14 +151,13 @@ struct Tile {
     static constexpr int BUF = ABYTES + WBYTES;
     static constexpr int UNITS = MODE == BACK ? 64 * 8 : 256 * BK / 32;
     static constexpr int UPT = UNITS / NT, TASKS = 4 * UPT;  // units a thread, tasks of eight weights
-    // Up to 32 rows of A a step's products are short against the memory's
-    // latency: what is on its way has to be several steps.  A then comes
-    // through registers as W does, and the compiler's own waits let every set
-    // but the one it needs stay on its way (a wait for direct loads to LDS is
-    // one for everything asked for before it).  131072 x 5120 Q6K: 170 -> 149
-    // us; with 37 rows of 4096 x 14336 the direct loads win, 26.5 against 33.
+    // Up to 32 rows of A, A comes through registers as W does: the compiler's
+    // own waits then let every set but the one it needs stay on its way (a wait
+    // for direct loads to LDS is one for everything asked for before it).  131072
+    // x 5120 Q6K, 32 rows: 170 -> 149 us; with 64 rows it makes no difference.
+    // Two sets: 30 rows of 14336 x 4096 Q8_0 21.5 us, one 22.0, four 23.1.
     static constexpr bool AREG = TM <= 32;
-    static constexpr int DEPTH = AREG ? 4 : 2;
+    static constexpr int DEPTH = 2;
     // 16-byte pieces of A a thread (where there are fewer than threads, two
     // threads bring the same one)
     static constexpr int PIECES = ABYTES / 16, APT = AREG ? (PIECES + NT - 1) / NT : 1;

@@ -359,8 +359,10 @@ int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M,
  * not depend on the order in which workgroups run.
  * workspace: device, qmatmul_grad_workspace_bytes() bytes, 16-byte aligned,
  * overwritten (nothing in it needs to start at zero); the size for M rows also
- * serves fewer.  Calls that can overlap in time need one each.  M == 0 launches
- * nothing; 0 <= M <= QLINEAR_MAX_M. */
+ * serves fewer.  Calls that can overlap in time need one each.  Results,
+ * inputs and workspace do not overlap.  M == 0 launches nothing; 0 <= M <=
+ * QLINEAR_MAX_M.  One row is computed in fp32 throughout (its products lose
+ * digits below 2^-126). */
 enum { QTYPE_F32 = 0, QTYPE_BF16 = 1 };
 size_t qmatmul_grad_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K);
 int qmatmul_grad(int fmt, const void *blocks, const void *dY, int dy_type, void *dX_bf16, int64_t M, int64_t N,
@@ -377,7 +379,7 @@ int qmatmul_grad(int fmt, const void *blocks, const void *dY, int dy_type, void 
  * adapters need.  act as in qmatmul_glu; ReLU's derivative at 0 is 0.
  * G and U are fp32 sums with the weights in fp16 and X as it is (down to 2^-31
  * of its row's largest), so each is within 2^-11 + K * 2^-23 of its magnitudes
- * summed; dX adds up dG and dU before their rounding to bf16, as fp16 times one
+ * summed (one or two rows: qmatmul's GEMV, with its accuracy); dX adds up dG and dU before their rounding to bf16, as fp16 times one
  * power of two for both rows (2^-11 of the value, and 2^-39 of the larger of
  * the two rows' largest).  The rest as in
  * qmatmul_grad. */
@@ -398,7 +400,7 @@ int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, co
  * lse: device fp32 [M] or NULL.  dX_bf16: device [M][K] bf16, or NULL (the loss
  * alone).  targets, weights, loss and lse 4-byte aligned.
  * The logits take each weight as a pair of fp16 (2^-22 of the weight) and sums
- * in fp32; 1 - p of the given token is formed as the others' share, so neither
+ * in fp32 (one or two rows: qmatmul's GEMV, with its accuracy); 1 - p of the given token is formed as the others' share, so neither
  * a loss nor a gradient near 0 is a difference of nearly equal numbers.  The
  * gradient's product is held as in qmatmul_grad, with p - [n = t] in place of
  * dY.  Rows go through in chunks of at most 2^26 logits (or 32 rows), which
