@@ -7,6 +7,7 @@
 #include "product.h"
 
 #include <initializer_list>
+#include <type_traits>
 
 namespace ql {
 
@@ -85,6 +86,32 @@ template <bool VEC> __device__ __forceinline__ void load8(const uint16_t *row, i
         for (int j = 0; j < 8; j++)
             v[j] = i + j < n ? __builtin_bit_cast(float, (uint32_t)row[i + j] << 16) : 0.0f;
     }
+}
+// v += the same of `more` further rows, `apart` values from one to the next, in
+// their order.  Four are asked for together (14 splits of 85 rows of 802 values,
+// the gated pair: 19 us one after the other, now 10).
+template <bool VEC>
+__device__ __forceinline__ void add8(const float *row, int64_t apart, int more, int64_t i, int64_t n, float v[8])
+{
+    auto take = [&](auto count) {
+        constexpr int C = decltype(count)::value;
+        float t[C][8];
+#pragma unroll
+        for (int s = 0; s < C; s++)
+            load8<VEC>(row + s * apart, i, n, t[s]);
+#pragma unroll
+        for (int s = 0; s < C; s++)
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                v[j] += t[s][j];
+        row += C * apart;
+    };
+    for (; more >= 4; more -= 4)
+        take(std::integral_constant<int, 4>{});
+    if (more & 2)
+        take(std::integral_constant<int, 2>{});
+    if (more & 1)
+        take(std::integral_constant<int, 1>{});
 }
 template <bool VEC> __device__ __forceinline__ void store8(uint16_t *row, int64_t i, int64_t n, const float v[8])
 {
@@ -239,12 +266,7 @@ __global__ __launch_bounds__(256) void join_few_kernel(const float *__restrict__
     if (k >= K)
         return;
     float v[8] = {};
-    for (int s = 0; s < splits; s++) {
-        const float4 *p = reinterpret_cast<const float4 *>(part + ((int64_t)s * M + m) * K + k);
-        const float4 a = p[0], b = p[1];
-        v[0] += a.x, v[1] += a.y, v[2] += a.z, v[3] += a.w;
-        v[4] += b.x, v[5] += b.y, v[6] += b.z, v[7] += b.w;
-    }
+    add8<true>(part + m * K, M * K, splits, k, K, v);
     const int x = e ? -e[m] : 0;
     const float f = w ? w[m] : 1.0f;
 #pragma unroll
@@ -282,6 +304,7 @@ struct GluRows {
     const float *g, *u;  // sums of the rows, the first split: row m at m ld
     const float *mg, *mu;  // the others, from column `from` on: row m of split s at ((s - 1) M + m) more_ld - from
     int splits, act;
+    bool whole;          // whether the sums' rows have room for whole groups of eight, 16-byte aligned
     int64_t more_ld, from;
     int64_t M, F, Mp, ld;
     const int *ex;       // exponents of X's rows, or null
@@ -299,21 +322,19 @@ __device__ __forceinline__ void glu_values(const GluRows &a, int64_t m, int64_t 
 {
     const int64_t F = a.F;
     const int x = a.ex ? -a.ex[m] : 0;
-    float g[8], u[8], h[8], t[8];
-    load8<VEC>(a.g + m * a.ld, 8 * c, F, g);
-    load8<VEC>(a.u + m * a.ld, 8 * c, F, u);
-    const int splits = 8 * c < a.from ? 1 : a.splits;
-    for (int s = 1; s < splits; s++) {
-        const int64_t at = ((int64_t)(s - 1) * a.M + m) * a.more_ld - a.from;
-        load8<VEC>(a.mg + at, 8 * c, F, t);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            g[j] += t[j];
-        load8<VEC>(a.mu + at, 8 * c, F, t);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            u[j] += t[j];
-    }
+    float g[8], u[8], h[8];
+    const int more = 8 * c < a.from ? 0 : a.splits - 1;
+    auto sums = [&](auto whole) {
+        constexpr bool V8 = decltype(whole)::value;
+        load8<V8>(a.g + m * a.ld, 8 * c, F, g);
+        load8<V8>(a.u + m * a.ld, 8 * c, F, u);
+        add8<V8>(a.mg + m * a.more_ld - a.from, a.M * a.more_ld, more, 8 * c, F, g);
+        add8<V8>(a.mu + m * a.more_ld - a.from, a.M * a.more_ld, more, 8 * c, F, u);
+    };
+    if (VEC || a.whole)
+        sums(std::true_type{});
+    else
+        sums(std::false_type{});
     load8<VEC>(static_cast<const V *>(a.dH) + m * F, 8 * c, F, h);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
@@ -455,13 +476,7 @@ __device__ __forceinline__ float logit(const XentRows &a, int64_t m, int64_t n, 
 template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, int64_t m, int64_t c, int x, float z[8])
 {
     load8<VEC>(a.part + m * a.ld, 8 * c, a.N, z);
-    for (int s = 1; s < (8 * c < a.from ? 1 : a.splits); s++) {
-        float t[8];
-        load8<VEC>(a.more + ((int64_t)(s - 1) * a.M + m) * a.more_ld - a.from, 8 * c, a.N, t);
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            z[j] += t[j];
-    }
+    add8<VEC>(a.more + m * a.more_ld - a.from, a.M * a.more_ld, 8 * c < a.from ? 0 : a.splits - 1, 8 * c, a.N, z);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         z[j] = __builtin_ldexpf(z[j], x);
@@ -769,7 +784,7 @@ struct Pieces {
 
 hipError_t run_join(const float *part, const int *e, const float *w, int splits, int64_t M, int64_t K, uint16_t *dX, hipStream_t s)
 {
-    // (48 splits of one row: 4 us against 11; 2 of 2048 rows: 13 against 19)
+    // (48 splits of one row: 4 us against 11)
     if (splits >= 16)
         join_kernel<<<dim3((unsigned)((K + 63) / 64), (unsigned)M), 256, 0, s>>>(part, e, w, splits, M, K, dX);
     else
@@ -895,7 +910,7 @@ int64_t glu_grad_workspace(int fmt, int64_t M, int64_t F, int64_t K)
     w.take(2 * panels_bytes(padded(R), F));
     w.take(4 * R);
     w.take(4 * R);
-    w.take(fore_part_bytes(R, 2 * F));
+    w.take(fore_part_bytes(R, 2 * up_to(F, 8)));
     w.take(back_part_bytes(R, K));
     return w.used;
 }
@@ -908,7 +923,7 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
     uint8_t *AX = w.take(panels_bytes(padded(R), a.K));
     uint8_t *AD = w.take(2 * panels_bytes(padded(R), a.F));
     int *ex = reinterpret_cast<int *>(w.take(4 * R)), *ed = reinterpret_cast<int *>(w.take(4 * R));
-    float *gu = reinterpret_cast<float *>(w.take(fore_part_bytes(R, 2 * a.F)));
+    float *gu = reinterpret_cast<float *>(w.take(fore_part_bytes(R, 2 * up_to(a.F, 8))));
     float *part = reinterpret_cast<float *>(w.take(back_part_bytes(R, a.K)));
     for (int64_t m = 0; m < a.M; m += R) {
         const int64_t n = a.M - m < R ? a.M - m : R;
@@ -932,11 +947,12 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
             err = run_rows<64>(a.X + m * a.K, n, a.K, up_to(a.K, p.f.step), p.Mp, AX, ex, nullptr, s);
             if (err != hipSuccess)
                 return err;
+            const int64_t wide = up_to(a.F, 8);
             ProductArgs g{};
-            g.W0 = a.gate, g.W1 = a.up, g.p = pl, g.A = AX, g.part = gu, g.M = n, g.ld = 2 * a.F, g.rows = a.F, g.K = a.K;
-            r.from = g.from = p.split_from(), r.more_ld = g.more_ld = 2 * (a.F - g.from), g.more = gu + n * g.ld;
+            g.W0 = a.gate, g.W1 = a.up, g.p = pl, g.A = AX, g.part = gu, g.M = n, g.ld = 2 * wide, g.rows = a.F, g.K = a.K;
+            r.from = g.from = p.split_from(), r.more_ld = g.more_ld = 2 * (wide - g.from), g.more = gu + n * g.ld;
             err = launch_product(a.fmt, FORE_GLU, p, g, s);
-            r.g = gu, r.u = gu + a.F, r.ld = 2 * a.F, r.mg = g.more, r.mu = g.more + g.more_ld / 2;
+            r.g = gu, r.u = gu + wide, r.ld = 2 * wide, r.whole = true, r.mg = g.more, r.mu = g.more + g.more_ld / 2;
             r.splits = p.splits, r.ex = ex, r.raw = true;
         }
         if (err != hipSuccess)
