@@ -681,7 +681,12 @@ Plan plan_of(int mode, int64_t M, int64_t cols, int64_t depth, int parts)
     if (M <= 64) {
         const int tile = M <= 32 ? TILE_32 : TILE_64;
         const Form f = form_of(mode, tile);
-        return plan_with(mode, tile, M, cols, depth, parts, kSplitTo / ((cols + f.cols - 1) / f.cols));
+        int64_t n = kSplitTo / ((cols + f.cols - 1) / f.cols);
+        // (a forward split takes four steps or more: gate and up of
+        // 50 x 1408 of 2048 in eighths 11.4 us, in quarters 10.1)
+        if (mode != BACK && n > depth / f.step / 4)
+            n = depth / f.step / 4;
+        return plan_with(mode, tile, M, cols, depth, parts, n);
     }
     Plan best{};
     double least = 0.0;
@@ -855,7 +860,7 @@ int64_t fore_part_bytes(int64_t M, int64_t width)
 
 // Up to two rows the forward products are matrix-vector products: the GEMV
 // takes the weights exactly and sums in fp32 (131072 x 5120 Q6K, one and two
-// rows: 99 and 148 us; tiles of 32 rows 270; three rows 336).
+// rows: 93 and 141 us, tiles of 32 rows 237; its three rows 334).
 constexpr int64_t kGemvRows = 2;
 
 }  // namespace

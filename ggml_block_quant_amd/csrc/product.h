@@ -451,26 +451,30 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
 // The forward product of few rows
 // ---------------------------------------------------------------------------
 
-// Up to 128 rows of A: the weights' bytes are what it costs, so a workgroup
+// Up to 64 rows of A: the weights' bytes are what it costs, so a workgroup
 // takes 64 rows of W (FORE_GLU: 32 of the gate, 32 of the up projection) and
-// 128 of K a step, which its lanes read as runs of a row (in the tiles above
-// every lane reads another row, 32 or 64 elements at a time: at one row of A
-// that fetched each line of the head several times, 1090 us).  Four waves: two
-// column tiles times the two halves of a step's K, whose sums meet in LDS at
-// the end.  The bytes on their way stand in registers as in product_kernel.
+// 128 of K a step.  Four waves: two column tiles times the two halves of a
+// step's K, whose sums meet in LDS at the end.  A lane decodes a unit of its own
+// row of W, eight weights a product, straight into the product's operand: the
+// order of K within a step is free as long as A's is the same, so the lanes
+// 0 .. 31 of a wave take one unit of the row and 32 .. 63 the next, and W never
+// passes through LDS.  Bound by the decode's instructions: of 131072 x 5120 Q6K
+// pairs of 3 rows 237 us (2.3 TB/s) and of 64 rows 285, with W through LDS 267
+// and 399.  Two steps on their way, so that three workgroups fit a CU (two of
+// 64 rows); with four, 40 x 32000 of 4096 Q4K took 63 us against 47.
 template <int MODE, int MI> struct Thin {
     static constexpr int TM = 32 * MI, BK = 128, NT = 256;
     static constexpr int P = MODE == FORE_PAIR ? 2 : 1;
-    static constexpr int ABYTES = TM * BK * 2, WPLANE = 64 * BK * 2, BUF = ABYTES + P * WPLANE;
-    static constexpr int DEPTH = 4, APT = ABYTES / 16 / NT;
+    static constexpr int ABYTES = TM * BK * 2, SUMS = 2 * MI * 16 * 64 * 4;
+    static constexpr int LDS = 2 * ABYTES > SUMS ? 2 * ABYTES : SUMS;
+    static constexpr int DEPTH = 2, APT = ABYTES / 16 / NT;
 };
 
 template <int FMT, int MODE, int MI>
-__global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
+__global__ __launch_bounds__(256, MI == 1 ? 3 : 2) void thin_kernel(ProductArgs a)
 {
     using T = Thin<MODE, MI>;
-    constexpr int P = T::P, NP = 4 * P;  // a wave's products of a step: four of 16, of each hi and lo
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * T::BUF];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[T::LDS];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int col = wave & 1, kh = wave >> 1;
@@ -480,14 +484,14 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
     const int64_t m0 = at.m0;
     const int s0 = at.s0, s1 = at.s1;
 
-    // W: unit tid % 4 of the step, row tid / 4 of the tile
+    // W: unit 2 kh + half of the step, row r32 of the wave's tile
     const uint32_t upr = (uint32_t)(a.K / 32);
-    const int rows = (int)a.rows, wr = tid >> 2, wc = tid & 3;
-    const int first = MODE == FORE_GLU ? (int)ct * 32 + (wr & 31) : (int)ct * 64 + wr;
+    const int rows = (int)a.rows, wc = 2 * kh + half;
+    const int first = (MODE == FORE_GLU ? (int)ct * 32 : (int)ct * 64 + col * 32) + r32;
     const uint64_t row0 = (uint64_t)(uint32_t)min(first, rows - 1) * upr;
-    const uint8_t *const W = MODE == FORE_GLU && wr >= 32 ? a.W1 : a.W0;
-    // a step's bytes on their way: the unit, and this thread's pieces of A's two
-    // panels of 64 columns
+    const uint8_t *const W = MODE == FORE_GLU && col ? a.W1 : a.W0;
+    // bytes on their way: the unit of a step, and this thread's pieces of A's
+    // two panels of 64 columns for the step behind it
     struct Set {
         Unit<FMT> u;
         u32x4 a[T::APT];
@@ -495,35 +499,22 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
     Set set[T::DEPTH];
     const int64_t panel = a.Mp * 128;
     const uint8_t *const Abase = a.A + m0 * 128;
-    auto load_set = [&](int s, Set &t) {
+    auto load_a = [&](int s, Set &t) {
 #pragma unroll
         for (int i = 0; i < T::APT; i++) {
             const int at = 16 * (tid + i * T::NT);
             t.a[i] = *reinterpret_cast<const u32x4 *>(Abase + (2 * s + at / (T::TM * 128)) * panel + at % (T::TM * 128));
         }
-        t.u.load(W, a.p, (int64_t)(row0 + min((uint32_t)(s * 4 + wc), upr - 1)));
     };
     auto store_a_regs = [&](const Set &t, int buf) {
 #pragma unroll
         for (int i = 0; i < T::APT; i++)
-            *reinterpret_cast<u32x4 *>(smem + buf * T::BUF + 16 * (tid + i * T::NT)) = t.a[i];
+            *reinterpret_cast<u32x4 *>(smem + buf * T::ABYTES + 16 * (tid + i * T::NT)) = t.a[i];
     };
-    // chunk c of row r of a tile of W: 16 rows' same chunk on all banks, and a
-    // row's units' same task on banks of their own
-    auto w_at = [&](int r, int c) { return r * 256 + 16 * ((4 * (c >> 2) + ((c & 3) ^ (c >> 2))) ^ (r & 15)); };
-    auto store_w = [&](Unit<FMT> &u, int t, int buf) {
-        if (t == 0)
-            u.begin();
-        uint8_t *const at = smem + buf * T::BUF + T::ABYTES + w_at(wr, 4 * wc + t);
-        uint32_t h[4];
-        if constexpr (MODE == FORE_PAIR) {
-            uint32_t l[4];
-            u.pairs(t, h, l);
-            *reinterpret_cast<uint4 *>(at + T::WPLANE) = make_uint4(l[0], l[1], l[2], l[3]);
-        } else {
-            u.halves(t, h);
-        }
-        *reinterpret_cast<uint4 *>(at) = make_uint4(h[0], h[1], h[2], h[3]);
+    const int last = s1 - 1;
+    auto load_set = [&](int s, Set &t) {
+        load_a(min(s + 1, last), t);
+        t.u.load(W, a.p, (int64_t)(row0 + min((uint32_t)(min(s, last) * 4 + wc), upr - 1)));
     };
 
     f32x16 acc[MI];
@@ -532,77 +523,62 @@ __global__ __launch_bounds__(256) void thin_kernel(ProductArgs a)
 #pragma unroll
         for (int r = 0; r < 16; r++)
             acc[i][r] = 0.0f;
-    // all fragments of a step (columns 16 kk of the wave's half), read before
-    // anything else of it: the decode of the next step hides their way
-    f16x8 af[4][MI], wf[NP];
-    auto read_all = [&](int from) {
-        const uint8_t *const b = smem + from * T::BUF;
-#pragma unroll
-        for (int x = 0; x < NP; x++) {
-            const int kk = x / P;
-            wf[x] = *reinterpret_cast<const f16x8 *>(b + T::ABYTES + (x % P) * T::WPLANE +
-                                                     w_at(col * 32 + r32, 8 * kh + 2 * kk + half));
-            if (x % P == 0)
-#pragma unroll
-                for (int i = 0; i < MI; i++) {
-                    const int row = 32 * i + r32;
-                    af[kk][i] = *reinterpret_cast<const f16x8 *>(b + kh * (T::TM * 128) + row * 128 +
-                                                                 16 * a_chunk<64>(row, 2 * kk + half));
-                }
-        }
-        if constexpr (P == 1 && MI == 1)  // (one token of 2 x 14336 x 4096 Q4K 37.8 -> 29.3 us; with more to read it costs)
-            __builtin_amdgcn_sched_barrier(0);
-    };
-    auto products = [&]() {
-#pragma unroll
-        for (int x = 0; x < NP; x++)
-#pragma unroll
-            for (int i = 0; i < MI; i++)
-                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[x / P][i], wf[x], acc[i], 0, 0, 0);
-    };
     int buf = 0;
-    const int last = s1 - 1;
     auto step = [&](int s, Set &t) {
-        read_all(buf);
-        store_a_regs(t, buf ^ 1);
+        // all of A's fragments, then the decode hides their way
+        f16x8 af[4][MI];
 #pragma unroll
         for (int x = 0; x < 4; x++)
-            store_w(t.u, x, buf ^ 1);
-        load_set(min(s + 1 + T::DEPTH, last), t);
-        products();
+#pragma unroll
+            for (int i = 0; i < MI; i++) {
+                const int row = 32 * i + r32;
+                af[x][i] = *reinterpret_cast<const f16x8 *>(smem + buf * T::ABYTES + kh * (T::TM * 128) + row * 128 +
+                                                            16 * a_chunk<64>(row, 4 * half + x));
+            }
+        store_a_regs(t, buf ^ 1);
+        t.u.begin();
+#pragma unroll
+        for (int x = 0; x < 4; x++) {
+            uint32_t h[4], l[4];
+            if constexpr (MODE == FORE_PAIR)
+                t.u.pairs(x, h, l);
+            else
+                t.u.halves(x, h);
+#pragma unroll
+            for (int i = 0; i < MI; i++) {
+                acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[x][i], __builtin_bit_cast(f16x8, h), acc[i], 0, 0, 0);
+                if constexpr (MODE == FORE_PAIR)
+                    acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(af[x][i], __builtin_bit_cast(f16x8, l), acc[i], 0, 0, 0);
+            }
+        }
+        load_set(s + T::DEPTH, t);
         lds_barrier();
         buf ^= 1;
     };
     if (s0 < s1) {
         Set head;
-        load_set(s0, head);
+        load_a(s0, head);
 #pragma unroll
         for (int i = 0; i < T::DEPTH; i++) {
             __builtin_amdgcn_sched_barrier(0);  // in this order, which the loop's waits count on
-            load_set(min(s0 + 1 + i, last), set[i]);
+            load_set(s0 + i, set[i]);
         }
         __builtin_amdgcn_sched_barrier(0);
         store_a_regs(head, 0);
-#pragma unroll
-        for (int t = 0; t < 4; t++)
-            store_w(head.u, t, 0);
         lds_barrier();
         int s = s0;
-        for (; s + T::DEPTH <= last; s += T::DEPTH)
+        for (; s + T::DEPTH <= s1; s += T::DEPTH)
 #pragma unroll
             for (int i = 0; i < T::DEPTH; i++)
                 step(s + i, set[i]);
 #pragma unroll
         for (int i = 0; i + 1 < T::DEPTH; i++)
-            if (s + i < last)
+            if (s + i < s1)
                 step(s + i, set[i]);
-        read_all(buf);
-        products();
     }
     // the halves of K meet: 64 lanes' values of a register stand together
     __syncthreads();
     float *const sum = reinterpret_cast<float *>(smem) + col * (MI * 16 * 64) + lane;
-    static_assert(2 * MI * 16 * 64 * 4 <= 2 * T::BUF, "room for the halves' sums");
     if (kh == 1)
 #pragma unroll
         for (int i = 0; i < MI; i++)

@@ -48,8 +48,14 @@ __device__ __forceinline__ uint32_t scale_codes(uint32_t codes, float s, float t
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t &hi, uint32_t &lo)
 {
     hi = pack_f16(a, b);
+    // (hi as it stands, and a factor that the compiler does not know to be -1:
+    // it makes hi twice and three instructions of a difference otherwise, and
+    // from this one mixed multiply-add a value)
+    float minus = -1.0f;
+    asm("" : "+s"(minus));
+    asm("" : "+v"(hi));
     const f16x2 p = __builtin_bit_cast(f16x2, hi);
-    lo = __builtin_bit_cast(uint32_t, f16x2{(_Float16)fmaf((float)p.x, -1.0f, a), (_Float16)fmaf((float)p.y, -1.0f, b)});
+    lo = __builtin_bit_cast(uint32_t, f16x2{(_Float16)fmaf((float)p.x, minus, a), (_Float16)fmaf((float)p.y, minus, b)});
 }
 
 // Through fp32: units that give values (decode)
