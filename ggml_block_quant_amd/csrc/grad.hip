@@ -860,8 +860,17 @@ int64_t fore_part_bytes(int64_t M, int64_t width)
 
 // Up to two rows the forward products are matrix-vector products: the GEMV
 // takes the weights exactly and sums in fp32 (131072 x 5120 Q6K, one and two
-// rows: 93 and 141 us, tiles of 32 rows 237; its three rows 334).
-constexpr int64_t kGemvRows = 2;
+// rows: 93 and 141 us, tiles of 32 rows 237).  So are three rows, and four of
+// the cross entropy's pairs, where its one-shot kernel takes them (32000 x 4096,
+// pairs, tiles against GEMV: Q4K 43 and 23, four 43 and 31; Q6K 51 and 39, four
+// 51 and 48; Q8_0 43 and 31, four 43 and 37; the gated pair's three 57 and 45,
+// 85 and 79, 87 and 62, but Q6K's four 85 and 96), but for Q6K and Q8_0 at three
+// chunks of 64 units a row, where it is slow (32000 x 5120, three rows: Q6K 58
+// and 96, Q8_0 52 and 71).
+bool gemv_takes(int fmt, int64_t M, int64_t K, int64_t most)
+{
+    return M <= 2 || (M <= most && gemv_one_shot_fits(fmt, (int)M, K) && (fmt == FMT_Q4K || (K / 32 + 63) / 64 != 3));
+}
 
 }  // namespace
 
@@ -940,7 +949,7 @@ hipError_t launch_glu_grad(const GluGradArgs &a, hipStream_t s)
                          : (const void *)(static_cast<const float *>(a.dH) + m * a.F);
         r.A = AD, r.e_out = ed, r.dG = a.dG ? a.dG + m * a.F : nullptr, r.dU = a.dU ? a.dU + m * a.F : nullptr;
         hipError_t err = hipErrorNotSupported;
-        if (n <= kGemvRows) {
+        if (gemv_takes(a.fmt, n, a.K, 3)) {
             float *u = gu + up_to(n * a.F, 64);
             r.g = gu, r.u = u, r.ld = a.F;
             err = launch_gemv(a.fmt, a.gate, a.X + m * a.K, gu, (int)n, a.F, a.K, s);
@@ -1062,7 +1071,7 @@ hipError_t launch_xent(const XentArgs &a, hipStream_t s)
             r.A = AD;
         r.loss = a.loss + m, r.lse = a.lse ? a.lse + m : nullptr;
         hipError_t err = hipErrorNotSupported;
-        if (n <= kGemvRows)
+        if (gemv_takes(a.fmt, n, a.K, 4))
             err = launch_gemv(a.fmt, a.W, X, z, (int)n, a.N, a.K, s);
         if (err == hipErrorNotSupported) {
             const Plan p = plan_of(FORE_PAIR, n, a.N, a.K, 1);

@@ -379,10 +379,10 @@ int qmatmul_grad(int fmt, const void *blocks, const void *dY, int dy_type, void 
  * adapters need.  act as in qmatmul_glu; ReLU's derivative at 0 is 0.
  * G and U are fp32 sums with the weights in fp16 and X as it is (down to 2^-31
  * of its row's largest), so each is within 2^-11 + K * 2^-23 of its magnitudes
- * summed (one or two rows: qmatmul's GEMV, with its accuracy); dX adds up dG and dU before their rounding to bf16, as fp16 times one
- * power of two for both rows (2^-11 of the value, and 2^-39 of the larger of
- * the two rows' largest).  The rest as in
- * qmatmul_grad. */
+ * summed (up to three rows: qmatmul's GEMV, with its accuracy, where that is
+ * the faster); dX adds up dG and dU before their rounding to bf16, as fp16
+ * times one power of two for both rows (2^-11 of the value, and 2^-39 of the
+ * larger of the two rows' largest).  The rest as in qmatmul_grad. */
 size_t qmatmul_glu_grad_workspace_bytes(int fmt, int64_t M, int64_t F, int64_t K);
 int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, const void *X_bf16, const void *dH,
                      int dh_type, void *dX_bf16, void *dG_bf16, void *dU_bf16, int64_t M, int64_t F, int64_t K, int act,
@@ -400,9 +400,10 @@ int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, co
  * lse: device fp32 [M] or NULL.  dX_bf16: device [M][K] bf16, or NULL (the loss
  * alone).  targets, weights, loss and lse 4-byte aligned.
  * The logits take each weight as a pair of fp16 (2^-22 of the weight) and sums
- * in fp32 (one or two rows: qmatmul's GEMV, with its accuracy); 1 - p of the given token is formed as the others' share, so neither
- * a loss nor a gradient near 0 is a difference of nearly equal numbers.  The
- * gradient's product is held as in qmatmul_grad, with p - [n = t] in place of
+ * in fp32 (up to four rows: qmatmul's GEMV, with its accuracy, where that is
+ * the faster); 1 - p of the given token is formed as the others' share, so
+ * neither a loss nor a gradient near 0 is a difference of nearly equal numbers.
+ * The gradient's product is held as in qmatmul_grad, with p - [n = t] in place of
  * dY.  Rows go through in chunks of at most 2^26 logits (or 32 rows), which
  * stay in the workspace.  A row of X that is not finite makes its own loss, lse
  * and dX not finite.  workspace: qmatmul_xent_workspace_bytes() (grad: whether

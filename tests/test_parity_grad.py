@@ -261,6 +261,13 @@ def test_glu_grad_sizes(fmt, M, F, K):
     check_glu(fmt, M, F, K, "silu", torch.float32 if M % 2 else torch.bfloat16, parts=F % 2 == 0, empty=(M - 1,) if M > 1 else ())
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,F,K", ((3, 333, 4096), (4, 331, 4096), (3, 100, 5120), (3, 65, 8192), (20, 700, 4096), (85, 802, 1792)))
+def test_glu_grad_few_rows(fmt, M, F, K):
+    """Either side of where the first products change their form; splits of odd rows."""
+    check_glu(fmt, M, F, K, "silu", parts=F % 2 == 1, empty=(M - 1,))
+
+
 @pytest.mark.parametrize("M,F,K", ((3, 50, 32), (70, 100, 1056), (140, 33, 224)))
 def test_glu_grad_rows_of_whole_blocks(M, F, K):
     check_glu("q8_0", M, F, K, "silu")

@@ -84,6 +84,15 @@ def test_small_and_long_vocabularies(M, N, K):
     check("q4k", X, W, b, t, label=f"{M}x{N}x{K}")
 
 
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M,N,K", ((2, 333, 4096), (3, 333, 4096), (4, 331, 4096), (3, 200, 5120), (4, 201, 5120), (3, 97, 8192),
+                                   (4, 97, 8192), (5, 97, 4096), (20, 1000, 4096), (50, 501, 5120)))
+def test_few_rows_of_wide_heads(fmt, M, N, K):
+    """Either side of where the logits' product changes its form."""
+    X, W, b, t = case(fmt, M, N, K)
+    check(fmt, X, W, b, t, label=f"{fmt} {M}x{N}x{K}")
+
+
 @pytest.mark.parametrize("M,N,K", ((3, 100, 32), (50, 301, 1056), (129, 77, 224)))
 def test_rows_of_whole_blocks(M, N, K):
     X, W, b, t = case("q8_0", M, N, K)
