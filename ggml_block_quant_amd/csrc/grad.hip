@@ -59,12 +59,21 @@ __device__ __forceinline__ int row_exponent(float v)
 }
 
 // Eight neighbouring values of a row of n from i on, zeros behind its end.
-// VEC: rows of whole groups of eight, 16-byte aligned.
+// VEC: rows of whole groups of eight, 16-byte aligned.  Others are as wide
+// loads and stores, at whatever address their rows start (one value at a time,
+// the gated pair's pass over 2 rows of 9330 took 23 us, so 15), but for the last
+// group.
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
 template <bool VEC> __device__ __forceinline__ void load8(const float *row, int64_t i, int64_t n, float v[8])
 {
-    if constexpr (VEC) {
-        const float4 a = *reinterpret_cast<const float4 *>(row + i), b = *reinterpret_cast<const float4 *>(row + i + 4);
-        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    if (VEC || i + 8 <= n) {
+        const f32x4_any *const p = reinterpret_cast<const f32x4_any *>(
+            VEC ? static_cast<const float *>(__builtin_assume_aligned(row + i, 16)) : row + i);
+        const f32x4_any a = p[0], b = p[1];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            v[j] = a[j], v[4 + j] = b[j];
     } else {
 #pragma unroll
         for (int j = 0; j < 8; j++)
@@ -73,9 +82,9 @@ template <bool VEC> __device__ __forceinline__ void load8(const float *row, int6
 }
 template <bool VEC> __device__ __forceinline__ void load8(const uint16_t *row, int64_t i, int64_t n, float v[8])
 {
-    if constexpr (VEC) {
-        const uint4 a = *reinterpret_cast<const uint4 *>(row + i);
-        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+    if (VEC || i + 8 <= n) {
+        const u32x4_any w = *reinterpret_cast<const u32x4_any *>(
+            VEC ? static_cast<const uint16_t *>(__builtin_assume_aligned(row + i, 16)) : row + i);
 #pragma unroll
         for (int j = 0; j < 4; j++) {
             v[2 * j] = __builtin_bit_cast(float, w[j] << 16);
@@ -87,6 +96,22 @@ template <bool VEC> __device__ __forceinline__ void load8(const uint16_t *row, i
             v[j] = i + j < n ? __builtin_bit_cast(float, (uint32_t)row[i + j] << 16) : 0.0f;
     }
 }
+template <bool VEC> __device__ __forceinline__ void store8(uint16_t *row, int64_t i, int64_t n, const float v[8])
+{
+    if (VEC || i + 8 <= n) {
+        u32x4_any h;
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            h[j] = bf16_bits(v[2 * j]) | (uint32_t)bf16_bits(v[2 * j + 1]) << 16;
+        *reinterpret_cast<u32x4_any *>(VEC ? static_cast<uint16_t *>(__builtin_assume_aligned(row + i, 16)) : row + i) = h;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 8; j++)
+            if (i + j < n)
+                row[i + j] = bf16_bits(v[j]);
+    }
+}
+
 // v += the same of `more` further rows, `apart` values from one to the next, in
 // their order.  Four are asked for together (14 splits of 85 rows of 802 values,
 // the gated pair: 19 us one after the other, now 10).
@@ -112,21 +137,6 @@ __device__ __forceinline__ void add8(const float *row, int64_t apart, int more, 
         take(std::integral_constant<int, 2>{});
     if (more & 1)
         take(std::integral_constant<int, 1>{});
-}
-template <bool VEC> __device__ __forceinline__ void store8(uint16_t *row, int64_t i, int64_t n, const float v[8])
-{
-    if constexpr (VEC) {
-        uint32_t h[4];
-#pragma unroll
-        for (int j = 0; j < 4; j++)
-            h[j] = bf16_bits(v[2 * j]) | (uint32_t)bf16_bits(v[2 * j + 1]) << 16;
-        *reinterpret_cast<uint4 *>(row + i) = make_uint4(h[0], h[1], h[2], h[3]);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; j++)
-            if (i + j < n)
-                row[i + j] = bf16_bits(v[j]);
-    }
 }
 
 // largest magnitude of eight values; infinite where one is not finite
