@@ -112,28 +112,34 @@ template <bool VEC> __device__ __forceinline__ void store8(uint16_t *row, int64_
     }
 }
 
-// v += the same of `more` further rows, `apart` values from one to the next, in
-// their order.  Four are asked for together (14 splits of 85 rows of 802 values,
-// the gated pair: 19 us one after the other, now 10).
-template <bool VEC>
-__device__ __forceinline__ void add8(const float *row, int64_t apart, int more, int64_t i, int64_t n, float v[8])
+// v[i] += the same of `more` further rows behind row[i], `apart` values from one
+// to the next, in their order.  Four groups are asked for together (14 splits of
+// 85 rows of 802 values, the gated pair: 19 us one after the other, now 10).
+template <bool VEC, int ROWS>
+__device__ __forceinline__ void add8(const float *const row[ROWS], int64_t apart, int more, int64_t i, int64_t n, float *const v[ROWS])
 {
+    int64_t at = 0;
     auto take = [&](auto count) {
         constexpr int C = decltype(count)::value;
-        float t[C][8];
-#pragma unroll
-        for (int s = 0; s < C; s++)
-            load8<VEC>(row + s * apart, i, n, t[s]);
+        float t[C][ROWS][8];
 #pragma unroll
         for (int s = 0; s < C; s++)
 #pragma unroll
-            for (int j = 0; j < 8; j++)
-                v[j] += t[s][j];
-        row += C * apart;
+            for (int r = 0; r < ROWS; r++)
+                load8<VEC>(row[r] + at + s * apart, i, n, t[s][r]);
+#pragma unroll
+        for (int s = 0; s < C; s++)
+#pragma unroll
+            for (int r = 0; r < ROWS; r++)
+#pragma unroll
+                for (int j = 0; j < 8; j++)
+                    v[r][j] += t[s][r][j];
+        at += C * apart;
     };
-    for (; more >= 4; more -= 4)
-        take(std::integral_constant<int, 4>{});
-    if (more & 2)
+    constexpr int TOGETHER = 4 / ROWS;
+    for (; more >= TOGETHER; more -= TOGETHER)
+        take(std::integral_constant<int, TOGETHER>{});
+    if (TOGETHER > 2 && more & 2)
         take(std::integral_constant<int, 2>{});
     if (more & 1)
         take(std::integral_constant<int, 1>{});
@@ -276,7 +282,9 @@ __global__ __launch_bounds__(256) void join_few_kernel(const float *__restrict__
     if (k >= K)
         return;
     float v[8] = {};
-    add8<true>(part + m * K, M * K, splits, k, K, v);
+    const float *const row[1] = {part + m * K};
+    float *const sums[1] = {v};
+    add8<true, 1>(row, M * K, splits, k, K, sums);
     const int x = e ? -e[m] : 0;
     const float f = w ? w[m] : 1.0f;
 #pragma unroll
@@ -333,19 +341,20 @@ __device__ __forceinline__ void glu_values(const GluRows &a, int64_t m, int64_t 
     const int64_t F = a.F;
     const int x = a.ex ? -a.ex[m] : 0;
     float g[8], u[8], h[8];
+    load8<VEC>(static_cast<const V *>(a.dH) + m * F, 8 * c, F, h);
     const int more = 8 * c < a.from ? 0 : a.splits - 1;
     auto sums = [&](auto whole) {
         constexpr bool V8 = decltype(whole)::value;
         load8<V8>(a.g + m * a.ld, 8 * c, F, g);
         load8<V8>(a.u + m * a.ld, 8 * c, F, u);
-        add8<V8>(a.mg + m * a.more_ld - a.from, a.M * a.more_ld, more, 8 * c, F, g);
-        add8<V8>(a.mu + m * a.more_ld - a.from, a.M * a.more_ld, more, 8 * c, F, u);
+        const float *const row[2] = {a.mg + m * a.more_ld - a.from, a.mu + m * a.more_ld - a.from};
+        float *const both[2] = {g, u};
+        add8<V8, 2>(row, a.M * a.more_ld, more, 8 * c, F, both);
     };
     if (VEC || a.whole)
         sums(std::true_type{});
     else
         sums(std::false_type{});
-    load8<VEC>(static_cast<const V *>(a.dH) + m * F, 8 * c, F, h);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         float p = __builtin_ldexpf(g[j], x), q = __builtin_ldexpf(u[j], x);
@@ -486,7 +495,9 @@ __device__ __forceinline__ float logit(const XentRows &a, int64_t m, int64_t n, 
 template <bool VEC> __device__ __forceinline__ void logits8(const XentRows &a, int64_t m, int64_t c, int x, float z[8])
 {
     load8<VEC>(a.part + m * a.ld, 8 * c, a.N, z);
-    add8<VEC>(a.more + m * a.more_ld - a.from, a.M * a.more_ld, 8 * c < a.from ? 0 : a.splits - 1, 8 * c, a.N, z);
+    const float *const row[1] = {a.more + m * a.more_ld - a.from};
+    float *const sums[1] = {z};
+    add8<VEC, 1>(row, a.M * a.more_ld, 8 * c < a.from ? 0 : a.splits - 1, 8 * c, a.N, sums);
 #pragma unroll
     for (int j = 0; j < 8; j++) {
         z[j] = __builtin_ldexpf(z[j], x);
