@@ -452,7 +452,8 @@ __global__ __launch_bounds__(ROW_THREADS) void glu_rows_kernel(GluRows a)
 // ---------------------------------------------------------------------------
 
 // The largest logit but the given token's (m), the sum of e^(z - m) of these
-// (l); FP8: the largest scale of the rows (s)
+// (l; NaN where one of the logits is, also where none of them is a number and m
+// stays -inf); FP8: the largest scale of the rows (s)
 struct Stat {
     float m, l, s;
 };
@@ -460,7 +461,7 @@ __device__ __forceinline__ Stat join(Stat a, Stat b)
 {
     const float m = fmaxf(a.m, b.m);
     if (m == -INFINITY)
-        return Stat{m, 0.0f, fmaxf(a.s, b.s)};
+        return Stat{m, a.l + b.l, fmaxf(a.s, b.s)};  // of zeros and NaN
     return Stat{m, a.l * expf(a.m - m) + b.l * expf(b.m - m), fmaxf(a.s, b.s)};
 }
 
