@@ -552,7 +552,8 @@ template <bool VEC> __global__ __launch_bounds__(256) void stat_kernel(XentRows 
 }
 
 // Row m: loss and lse, and its gradient with respect to the logits as a row of
-// A (a token that is not scored gives zeros).  p_n - [n = t] is at most
+// A (zeros for a token that is not scored and for one of weight 0, whatever
+// their logits: padding may hold anything).  p_n - [n = t] is at most
 // max(largest p of the others, 1 - p_t) in size, which fixes the power of two;
 // the row's weight enters as a factor of its own afterwards (w_out).
 template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(XentRows a)
@@ -593,6 +594,7 @@ template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(Xent
     const float gt = -lr * rl;
     const int e = row_exponent(big);
     const float weight = given ? (a.weights ? a.weights[m] : 1.0f) : 0.0f;
+    const bool counts = weight != 0.0f;
     if (first && a.A) {
         a.e_out[m] = e;
         a.w_out[m] = weight;
@@ -600,7 +602,7 @@ template <bool VEC> __global__ __launch_bounds__(256) void xent_rows_kernel(Xent
     const int64_t full = (a.N + 7) / 8, c1 = min((a.N + 63) / 64 * 8, ((int64_t)blockIdx.x + 1) * a.run / 8);
     for (int64_t c = blockIdx.x * a.run / 8 + threadIdx.x; c < c1; c += 256) {
         float v[8] = {};
-        if (given && c < full) {
+        if (counts && c < full) {
             logits8<VEC>(a, m, c, x, v);
 #pragma unroll
             for (int j = 0; j < 8; j++) {

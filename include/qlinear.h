@@ -406,7 +406,8 @@ int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, co
  * The gradient's product is held as in qmatmul_grad, with p - [n = t] in place of
  * dY.  Rows go through in chunks of at most 2^26 logits (or 32 rows), which
  * stay in the workspace.  A row of X that is not finite makes its own loss, lse
- * and dX not finite.  workspace: qmatmul_xent_workspace_bytes() (grad: whether
+ * and dX not finite, but for the loss and dX of a token that is not scored and
+ * the dX of one of weight 0, which are zeros all the same.  workspace: qmatmul_xent_workspace_bytes() (grad: whether
  * dX is wanted), 16-byte aligned; the size for M rows also serves fewer, and
  * that with grad the loss alone.  M == 0 launches nothing. */
 size_t qmatmul_xent_workspace_bytes(int fmt, int64_t M, int64_t N, int64_t K, int grad);

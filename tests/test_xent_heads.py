@@ -41,6 +41,40 @@ def test_head_rows_that_are_not_finite_reach_every_token(fmt, M):
                 assert r.dX is None or not torch.isfinite(r.dX).any(), (bad, other)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", (1, 2, 5, 40, 130))
+@pytest.mark.parametrize("N", (300, 5000))
+def test_masked_tokens_that_are_not_finite(fmt, M, N):
+    """Padding whose inputs are NaN or infinite: a token that is not scored has a
+    loss of 0 and a gradient of zeros, one of weight 0 a gradient of zeros, and
+    the others have the bits that they have beside finite padding."""
+    K = 256
+    blocks = ql.isq(fmt, to_dev_bf16(synth.weights_bf16(85100, N, K)))
+    X = to_dev_bf16(synth.activations_bf16(85101 + M, M, K))
+    t = torch.arange(M, dtype=torch.int32, device="cuda") * 7 % N
+    wt = torch.linspace(0.5, 2.0, M, device="cuda")
+    for pad in ([0], [M - 1], list(range(0, M, 3))):
+        keep = [m for m in range(M) if m not in pad]
+        for unscored in (True, False):
+            tt, ww = t.clone(), wt.clone()
+            if unscored:
+                tt[pad] = -100
+            else:
+                ww[pad] = 0.0
+            clean = ql.qmatmul_xent(fmt, blocks, X, N, tt, weights=ww)
+            assert not clean.dX[pad].any()
+            for value in (float("nan"), float("inf")):
+                bad = X.clone()
+                bad[pad, 9] = value
+                r = ql.qmatmul_xent(fmt, blocks, bad, N, tt, weights=ww)
+                assert not r.dX[pad].any() and not torch.isnan(r.dX[pad]).any(), (pad, unscored, value)
+                if unscored:
+                    assert not r.loss[pad].any()
+                for a, b in zip(r, clean):
+                    assert torch.equal(a[keep], b[keep])
+
+
 # ---------------------------------------------------------------------------
 # every digit of the logits
 # ---------------------------------------------------------------------------
