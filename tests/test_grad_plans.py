@@ -8,7 +8,7 @@ import torch
 
 import ggml_block_quant_amd as ql
 import synth
-from grad_util import back, rounded, within
+from grad_util import FMTS, back, rounded, within
 from gpu_util import to_dev_bf16
 from test_parity_grad import act_and_slope, check_glu, check_grad, gradients
 from test_parity_xent import case, check, want
@@ -163,6 +163,50 @@ def test_long_inputs():
     for M in (20, 70):
         X, W, b, t = case("q6k", M, 300, K)
         check("q6k", X, W, b, t, label=f"{M} rows of {K}")
+
+
+# ---------------------------------------------------------------------------
+# addresses that are whole multiples of 16 bytes and of no more
+# ---------------------------------------------------------------------------
+
+def barely(t):
+    """A copy of t at an address of 16 bytes more than a multiple of 256."""
+    n = t.numel() * t.element_size()
+    hold = torch.zeros(n + 512, dtype=torch.uint8, device="cuda")
+    at = (16 - hold.data_ptr()) % 256
+    out = hold[at:at + n].view(t.dtype).view(t.shape)
+    out.copy_(t)
+    assert out.data_ptr() % 256 == 16
+    return out
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("M", (1, 3, 20, 60, 100, 300))
+def test_barely_aligned_buffers(fmt, M):
+    """Every buffer 16 bytes off a multiple of 256: the same bits."""
+    N, K = 333, 512
+    b = ql.isq(fmt, to_dev_bf16(synth.weights_bf16(86400, N, K)))
+    X, d = to_dev_bf16(synth.activations_bf16(86401, M, K)), gradients(3, M, N)
+    t, wt = torch.arange(M, dtype=torch.int32, device="cuda"), torch.linspace(0.5, 2.0, M, device="cuda")
+
+    def space(n):
+        return barely(torch.zeros(n, dtype=torch.uint8, device="cuda"))
+
+    bf, f32 = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda"), torch.zeros(M, device="cuda")
+    fb = torch.zeros((M, N), dtype=torch.bfloat16, device="cuda")
+    b2, X2, t2, w2 = barely(b), barely(X), barely(t), barely(wt)
+    for dY in (d, d.bfloat16()):
+        d2 = barely(dY)
+        got = ql.qmatmul_grad(fmt, b2, d2, K, out=barely(bf), workspace=space(ql.grad_workspace_bytes(fmt, M, N, K)))
+        assert torch.equal(got, ql.qmatmul_grad(fmt, b, dY, K))
+        got = ql.qmatmul_glu_grad(fmt, b2, b2, X2, d2, out=ql.GluGrad(barely(bf), barely(fb), barely(fb)),
+                                  workspace=space(ql.glu_grad_workspace_bytes(fmt, M, N, K)))
+        for u, v in zip(got, ql.qmatmul_glu_grad(fmt, b, b, X, dY, parts=True)):
+            assert torch.equal(u, v)
+    got = ql.qmatmul_xent(fmt, b2, X2, N, t2, weights=w2, out=ql.Xent(barely(f32), barely(f32), barely(bf)),
+                          workspace=space(ql.xent_workspace_bytes(fmt, M, N, K)))
+    for u, v in zip(got, ql.qmatmul_xent(fmt, b, X, N, t, weights=wt)):
+        assert torch.equal(u, v)
 
 
 # ---------------------------------------------------------------------------
