@@ -651,8 +651,10 @@ struct Plan {
     int64_t split_from() const { return splits > 1 ? whole / (Mp / rows) * f.cols : 0; }  // the first column that is split
     int64_t rows;  // of a tile
 };
-// Up to 64 rows a launch is split until it fills the card twice; from 65 on a
-// workgroup has a CU to itself, and splits are chosen by time.
+// Up to 64 rows a launch is split until it fills the card twice; from 65 on
+// splits are chosen by time, with one workgroup a CU.  (Their LDS admits no more
+// but in the pairs' form of 128 rows, of which two would fit: its 97 x 32003 of
+// 2048 run as 252 workgroups of four waves, one wave a SIMD.)
 constexpr int kSplitTo = 512, kTimedSplits = 64, kTimedTo = 1024;
 
 Plan plan_with(int mode, int tile, int64_t M, int64_t cols, int64_t depth, int parts, int64_t n)

@@ -17,7 +17,8 @@
 //   format's weights are whole multiples of 2^-24, fp16's smallest step, so
 //   none is lost for being small; weights above 65504 are not finite here.
 // - The cross entropy's logits take each weight as an fp16 pair, w = hi + lo
-//   within 2^-22: its loss is fp32.
+//   within 2^-22: its loss is fp32.  (FP8's codes are whole in hi: their lo is
+//   zero, and the products with it, half of its logits' work, add nothing.)
 #pragma once
 
 #include "units.h"
@@ -458,10 +459,13 @@ __global__ __launch_bounds__(64 * WM *WN) void product_kernel(ProductArgs a)
 // row of W, eight weights a product, straight into the product's operand: the
 // order of K within a step is free as long as A's is the same, so the lanes
 // 0 .. 31 of a wave take one unit of the row and 32 .. 63 the next, and W never
-// passes through LDS.  Bound by the decode's instructions: of 131072 x 5120 Q6K
-// pairs of 3 rows 237 us (2.3 TB/s) and of 64 rows 285, with W through LDS 267
-// and 399.  Two steps on their way, so that three workgroups fit a CU (two of
-// 64 rows); with four, 40 x 32000 of 4096 Q4K took 63 us against 47.
+// passes through LDS.  131072 x 5120 Q6K pairs of 3 rows take 237 us (2.3 TB/s)
+// and of 64 rows 285, with W through LDS 267 and 399.  Of these 111 and 117 are
+// vector instructions (416 and 440 for two steps, four clocks each); the rest
+// are waits at the barrier of every step and for the memory: Q4K's loop, for
+// one, waits for its second set's header in the first one's step, which nothing
+// in begin() holds back.  Two steps on their way, so that three workgroups fit a
+// CU (two of 64 rows); with four, 40 x 32000 of 4096 Q4K took 63 us against 47.
 template <int MODE, int MI> struct Thin {
     static constexpr int TM = 32 * MI, BK = 128, NT = 256;
     static constexpr int P = MODE == FORE_PAIR ? 2 : 1;
@@ -623,11 +627,15 @@ struct OneArgs {
 // tiles of 32 rows, which also need the gradients as fp16 panels first (3.5
 // us): 14336 x 4096 Q4K 13.4 against 14.6 us, Q8_0 16.1 against 18.1, 131072 x
 // 5120 Q6K 122 against 141; two rows in this way 20 us, so they take the tiles.
-// Bound by the decode's instructions (2.4 to 4.5 TB/s of weights).
+// 2.4 to 4.5 TB/s of weights, bound by waits as much as by the decode: Q4K's 242
+// vector instructions for 64 weights a lane are 5.6 of the 13 us, Q6K's 311 are
+// 83 of the 122.  The sets are no prefetch: load() uses the row's gradient where
+// it asks for it, and the compiler asks for most formats' units at the head of
+// the turn that decodes them.
 template <int FMT, typename V>
 __global__ __launch_bounds__(256) void one_kernel(OneArgs a)
 {
-    constexpr int DEPTH = 2;  // (131072 x 5120 Q6K: 122 us; 3, 4 and 6: 130, 131, 157)
+    constexpr int DEPTH = 2;  // rows a turn (131072 x 5120 Q6K: 122 us; 3, 4 and 6: 130, 131, 157)
     __shared__ float sum[32][256 + 4];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int slot = wave * 8 + (lane >> 3), c = lane & 7;

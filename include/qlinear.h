@@ -353,10 +353,11 @@ int qmatmul_logprobs(int fmt, const void *blocks, const void *X_bf16, int64_t M,
  * fp16 (2^-11 of the weight), sums are fp32, and the result is rounded to bf16:
  * |dX - exact| <= (2^-9.99 + N * 2^-24) * sum_n |dY||w| + 2^-7.99 |dX|
  *                 + 2^-38 * max_n |dY| * sum_n |w|.
- * A weight above 65504 is taken as infinite (FP8: a code times its row's scale
- * may be any size; dY times that scale takes dY's part above).  A row of dY
- * that is not finite makes its row of dX not finite, and no other.  Results do
- * not depend on the order in which workgroups run.
+ * From two rows on a weight above 65504 is taken as infinite (FP8: a code times
+ * its row's scale may be any size; dY times that scale takes dY's part above);
+ * one row takes it as it is.  A row of dY that is not finite makes its row of dX
+ * not finite, and no other.  Results do not depend on the order in which
+ * workgroups run.
  * workspace: device, qmatmul_grad_workspace_bytes() bytes, 16-byte aligned,
  * overwritten (nothing in it needs to start at zero); the size for M rows also
  * serves fewer.  Calls that can overlap in time need one each.  Results,
@@ -380,9 +381,13 @@ int qmatmul_grad(int fmt, const void *blocks, const void *dY, int dy_type, void 
  * G and U are fp32 sums with the weights in fp16 and X as it is (down to 2^-31
  * of its row's largest), so each is within 2^-11 + K * 2^-23 of its magnitudes
  * summed (up to three rows: qmatmul's GEMV, with its accuracy, where that is
- * the faster); dX adds up dG and dU before their rounding to bf16, as fp16
- * times one power of two for both rows (2^-11 of the value, and 2^-39 of the
- * larger of the two rows' largest).  The rest as in qmatmul_grad. */
+ * the faster).  They are not qmatmul_glu's bit for bit, which rounds in other
+ * places (its weights to 2^-17 or not at all): a ReLU gate that is closer to 0
+ * than these bounds can be open there and shut here, or the other way.  dX adds
+ * up dG and dU before their rounding to bf16, as fp16 times one power of two for
+ * both rows (2^-11 of the value, and 2^-39 of the larger of the two rows'
+ * largest).  The rest as in qmatmul_grad; a weight above 65504 makes G and U not
+ * finite where the GEMV does not take them. */
 size_t qmatmul_glu_grad_workspace_bytes(int fmt, int64_t M, int64_t F, int64_t K);
 int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, const void *X_bf16, const void *dH,
                      int dh_type, void *dX_bf16, void *dG_bf16, void *dU_bf16, int64_t M, int64_t F, int64_t K, int act,
@@ -401,8 +406,9 @@ int qmatmul_glu_grad(int fmt, const void *gate_blocks, const void *up_blocks, co
  * alone).  targets, weights, loss and lse 4-byte aligned.
  * The logits take each weight as a pair of fp16 (2^-22 of the weight) and sums
  * in fp32 (up to four rows: qmatmul's GEMV, with its accuracy, where that is
- * the faster); 1 - p of the given token is formed as the others' share, so
- * neither a loss nor a gradient near 0 is a difference of nearly equal numbers.
+ * the faster; elsewhere a weight above 65504 makes its logits not finite); 1 - p
+ * of the given token is formed as the others' share, so neither a loss nor a
+ * gradient near 0 is a difference of nearly equal numbers.
  * The gradient's product is held as in qmatmul_grad, with p - [n = t] in place of
  * dY.  Rows go through in chunks of at most 2^26 logits (or 32 rows), which
  * stay in the workspace.  A row of X that is not finite makes its own loss, lse
