@@ -155,6 +155,21 @@ def test_gated_pair_long_rows(fmt, F, dtype):
         check_glu(fmt, M, F, 256, "silu", dtype, parts=parts, empty=(M - 1,))
 
 
+@pytest.mark.parametrize("M,F", ((1, 300), (3, 300), (3, 16385), (40, 301), (100, 16392)))
+def test_gated_pair_with_one_of_the_parts(M, F):
+    """dG or dU alone: the same bits, nothing else written."""
+    K = 256
+    bg, bu = (ql.isq("q4k", to_dev_bf16(synth.weights_bf16(86500 + i, F, K))) for i in range(2))
+    X, dH = to_dev_bf16(synth.activations_bf16(86502, M, K)), gradients(2, M, F)
+    both = ql.qmatmul_glu_grad("q4k", bg, bu, X, dH, parts=True)
+    for g, u in ((True, False), (False, True)):
+        bf = [torch.zeros((M, n), dtype=torch.bfloat16, device="cuda") for n in (K, F, F)]
+        r = ql.qmatmul_glu_grad("q4k", bg, bu, X, dH, out=ql.GluGrad(bf[0], bf[1] if g else None, bf[2] if u else None))
+        assert torch.equal(r.dX, both.dX)
+        assert torch.equal(bf[1], both.dG if g else torch.zeros_like(bf[1]))
+        assert torch.equal(bf[2], both.dU if u else torch.zeros_like(bf[2]))
+
+
 def test_long_inputs():
     """X's own rows: K beyond what is held, panels of either width."""
     K = 17408

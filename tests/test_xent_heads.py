@@ -43,7 +43,7 @@ def test_head_rows_that_are_not_finite_reach_every_token(fmt, M):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("fmt", FMTS)
-@pytest.mark.parametrize("M", (1, 2, 5, 40, 130))
+@pytest.mark.parametrize("M", (1, 2, 3, 4, 5, 40, 130))
 @pytest.mark.parametrize("N", (300, 5000))
 def test_masked_tokens_that_are_not_finite(fmt, M, N):
     """Padding whose inputs are NaN or infinite: a token that is not scored has a
